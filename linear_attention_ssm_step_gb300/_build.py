@@ -17,8 +17,9 @@ BUILD_DIR = os.path.join(PKG_DIR, "_build")
 LIB_PATH = os.path.join(PKG_DIR, "libkda_gb300.so")
 
 SOURCES = ["kda_api.cu", "kda_step.cu", "kda_ring.cu", "kda_tmap.cu", "kda_verify_tc.cu", "kda_fp8.cu",
-           "kda_prefill.cu", "kda_prefill_tc.cu", "kda_prefill_chain.cu"]
-HEADERS = ["kda_device.cuh", "kda_launch.h", "kda_tc.cuh", "kda_chunk.cuh", "kda_fp8_codec.cuh"]
+           "kda_prefill.cu", "kda_prefill_tc.cu", "kda_prefill_chain.cu", "kda_paged.cu", "kda_paged_api.cu"]
+HEADERS = ["kda_device.cuh", "kda_launch.h", "kda_tc.cuh", "kda_chunk.cuh", "kda_fp8_codec.cuh", "kda_error.h", "kda_paged.cuh",
+           "kda_paged_launch.h"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 # --fmad=false: no implicit mul+add contraction anywhere, so every fused
@@ -36,7 +37,7 @@ def _nvcc():
 
 
 def _inputs():
-    files = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(INCLUDE, h) for h in ("kda.h", "kda_fp8.h", "kda_prefill.h")]
+    files = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(INCLUDE, h) for h in ("kda.h", "kda_fp8.h", "kda_prefill.h", "kda_paged.h")]
     files.append(os.path.abspath(__file__))
     return files
 

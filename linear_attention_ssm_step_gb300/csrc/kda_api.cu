@@ -7,6 +7,7 @@
 #include <stdio.h>
 
 #include "kda.h"
+#include "kda_error.h"
 #include "kda_fp8.h"
 #include "kda_launch.h"
 #include "kda_prefill.h"
@@ -28,6 +29,10 @@ namespace {
 
 thread_local char g_err[512] = "";
 
+}  // namespace
+
+namespace kda {
+
 kda_status fail(kda_status s, const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);
@@ -40,6 +45,13 @@ kda_status ok() {
   g_err[0] = '\0';
   return KDA_OK;
 }
+
+}  // namespace kda
+
+namespace {
+
+using kda::fail;
+using kda::ok;
 
 // Rows of V per CTA, by configuration index. Configuration 4 runs whole heads
 // with the dot products on the tensor cores (T > 1 only).

@@ -1,4 +1,4 @@
-"""Thin ctypes binding of libkda_gb300.so (include/kda.h).
+"""Thin ctypes binding of libkda_gb300.so (include/kda.h, kda_fp8.h, kda_prefill.h, kda_paged.h).
 
 Argument marshalling only: torch tensors supply device pointers, strides and
 the current CUDA stream; every step of the computation runs in the library's
@@ -6,6 +6,7 @@ kernels. There is no CPU or fallback path: if the library is missing or a
 call is rejected, this module raises.
 """
 
+import collections
 import ctypes
 import os
 
@@ -18,6 +19,11 @@ KDA_ERR_HIST_LEN = 1
 KDA_ERR_TIMEOUT = 2
 KDA_ERR_CACHE_BASE = 4
 KDA_ERR_SEQLENS = 8
+KDA_ERR_PAGES = 16
+KDA_ERR_LENGTHS = 32
+KDA_MAX_REQUESTS = 4096
+KDA_ATTENTION_WORKSPACE_ZEROED = 4096
+KDA_ROPE_PLAIN, KDA_ROPE_LINEAR, KDA_ROPE_BASE, KDA_ROPE_PARTS = 0, 1, 2, 3
 KDA_MAX_T = 16
 KDA_GATE_RAW, KDA_GATE_PRECOMPUTED = 0, 1
 STATUS_NAMES = {0: "KDA_OK", 1: "KDA_EINVAL", 2: "KDA_EUNSUPPORTED", 3: "KDA_ELAUNCH"}
@@ -73,6 +79,61 @@ class KdaSeqs(ctypes.Structure):
     _fields_ = [("cu_seqlens", ctypes.c_void_p), ("num_seqs", ctypes.c_int32)]
 
 
+class KdaPages(ctypes.Structure):
+    """kda_pages of include/kda_paged.h."""
+
+    _fields_ = [("ptr", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class KdaPagedCache(ctypes.Structure):
+    """kda_paged_cache of include/kda_paged.h."""
+
+    _fields_ = [("k", KdaPages), ("v", KdaPages), ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("num_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class KdaPlanParams(ctypes.Structure):
+    """kda_plan_params of include/kda_paged.h."""
+
+    _fields_ = [
+        ("num_requests", ctypes.c_int32), ("num_tokens", ctypes.c_int32),
+        ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+        ("cached", ctypes.c_void_p), ("new_len", ctypes.c_void_p),
+        ("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("table_width", ctypes.c_int32),
+        ("free_pages", ctypes.c_void_p), ("free_capacity", ctypes.c_int32),
+        ("free_count", ctypes.c_void_p), ("free_count_out", ctypes.c_void_p),
+        ("cu_new", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+        ("positions", ctypes.c_void_p), ("slots", ctypes.c_void_p), ("error_word", ctypes.c_void_p),
+    ]
+
+
+class KdaRopeParams(ctypes.Structure):
+    """kda_rope_params of include/kda_paged.h."""
+
+    _fields_ = [
+        ("num_tokens", ctypes.c_int32), ("num_q_heads", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32), ("mscale", ctypes.c_float),
+        ("q", KdaView), ("k", KdaView), ("v", KdaView),
+        ("q_out", ctypes.c_void_p), ("q_out_b_stride", ctypes.c_int64), ("q_out_h_stride", ctypes.c_int64),
+        ("positions", ctypes.c_void_p), ("slots", ctypes.c_void_p), ("freqs", ctypes.c_void_p),
+        ("cache", KdaPagedCache), ("error_word", ctypes.c_void_p),
+    ]
+
+
+class KdaAttentionParams(ctypes.Structure):
+    """kda_attention_params of include/kda_paged.h."""
+
+    _fields_ = [
+        ("num_requests", ctypes.c_int32), ("num_tokens", ctypes.c_int32), ("num_q_heads", ctypes.c_int32),
+        ("window", ctypes.c_int32), ("scale", ctypes.c_float), ("q", KdaView),
+        ("out", ctypes.c_void_p), ("out_b_stride", ctypes.c_int64), ("out_h_stride", ctypes.c_int64),
+        ("lse", ctypes.c_void_p), ("cu_new", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+        ("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("table_width", ctypes.c_int32),
+        ("cache", KdaPagedCache), ("error_word", ctypes.c_void_p),
+    ]
+
+
 EXPORTS = {
     "kda_decode": ([ctypes.POINTER(KdaParams), ctypes.c_void_p], ctypes.c_int),
     "kda_decode_fp8": ([ctypes.POINTER(KdaParams), ctypes.POINTER(KdaFp8Pool), ctypes.c_void_p], ctypes.c_int),
@@ -95,6 +156,13 @@ EXPORTS = {
     "kda_select_config": ([ctypes.c_int32, ctypes.c_int32], ctypes.c_int32),
     "kda_select_ring_config": ([ctypes.c_int32, ctypes.c_int32], ctypes.c_int32),
     "kda_last_error": ([], ctypes.c_char_p),
+    "kda_paged_plan": ([ctypes.POINTER(KdaPlanParams), ctypes.c_void_p], ctypes.c_int),
+    "kda_rope_append": ([ctypes.POINTER(KdaRopeParams), ctypes.c_void_p], ctypes.c_int),
+    "kda_rope_freqs": ([ctypes.c_void_p, ctypes.c_int32, ctypes.c_double, ctypes.c_int32, ctypes.c_double,
+                        ctypes.c_double, ctypes.c_double, ctypes.c_double], ctypes.c_int),
+    "kda_paged_attention": ([ctypes.POINTER(KdaAttentionParams), ctypes.c_void_p, ctypes.c_size_t,
+                             ctypes.c_void_p], ctypes.c_int),
+    "kda_paged_attention_workspace_bytes": ([ctypes.c_int32], ctypes.c_size_t),
 }
 
 _lib = None
@@ -508,3 +576,200 @@ def kda_config_tile_v(config):
 
 def kda_last_error():
     return load_library().kda_last_error().decode()
+
+
+def _ints(t, name, shape):
+    _need(t, name, torch.int32)
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {list(shape)} tensor, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _error_word(error_word):
+    if error_word is None:
+        return None
+    _need(error_word, "error_word", torch.int32)
+    return error_word.data_ptr()
+
+
+def _table(block_table, num_requests):
+    _need(block_table, "block_table", torch.int32)
+    if block_table.dim() != 2 or block_table.shape[0] != num_requests or (
+            num_requests > 0 and block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError(f"block_table must be [{num_requests}, pages] with contiguous rows, "
+                         f"got {tuple(block_table.shape)}")
+    return block_table.data_ptr(), block_table.stride(0), block_table.shape[1]
+
+
+def _paged_cache(k_cache, v_cache, num_heads=None, head_dim=None):
+    """KdaPagedCache of k_cache and v_cache, views [pages, page_size, heads, head_dim] with any strides."""
+    c = KdaPagedCache()
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _need(t, name, torch.bfloat16)
+        if t.dim() != 4 or (t.shape[3] > 1 and t.stride(3) != 1):
+            raise ValueError(f"{name} must be [pages, page_size, heads, head_dim] with a contiguous last dim")
+        if t.shape != k_cache.shape:
+            raise ValueError(f"v_cache has shape {tuple(t.shape)}, k_cache {tuple(k_cache.shape)}")
+        if (num_heads is not None and t.shape[2] != num_heads) or (head_dim is not None and t.shape[3] != head_dim):
+            raise ValueError(f"{name} must have heads of {head_dim}, got {tuple(t.shape)}")
+    c.k = KdaPages(k_cache.data_ptr(), *k_cache.stride()[:3])
+    c.v = KdaPages(v_cache.data_ptr(), *v_cache.stride()[:3])
+    c.num_pages, c.page_size, c.num_heads, c.head_dim = k_cache.shape
+    return c
+
+
+def _rows(t, name, num_tokens=None, num_heads=None, head_dim=None):
+    _need(t, name, torch.bfloat16)
+    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError(f"{name} must be [tokens, heads, head_dim] with a contiguous last dim")
+    for got, want in zip(t.shape, (num_tokens, num_heads, head_dim)):
+        if want is not None and got != want:
+            raise ValueError(f"{name} must be [{num_tokens}, {num_heads or 'heads'}, {head_dim}], got {tuple(t.shape)}")
+    return KdaView(t.data_ptr(), t.stride(0), 0, t.stride(1))
+
+
+PagedPlan = collections.namedtuple("PagedPlan", "cu_new kv_len positions slots free_count")
+
+
+def prepare_paged_plan(cached, new_len, block_table, free_pages, free_count, page_size, num_pages, num_tokens,
+                       out=None, error_word=None, stream=None):
+    """kda_paged_plan bound to these tensors (see PreparedCall); same arguments. out is its PagedPlan."""
+    _need(cached, "cached", torch.int32)
+    R = cached.shape[0] if cached.dim() == 1 else -1
+    p = KdaPlanParams()
+    p.num_requests, p.num_tokens, p.page_size, p.num_pages = R, num_tokens, page_size, num_pages
+    p.cached, p.new_len = _ints(cached, "cached", (R,)), _ints(new_len, "new_len", (R,))
+    p.table, p.table_stride, p.table_width = _table(block_table, R)
+    _need(free_pages, "free_pages", torch.int32)
+    p.free_pages, p.free_capacity = _ints(free_pages, "free_pages", (free_pages.numel(),)), free_pages.numel()
+    p.free_count = _ints(free_count, "free_count", (1,))
+    if out is None:
+        new = lambda n: torch.empty(n, dtype=torch.int32, device=cached.device)  # noqa: E731
+        out = PagedPlan(new(R + 1), new(R), new(num_tokens), new(num_tokens), new(1))
+    p.cu_new, p.kv_len = _ints(out.cu_new, "out.cu_new", (R + 1,)), _ints(out.kv_len, "out.kv_len", (R,))
+    p.positions = _ints(out.positions, "out.positions", (num_tokens,))
+    p.slots = _ints(out.slots, "out.slots", (num_tokens,))
+    p.free_count_out = _ints(out.free_count, "out.free_count", (1,))
+    p.error_word = _error_word(error_word)
+    keep = (p, cached, new_len, block_table, free_pages, free_count, error_word)
+    return PreparedCall(load_library().kda_paged_plan, (ctypes.byref(p), _stream_handle(stream, cached.device)), out,
+                        keep)
+
+
+def kda_paged_plan(cached, new_len, block_table, free_pages, free_count, page_size, num_pages, num_tokens,
+                   out=None, error_word=None, stream=None):
+    """The page plan of a step (include/kda_paged.h). cached, new_len: int32 [R],
+    tokens each request has in the cache and brings; block_table: int32 [R, W],
+    updated in place; free_pages: int32 list of free pages, of which the first
+    free_count[0] are free (taken from the end); num_tokens: rows of positions
+    and slots (at least the sum of new_len; rows beyond it get -1). Returns
+    PagedPlan(cu_new [R + 1], kv_len [R], positions, slots [num_tokens],
+    free_count [1]), all int32; pass the returned free_count to the next call."""
+    return prepare_paged_plan(cached, new_len, block_table, free_pages, free_count, page_size, num_pages, num_tokens,
+                              out, error_word, stream)()
+
+
+def rope_freqs(rotary_dim, base=10000.0, scaling=KDA_ROPE_PLAIN, factor=1.0, original_len=0.0, low=1.0, high=32.0,
+               device="cuda"):
+    """kda_rope_freqs as an int64 device tensor [rotary_dim / 2] for kda_rope_append
+    (the bits of the library's uint64 turns per position)."""
+    host = torch.empty(max(1, rotary_dim // 2), dtype=torch.int64)
+    _check(load_library().kda_rope_freqs(host.data_ptr(), rotary_dim, base, scaling, factor, original_len, low, high))
+    return host.to(device)
+
+
+def prepare_rope_append(q, k, v, positions, slots, freqs, k_cache, v_cache, q_out=None, interleaved=False, mscale=1.0,
+                        error_word=None, stream=None):
+    """kda_rope_append bound to these tensors (see PreparedCall); same arguments. out is q_out."""
+    p = KdaRopeParams()
+    p.q = _rows(q, "q")
+    T, Hq, D = q.shape
+    p.cache = _paged_cache(k_cache, v_cache, head_dim=D)
+    Hkv = p.cache.num_heads
+    p.num_tokens, p.num_q_heads = T, Hq
+    p.k, p.v = _rows(k, "k", T, Hkv, D), _rows(v, "v", T, Hkv, D)
+    if q_out is None:
+        q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+    o = _rows(q_out, "q_out", T, Hq, D)
+    p.q_out, p.q_out_b_stride, p.q_out_h_stride = o.ptr, o.b_stride, o.h_stride
+    p.positions, p.slots = _ints(positions, "positions", (T,)), _ints(slots, "slots", (T,))
+    _need(freqs, "freqs", torch.int64)
+    if freqs.dim() != 1 or not freqs.is_contiguous():
+        raise ValueError("freqs must be a contiguous [rotary_dim / 2] tensor")
+    p.freqs, p.rotary_dim = freqs.data_ptr(), 2 * freqs.shape[0]
+    p.interleaved, p.mscale = int(bool(interleaved)), mscale
+    p.error_word = _error_word(error_word)
+    keep = (p, q, k, v, positions, slots, freqs, k_cache, v_cache, error_word)
+    return PreparedCall(load_library().kda_rope_append, (ctypes.byref(p), _stream_handle(stream, q.device)), q_out,
+                        keep)
+
+
+def kda_rope_append(q, k, v, positions, slots, freqs, k_cache, v_cache, q_out=None, interleaved=False, mscale=1.0,
+                    error_word=None, stream=None):
+    """Rotary positions and the append to the cache (include/kda_paged.h). q: bf16
+    [T, Hq, D]; k, v: bf16 [T, Hkv, D] (any row and head strides); positions,
+    slots: int32 [T] (kda_paged_plan's); freqs: int64 [rotary_dim / 2]
+    (rope_freqs); k_cache, v_cache: bf16 [pages, page_size, Hkv, D] views with
+    any strides, written at the slots. Returns q_out bf16 [T, Hq, D] (q itself
+    turns in place)."""
+    return prepare_rope_append(q, k, v, positions, slots, freqs, k_cache, v_cache, q_out, interleaved, mscale,
+                               error_word, stream)()
+
+
+def paged_attention_workspace_bytes(head_dim):
+    """Bytes of the workspace kda_paged_attention needs (include/kda_paged.h)."""
+    return int(load_library().kda_paged_attention_workspace_bytes(head_dim))
+
+
+def paged_attention_workspace(head_dim, device):
+    """A device workspace for kda_paged_attention calls on one stream, zeroed as its first use needs."""
+    device = torch.device(device)
+    with torch.cuda.device(device):
+        return torch.zeros(max(16, paged_attention_workspace_bytes(head_dim)), dtype=torch.uint8, device=device)
+
+
+def prepare_paged_attention(q, k_cache, v_cache, block_table, cu_new, kv_len, out=None, lse=None, scale=None,
+                            window=0, workspace=None, error_word=None, stream=None):
+    """kda_paged_attention bound to these tensors (see PreparedCall); same arguments."""
+    p = KdaAttentionParams()
+    p.q = _rows(q, "q")
+    T, Hq, D = q.shape
+    p.cache = _paged_cache(k_cache, v_cache, head_dim=D)
+    _need(kv_len, "kv_len", torch.int32)
+    R = kv_len.numel()
+    p.num_requests, p.num_tokens, p.num_q_heads, p.window = R, T, Hq, window
+    p.scale = D ** -0.5 if scale is None else scale
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+    o = _rows(out, "out", T, Hq, D)
+    p.out, p.out_b_stride, p.out_h_stride = o.ptr, o.b_stride, o.h_stride
+    if lse is not None:
+        _need(lse, "lse", torch.float32)
+        if lse.shape != (T, Hq) or not lse.is_contiguous():
+            raise ValueError(f"lse must be a contiguous [{T}, {Hq}] tensor, got {tuple(lse.shape)}")
+        p.lse = lse.data_ptr()
+    p.cu_new, p.kv_len = _ints(cu_new, "cu_new", (R + 1,)), _ints(kv_len, "kv_len", (R,))
+    p.table, p.table_stride, p.table_width = _table(block_table, R)
+    p.error_word = _error_word(error_word)
+    if workspace is None:
+        workspace = paged_attention_workspace(D, q.device)
+    _need(workspace, "workspace", torch.uint8)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous byte tensor")
+    keep = (p, q, k_cache, v_cache, block_table, cu_new, kv_len, lse, workspace, error_word)
+    args = (ctypes.byref(p), workspace.data_ptr(), workspace.numel(), _stream_handle(stream, q.device))
+    return PreparedCall(load_library().kda_paged_attention, args, out, keep)
+
+
+def kda_paged_attention(q, k_cache, v_cache, block_table, cu_new, kv_len, out=None, lse=None, scale=None, window=0,
+                        workspace=None, error_word=None, stream=None):
+    """Attention of each request's new tokens over the paged cache
+    (include/kda_paged.h). q: bf16 [T, Hq, D], request r owning rows cu_new[r]
+    .. cu_new[r+1]-1; k_cache, v_cache: bf16 [pages, page_size, Hkv, D] views
+    with any strides, holding the new tokens' keys and values too; block_table:
+    int32 [R, W]; kv_len: int32 [R]; lse: optional fp32 [T, Hq], written;
+    scale: D ** -0.5 when None; window: keys a row sees at most (0: all);
+    workspace: a paged_attention_workspace kept between calls (allocated when
+    None). Returns out bf16 [T, Hq, D]."""
+    return prepare_paged_attention(q, k_cache, v_cache, block_table, cu_new, kv_len, out, lse, scale, window,
+                                   workspace, error_word, stream)()

@@ -48,3 +48,10 @@ from .kda_prefill_oracle import (  # noqa: F401,E402
     kda_prefill,
     PREFILL_ERR_SEQLENS,
 )
+from .kda_paged_oracle import (  # noqa: F401,E402
+    paged_plan,
+    rope_rotate,
+    rope_append,
+    rope_frequencies,
+    paged_attention,
+)
