@@ -101,6 +101,16 @@ bool wide_rows(const void* p, int64_t b_stride, int64_t h_stride) {
   return aligned(p, 16) && b_stride % 8 == 0 && h_stride % 8 == 0;
 }
 
+// CTAs of the tensor-core attention: one an SM, each with a counter in the workspace's zeroed part. 0 without a device.
+int attention_ctas() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 0;
+  const int most = KDA_ATTENTION_WORKSPACE_ZEROED / (int)sizeof(unsigned);
+  return sms < most ? sms : most;
+}
+
 bool wide_pages(const kda_pages& g) {
   return aligned(g.ptr, 16) && g.page_stride % 8 == 0 && g.token_stride % 8 == 0 && g.head_stride % 8 == 0;
 }
@@ -239,7 +249,9 @@ kda_status kda_rope_freqs(uint64_t* freqs, int32_t rotary_dim, double base, int3
 
 size_t kda_paged_attention_workspace_bytes(int32_t head_dim) {
   if (head_dim < 1 || head_dim > 256) return 0;
-  return KDA_ATTENTION_WORKSPACE_ZEROED;
+  const int ctas = attention_ctas();
+  if (ctas == 0) return 0;
+  return KDA_ATTENTION_WORKSPACE_ZEROED + kda::paged_attention_parts_bytes(head_dim, ctas);
 }
 
 kda_status kda_paged_attention(const kda_attention_params* p, void* workspace, size_t workspace_bytes, void* stream) {
@@ -266,15 +278,9 @@ kda_status kda_paged_attention(const kda_attention_params* p, void* workspace, s
   if ((s = check_words("kv_len", p->kv_len, true)) != KDA_OK) return s;
   if ((s = check_words("lse", p->lse, false)) != KDA_OK) return s;
   if ((s = check_words("error_word", p->error_word, false)) != KDA_OK) return s;
-  const size_t need = kda_paged_attention_workspace_bytes(D);
-  if (need == 0) return fail(KDA_ELAUNCH, "kda_paged_attention: no current device");
-  if (workspace == nullptr || !aligned(workspace, 16)) return fail(KDA_EINVAL, "workspace is NULL or not 16-byte aligned");
-  if (workspace_bytes < need)
-    return fail(KDA_EINVAL, "workspace_bytes = %zu is below the %zu this call needs (kda_paged_attention_workspace_bytes)",
-                workspace_bytes, need);
   const size_t rows = (size_t)p->num_tokens * p->num_q_heads, R = (size_t)p->num_requests;
   const Extent o = rows_extent(p->out, p->num_tokens, p->out_b_stride, p->num_q_heads, p->out_h_stride, D);
-  const Extent l = bytes_extent(p->lse, p->lse ? rows * 4 : 0), w = bytes_extent(workspace, need);
+  const Extent l = bytes_extent(p->lse, p->lse ? rows * 4 : 0);
   const struct {
     const char* name;
     Extent e;
@@ -287,10 +293,22 @@ kda_status kda_paged_attention(const kda_attention_params* p, void* workspace, s
   for (const auto& in : inputs) {
     if (overlaps(o, in.e)) return fail(KDA_EINVAL, "out overlaps %s", in.name);
     if (overlaps(l, in.e)) return fail(KDA_EINVAL, "lse overlaps %s", in.name);
-    if (overlaps(w, in.e)) return fail(KDA_EINVAL, "workspace overlaps %s", in.name);
   }
-  if (overlaps(o, l) || overlaps(o, w) || overlaps(l, w)) return fail(KDA_EINVAL, "out, lse and workspace overlap");
-  const cudaError_t e = kda::launch_paged_attention_simt(*p, static_cast<cudaStream_t>(stream));
+  if (overlaps(o, l)) return fail(KDA_EINVAL, "out overlaps lse");
+  const size_t need = kda_paged_attention_workspace_bytes(D);
+  if (need == 0) return fail(KDA_ELAUNCH, "kda_paged_attention: no current device");
+  if (workspace == nullptr || !aligned(workspace, 16)) return fail(KDA_EINVAL, "workspace is NULL or not 16-byte aligned");
+  if (workspace_bytes < need)
+    return fail(KDA_EINVAL, "workspace_bytes = %zu is below the %zu this call needs (kda_paged_attention_workspace_bytes)",
+                workspace_bytes, need);
+  const Extent w = bytes_extent(workspace, need);
+  for (const auto& in : inputs)
+    if (overlaps(w, in.e)) return fail(KDA_EINVAL, "workspace overlaps %s", in.name);
+  if (overlaps(w, o) || overlaps(w, l)) return fail(KDA_EINVAL, "workspace overlaps out or lse");
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaErrorNotSupported;
+  if (kda::paged_attention_on_tensor_cores(p->cache)) e = kda::launch_paged_attention_tc(*p, workspace, attention_ctas(), st);
+  if (e == cudaErrorNotSupported) e = kda::launch_paged_attention_simt(*p, st);
   if (e != cudaSuccess) return fail(KDA_ELAUNCH, "kda_paged_attention launch: %s", cudaGetErrorString(e));
   return ok();
 }

@@ -14,4 +14,17 @@ cudaError_t launch_rope_append(const kda_rope_params& p, bool wide, cudaStream_t
 // One warp per (row, query head) on the CUDA cores: any cache.
 cudaError_t launch_paged_attention_simt(const kda_attention_params& p, cudaStream_t s);
 
+// One side of a paged cache as a tensor map for copies of 64 columns of `box` tokens (kda_tmap.cu).
+cudaError_t pages_tensor_map(const kda_pages& g, const kda_paged_cache& c, int box, CUtensorMap* out);
+
+// Whether the tensor-core kernel takes this cache (head_dim, page size, alignment).
+bool paged_attention_on_tensor_cores(const kda_paged_cache& c);
+
+// Workspace bytes of that kernel for parts of items, on `ctas` CTAs, after the zeroed counters.
+size_t paged_attention_parts_bytes(int head_dim, int ctas);
+
+// Attention on the tensor cores, persistent on `ctas` CTAs (one an SM); cudaErrorNotSupported, with nothing launched,
+// when the cache's strides have no tensor map.
+cudaError_t launch_paged_attention_tc(const kda_attention_params& p, void* workspace, int ctas, cudaStream_t s);
+
 }  // namespace kda

@@ -1,0 +1,879 @@
+// kda_paged_tc.cu - paged attention on the fifth-generation tensor cores
+// (include/kda_paged.h), head_dim 64 or 128.
+//
+// Mathematics. For one key-value head and the rows that read it, over units of
+// 128 keys: S = Q K^T, P = exp2(c (S - m)) with c = scale log2 e and m a running
+// reference of the row's maximum, l += sum P, O += P V; out = O / l, lse = m
+// scale + ln l. m follows the maximum only when that has grown by more than 8
+// in log2 units (then O and l are scaled down once): P stays below 2^8, which
+// changes no relative precision, and most units need no pass over O.
+//
+// Rows. The query heads of one key-value head and consecutive new tokens of one
+// request are the rows of a tile of 128 (token-major), so that a key is read
+// once for all of them: floor(128 / g) tokens of g heads. An item is one key-
+// value head and two such tiles; its units run over the keys any of its rows
+// sees.
+//
+// Split. The items of all requests form one line of units, which the persistent
+// CTAs (one an SM) share out evenly, at any unit: lengths may be as ragged as
+// they like and few rows over a long cache still fill the GPU. Every CTA finds
+// its share itself from the requests' lengths. An item cut between CTAs leaves
+// unnormalised O, m and l of each part in the workspace, and the CTA that
+// finishes last joins them in the order of the parts: the same bits whichever
+// comes last.
+//
+// A CTA is twelve warps: two softmax groups of four (a thread per row), a warp
+// each that loads keys and values (one tensor-map copy per page and 64
+// columns), that issues the products, and that walks the line. With two row
+// tiles, group t owns tile t; a single tile (decode, verify) takes the units in
+// turn with the groups, each with its own O, joined at the end, so that in
+// either case one group's exponentials run while the other's products do.
+// S and P share tensor-memory columns: P (bf16) overwrites the S it came from
+// and enters the second product from there.
+#include <math.h>
+
+#include "kda_paged.cuh"
+#include "kda_paged_launch.h"
+#include "kda_tc.cuh"
+
+namespace kda {
+
+namespace {
+
+constexpr int UNIT = 128;   // keys a unit
+constexpr int TILE = 128;   // rows a tile
+constexpr int THREADS = 384;
+constexpr int SOFTMAX_THREADS = 256;
+constexpr int K_WARP = 8, V_WARP = 9, MMA_WARP = 10, WALK_WARP = 11;
+constexpr int RING = 4;  // segments the walking warp may be ahead
+// Registers a thread after the split: 256 x 208 + 128 x 88 = 384 x 168, what the block launches with.
+constexpr int SOFTMAX_REGS = 208, OTHER_REGS = 88;
+
+template <int D>
+struct Shape {
+  static constexpr int K_STAGES = D == 128 ? 3 : 4;
+  static constexpr int V_STAGES = D == 128 ? 2 : 4;
+  static constexpr uint32_t TILE_BYTES = TILE * D * 2;  // also a unit of keys or values
+  static constexpr uint32_t Q0 = 0, Q1 = TILE_BYTES;
+  static constexpr uint32_t K0 = 2 * TILE_BYTES;
+  static constexpr uint32_t V0 = K0 + K_STAGES * TILE_BYTES;
+  static constexpr uint32_t END = V0 + V_STAGES * TILE_BYTES;
+};
+
+// A run of units of one item, for one CTA.
+struct Segment {
+  int row0, ntok;        // first row of q, new tokens of the item
+  int head;              // key-value head
+  int pos0;              // position of the first token
+  int request;
+  int lo, hi;            // keys any of its rows sees: [lo, hi)
+  int u0, u1;            // units of this run
+  int dual;              // two row tiles
+  int part, parts, cta0; // this run's place among the item's parts, held by the CTAs from cta0 on
+};
+
+struct Shared {
+  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
+  uint64_t v_tail, q_full[2], s_full[2], p_full[2], o_done[2], seg_full[RING], seg_empty[RING], drain;
+  Segment seg[RING];
+  float m1[TILE], l1[TILE];  // the second group's m and l when both groups share a tile
+  long long warp_sum[THREADS / 32];
+  long long start_prefix;
+  uint32_t tmem;
+  int start_request;
+  int last_part;
+};
+
+// The keys [lo, hi) that item i (tokens i w .. of n, the first at position pos) sees, and its units.
+struct Span {
+  int lo, hi, u0, u1;
+};
+
+__device__ __forceinline__ Span item_span(int pos, int n, int i, int w, int window) {
+  Span s;
+  s.hi = max(0, pos + min(n, (i + 1) * w));
+  s.lo = window > 0 ? max(0, pos + i * w - window + 1) : 0;
+  if (s.hi == 0) s.lo = 0;
+  s.u0 = s.lo / UNIT;
+  s.u1 = max(s.u0 + 1, (s.hi + UNIT - 1) / UNIT);  // rows that see no key still need their zeros
+  return s;
+}
+
+// Units of one key-value head of a request: n tokens, w an item. Called by whole warps, one request a lane; a request
+// of many items (a long chunk) is summed by the warp together.
+__device__ __forceinline__ long long head_units(int pos, int n, int w, int window) {
+  const int items = (n + w - 1) / w;
+  long long units = 0;
+  if (items <= 4)
+    for (int i = 0; i < items; ++i) {
+      const Span s = item_span(pos, n, i, w, window);
+      units += s.u1 - s.u0;
+    }
+  unsigned many = __ballot_sync(0xffffffffu, items > 4);
+  const int lane = threadIdx.x & 31;
+  while (many) {
+    const int src = __ffs(many) - 1;
+    many &= many - 1;
+    const int pn = __shfl_sync(0xffffffffu, pos, src), nn = __shfl_sync(0xffffffffu, n, src);
+    const int ni = (nn + w - 1) / w;
+    long long part = 0;
+    for (int i = lane; i < ni; i += 32) {
+      const Span s = item_span(pn, nn, i, w, window);
+      part += s.u1 - s.u0;
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+    if (lane == src) units = part;
+  }
+  return units;
+}
+
+// ---------------------------------------------------------------- tensor memory in 32-column blocks
+
+// 32 columns, without the wait.
+__device__ __forceinline__ void ld32(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+
+// Names 32 registers a load fills, so that no use of them moves above the wait before it.
+__device__ __forceinline__ void hold32(uint32_t* r) {
+  asm volatile(""
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                 "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                 "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                 "+r"(r[29])
+               :
+               : "memory");
+  asm volatile("" : "+r"(r[30]), "+r"(r[31]) : : "memory");
+}
+
+__device__ __forceinline__ void ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void st32(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+      "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+      "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+// A wait of a whole warp; false for every lane if it gave up for any.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity));
+}
+
+// A barrier of `count` threads that tells all of them whether `x` held for any.
+__device__ __forceinline__ bool bar_any(uint32_t id, uint32_t count, bool x) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"((uint32_t)x), "r"(id), "r"(count)
+      : "memory");
+  return any != 0;
+}
+
+// The value operand: 64-column regions of TILE rows (keys) x 128 bytes, N (the columns) contiguous. Leading byte
+// offset: the next 64 columns, TILE * 128 bytes on; stride byte offset: the next 8 keys, 1024 bytes on. A K step of
+// 16 keys adds 2048 bytes to the start address.
+__device__ __forceinline__ uint64_t value_desc(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)((TILE * 128u) >> 4) << 16) | ((uint64_t)(1024u >> 4) << 32) |
+         ((uint64_t)1u << 46) | ((uint64_t)2u << 61);
+}
+constexpr uint32_t B_MN_MAJOR = 1u << 16;  // instruction descriptor: B with N contiguous
+
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float SLACK = 8.f;  // growth of the maximum (log2) that the reference may lag behind
+
+struct AttnArgs {
+  kda_attention_params p;
+  float* parts;        // workspace: 2 slots a CTA of TILE x 2 rows of D sums, then m and l of each row
+  unsigned* counters;  // one a CTA, zero between calls
+  int q_wide, out_wide;
+  int box;             // keys a copy brings: min(page_size, UNIT)
+};
+
+template <int D>
+__device__ __forceinline__ float* part_slot(const AttnArgs& a, int slot) {
+  return a.parts + (size_t)slot * (2 * TILE) * (D + 2);
+}
+
+}  // namespace
+
+template <int D>
+__global__ void __launch_bounds__(THREADS, 1)
+    kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                                  const __grid_constant__ AttnArgs a) {
+  using S = Shape<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Shared& sh = *reinterpret_cast<Shared*>(smem + S::END);
+  const kda_attention_params& p = a.p;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = p.num_q_heads / p.cache.num_heads, Hkv = p.cache.num_heads;
+  const int tpt = TILE / g, w = 2 * tpt;  // tokens a tile, an item
+  const int window = p.window;
+
+  if (tid == 0) {
+    for (int i = 0; i < S::K_STAGES; ++i) {
+      mbar_init(&sh.k_full[i], 1);
+      mbar_init(&sh.k_empty[i], 1);
+    }
+    for (int i = 0; i < S::V_STAGES; ++i) {
+      mbar_init(&sh.v_full[i], 1);
+      mbar_init(&sh.v_empty[i], 1);
+    }
+    mbar_init(&sh.v_tail, 1);
+    mbar_init(&sh.drain, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.q_full[i], TILE);
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_full[i], TILE);
+      mbar_init(&sh.o_done[i], 1);
+    }
+    for (int i = 0; i < RING; ++i) {
+      mbar_init(&sh.seg_full[i], 1);
+      mbar_init(&sh.seg_empty[i], 5);  // key, value and product warps, both softmax groups
+    }
+    sh.start_request = -1;
+  }
+
+  // ---- this CTA's share of the line of units
+  long long total = 0;
+  unsigned bad = 0;
+  long long mine = 0, before = 0;  // the units of this thread's request in the latest block, and those before it
+  const int R = p.num_requests;
+  const bool one_block = R <= THREADS;
+  auto block_units = [&](int base) {
+    const int r = base + tid;
+    int n = 0, pos = 0;
+    if (r < R) {
+      const AttnRequest q = attn_request(p, r);
+      bad |= q.bad;
+      n = q.n;
+      pos = q.kv - q.n;
+    }
+    mine = head_units(pos, n, w, window) * Hkv;
+    long long scan = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, scan, o);
+      if (lane >= o) scan += x;
+    }
+    __syncthreads();
+    if (lane == 31) sh.warp_sum[warp] = scan;
+    __syncthreads();
+    before = scan - mine;
+    long long all = 0;
+#pragma unroll
+    for (int i = 0; i < THREADS / 32; ++i) {
+      if (i < warp) before += sh.warp_sum[i];
+      all += sh.warp_sum[i];
+    }
+    return all;
+  };
+  for (int base = 0; base < R; base += THREADS) total += block_units(base);
+  if (blockIdx.x == 0 && bad && p.error_word) atomicOr(p.error_word, bad);
+  const long long ctas = total < (long long)gridDim.x ? total : (long long)gridDim.x;
+  const long long cta = blockIdx.x;
+  if (cta >= ctas) return;  // the whole CTA: nothing allocated yet
+  const long long begin = total * cta / ctas, end = total * (cta + 1) / ctas;
+  {
+    long long prefix = 0;
+    for (int base = 0; base < R; base += THREADS) {
+      const long long all = one_block ? total : block_units(base);
+      if (begin >= prefix + before && begin < prefix + before + mine) {
+        sh.start_request = base + tid;
+        sh.start_prefix = prefix + before;
+      }
+      prefix += all;
+    }
+  }
+  if (warp == MMA_WARP) tmem_alloc(&sh.tmem, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  const uint32_t S_COL = tmem, O_COL = tmem + 2 * TILE;
+
+  if (warp >= SOFTMAX_THREADS / 32) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
+    bool alive = true;
+
+    if (warp == WALK_WARP) {
+      // ---- the line of units, cut into segments
+      int r = sh.start_request;
+      long long at = begin;
+      long long prefix = sh.start_prefix;  // first unit of the current head's first item
+      uint32_t out = 0;
+      int head = 0, item = 0;
+      bool fresh = true;  // the place inside request r is still to be found
+      while (alive && at < end && r < R) {
+        const AttnRequest q = attn_request(p, r);
+        const int pos = q.kv - q.n, items = (q.n + w - 1) / w;
+        if (fresh) {
+          // whole heads first, then 32 items at a time
+          const long long per_head = head_units(pos, lane == 0 ? q.n : 0, w, window);
+          const long long uh = __shfl_sync(0xffffffffu, per_head, 0);
+          head = (int)((at - prefix) / uh);
+          prefix += uh * head;
+          item = 0;
+          for (int base = 0; base < items; base += 32) {
+            const int i = base + lane;
+            long long u = 0;
+            if (i < items) {
+              const Span s = item_span(pos, q.n, i, w, window);
+              u = s.u1 - s.u0;
+            }
+            long long scan = u;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+              const long long x = __shfl_up_sync(0xffffffffu, scan, o);
+              if (lane >= o) scan += x;
+            }
+            const bool here = i < items && prefix + scan > at;
+            const unsigned found = __ballot_sync(0xffffffffu, here);
+            if (found) {
+              const int src = __ffs(found) - 1;
+              item = base + src;
+              prefix += __shfl_sync(0xffffffffu, scan - u, src);
+              break;
+            }
+            prefix += __shfl_sync(0xffffffffu, scan, 31);
+          }
+          fresh = false;
+        }
+        // `prefix` is the first unit of item `item` of head `head`
+        while (alive && at < end && head < Hkv && items > 0) {
+          const Span s = item_span(pos, q.n, item, w, window);
+          const long long item_end = prefix + (s.u1 - s.u0);
+          Segment g2;
+          g2.row0 = q.row0 + item * w;
+          g2.ntok = min(q.n - item * w, w);
+          g2.head = head;
+          g2.pos0 = pos + item * w;
+          g2.request = r;
+          g2.lo = s.lo;
+          g2.hi = s.hi;
+          g2.u0 = s.u0 + (int)(at - prefix);
+          const long long stop = end < item_end ? end : item_end;
+          g2.u1 = s.u0 + (int)(stop - prefix);
+          g2.dual = g2.ntok > tpt;
+          // the CTA that holds unit x: the last whose share begins at or before it
+          const long long c0 = ((prefix + 1) * ctas - 1) / total, c1 = (item_end * ctas - 1) / total;
+          g2.cta0 = (int)c0;
+          g2.parts = (int)(c1 - c0) + 1;
+          g2.part = (int)(cta - c0);
+          const uint32_t slot = out % RING;
+          alive = warp_wait(&sh.seg_empty[slot], (out / RING + 1) & 1);
+          if (!alive) break;
+          if (lane == 0) {
+            sh.seg[slot] = g2;
+            mbar_arrive(&sh.seg_full[slot]);
+          }
+          __syncwarp();
+          ++out;
+          at = stop;
+          prefix = item_end;
+          if (++item == items) {
+            item = 0;
+            ++head;
+          }
+        }
+        ++r;
+        head = item = 0;
+      }
+      if (alive) {
+        const uint32_t slot = out % RING;
+        alive = warp_wait(&sh.seg_empty[slot], (out / RING + 1) & 1);
+        if (alive && lane == 0) {
+          sh.seg[slot].ntok = -1;
+          mbar_arrive(&sh.seg_full[slot]);
+        }
+      }
+    } else if (warp == K_WARP || warp == V_WARP) {
+      // ---- keys or values of the CTA's units, a lane per copy
+      const bool values = warp == V_WARP;
+      const CUtensorMap* const map = values ? &vmap : &kmap;
+      const int stages = values ? S::V_STAGES : S::K_STAGES;
+      uint8_t* const ring = smem + (values ? S::V0 : S::K0);
+      uint64_t* const full = values ? sh.v_full : sh.k_full;
+      uint64_t* const empty = values ? sh.v_empty : sh.k_empty;
+      const int P = p.cache.page_size, box = a.box;
+      const int copies = (UNIT / box) * (D / 64);
+      const int piece = lane / (D / 64), half = lane % (D / 64);  // which keys of the unit, which columns
+      uint32_t n = 0, tails = 0;
+      bool bad_page = false;
+      for (uint32_t in = 0; alive; ++in) {
+        const uint32_t slot = in % RING;
+        alive = warp_wait(&sh.seg_full[slot], (in / RING) & 1);
+        if (!alive) break;
+        const Segment sg = sh.seg[slot];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.seg_empty[slot]);
+        if (sg.ntok < 0) break;
+        const int32_t* const table = p.table + (int64_t)sg.request * p.table_stride;
+        for (int u = sg.u0; u < sg.u1; ++u) {
+          // up to 32 copies a round; a unit of 128 keys in pages of 16 has 8 pieces, 16 copies
+          const int key = u * UNIT + piece * box;
+          const bool wanted = lane < copies && key < sg.hi && key + box > sg.lo;
+          int page = 0;
+          if (wanted) {
+            page = table[key / P];
+            if (page < 0 || page >= p.cache.num_pages) {
+              page = p.cache.num_pages;  // past the end: the copy brings zeros
+              bad_page = true;
+            }
+          }
+          const uint32_t st = n % stages;
+          alive = warp_wait(&empty[st], (n / stages + 1) & 1);
+          if (!alive) break;
+          uint8_t* const dst = ring + st * S::TILE_BYTES;
+          const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, wanted)) * (uint32_t)box * 128u;
+          const int first = max(sg.lo - u * UNIT, 0), last = min(sg.hi - u * UNIT, UNIT);  // the unit's keys in use
+          const bool ragged = values && (first > 0 || last < UNIT);
+          uint64_t* const bar = ragged ? &sh.v_tail : &full[st];
+          if (lane == 0) mbar_expect_tx(bar, bytes);
+          __syncwarp();
+          if (wanted)
+            tma_load_4d(dst + half * (TILE * 128) + piece * box * 128, map, half * 64, key % P, sg.head, page, bar);
+          if (ragged) {
+            // weights of unseen keys are zero, but zero times what lies there need not be: clear those rows
+            alive = warp_wait(&sh.v_tail, tails & 1);
+            if (!alive) break;
+            ++tails;
+            for (int x = lane; x < TILE * (D / 8); x += 32) {
+              const int row = (x >> 3) & (TILE - 1);
+              if (row < first || row >= last) *reinterpret_cast<uint4*>(dst + x * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[st]);
+          }
+          ++n;
+        }
+      }
+      if (bad_page && p.error_word) atomicOr(p.error_word, KDA_ERR_PAGES);
+      if (!alive) {  // copies in flight land before the CTA leaves
+        if (values) mbar_drain_bounded(&sh.v_tail, tails & 1);
+        for (uint32_t i = n > (uint32_t)stages ? n - stages : 0; i < n; ++i)
+          mbar_drain_bounded(&full[i % stages], (i / stages) & 1);
+      }
+    } else {
+      // ---- the products
+      uint32_t kn = 0, vn = 0, seen_p[2] = {0, 0}, segs = 0;  // units of keys and values taken, weights waited for
+      const uint32_t smem_base = smem_addr(smem);
+      constexpr uint32_t IDESC_S = idesc_bf16_f32(TILE, UNIT);
+      constexpr uint32_t IDESC_O = idesc_bf16_f32(TILE, D) | B_MN_MAJOR;
+      for (uint32_t in = 0; alive; ++in) {
+        const uint32_t slot = in % RING;
+        alive = warp_wait(&sh.seg_full[slot], (in / RING) & 1);
+        if (!alive) break;
+        const Segment sg = sh.seg[slot];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.seg_empty[slot]);
+        if (sg.ntok < 0) break;
+        alive = warp_wait(&sh.q_full[0], segs & 1) && warp_wait(&sh.q_full[1], segs & 1);
+        ++segs;
+        if (!alive) break;
+        const int n = sg.u1 - sg.u0, dual = sg.dual, steps = dual ? 2 * n : n;
+        const uint32_t k0 = kn, v0 = vn;  // the run's first units in the rings
+        kn += n;
+        vn += n;
+        auto scores = [&](int s) {  // S of step s: tile s & 1
+          const int t = s & 1;
+          const uint32_t u = k0 + (dual ? s >> 1 : s), st = u % S::K_STAGES;
+          if (!dual || t == 0) {
+            if (!warp_wait(&sh.k_full[st], (u / S::K_STAGES) & 1)) return false;
+            tc_fence_after();
+          }
+          const uint32_t q = smem_base + (dual && t ? S::Q1 : S::Q0), k = smem_base + S::K0 + st * S::TILE_BYTES;
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            const uint32_t off = (i >> 2) * (TILE * 128) + (i & 3) * 32;
+            tc_mma_bf16_w(S_COL + t * TILE, sw128_desc(q + off), sw128_desc(k + off), IDESC_S, i > 0);
+          }
+          if (!dual || t == 1) tc_commit_w(&sh.k_empty[st]);
+          tc_commit_w(&sh.s_full[t]);
+          return true;
+        };
+        alive = scores(0) && (steps < 2 || scores(1));
+        for (int s = 0; alive && s < steps; ++s) {
+          const int t = s & 1;
+          const uint32_t u = v0 + (dual ? s >> 1 : s), st = u % S::V_STAGES;
+          if (!dual || t == 0) alive = warp_wait(&sh.v_full[st], (u / S::V_STAGES) & 1);
+          alive = alive && warp_wait(&sh.p_full[t], seen_p[t] & 1);
+          if (!alive) break;
+          ++seen_p[t];
+          tc_fence_after();
+          const uint32_t v = smem_base + S::V0 + st * S::TILE_BYTES;
+#pragma unroll
+          for (int i = 0; i < UNIT / 16; ++i)
+            tc_mma_bf16_ta_w(O_COL + t * D, S_COL + t * TILE + i * 8, value_desc(v + i * 2048), IDESC_O, s > 1 || i > 0);
+          if (!dual || t == 1) tc_commit_w(&sh.v_empty[st]);
+          tc_commit_w(&sh.o_done[t]);
+          if (s + 2 < steps) alive = scores(s + 2);
+        }
+      }
+      if (!alive) {  // products in flight end before the tensor memory goes
+        tc_commit_w(&sh.drain);
+        mbar_drain_bounded(&sh.drain, 0);
+      }
+    }
+    if (!alive && lane == 0 && p.error_word) atomicOr(p.error_word, KDA_ERR_TIMEOUT);
+  } else {
+    // ---- softmax: group t, thread (row) x
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SOFTMAX_REGS));
+    const int t = warp >> 2, x = tid & (TILE - 1);
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_addr = S_COL + t * TILE + lane_base, o_addr = O_COL + t * D + lane_base;
+    const float c = p.scale * LOG2E;
+    uint32_t seen_s = 0;  // scores waited for; as many products with values were asked for
+    bool alive = true;
+    const int token_of_row = x / g, head_of_row = x - token_of_row * g;
+    for (uint32_t in = 0;; ++in) {
+      const uint32_t slot = in % RING;
+      alive = warp_wait(&sh.seg_full[slot], (in / RING) & 1);
+      if (bar_any(1, SOFTMAX_THREADS, !alive)) {  // both groups leave together
+        alive = false;
+        break;
+      }
+      const Segment sg = sh.seg[slot];
+      bar_sync(2, SOFTMAX_THREADS);
+      if (x == 0) mbar_arrive(&sh.seg_empty[slot]);
+      if (sg.ntok < 0) break;
+      const int dual = sg.dual;
+
+      // queries: this group's tile, or its half of the shared one
+      {
+        const int tile0 = dual ? t * tpt : 0;  // first token of the tile
+        const int rows = min(sg.ntok - tile0, tpt) * g;
+        uint8_t* const qs = smem + (dual && t ? S::Q1 : S::Q0);
+        const int from = dual ? 0 : t * (TILE / 2), to = min(rows, dual ? TILE : from + TILE / 2);
+        const uint16_t* const qg = static_cast<const uint16_t*>(p.q.ptr);
+        for (int i = from * (D / 8) + x; i < to * (D / 8); i += TILE) {
+          const int row = i / (D / 8), ch = i % (D / 8);
+          const int tok = row / g, hd = row - tok * g;
+          const uint16_t* const src = qg + (int64_t)(sg.row0 + tile0 + tok) * p.q.b_stride +
+                                      (int64_t)(sg.head * g + hd) * p.q.h_stride + ch * 8;
+          uint4 val;
+          if (a.q_wide) {
+            val = __ldg(reinterpret_cast<const uint4*>(src));
+          } else {
+            uint32_t e[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) e[j] = (uint32_t)src[2 * j] | ((uint32_t)src[2 * j + 1] << 16);
+            val = make_uint4(e[0], e[1], e[2], e[3]);
+          }
+          *reinterpret_cast<uint4*>(qs + (ch >> 3) * (TILE * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4)) = val;
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&sh.q_full[t]);
+      }
+
+      const int tok = (dual ? t * tpt : 0) + token_of_row;
+      const bool valid = token_of_row < tpt && tok < sg.ntok;
+      const int hi = valid ? sg.pos0 + tok + 1 : 0;  // this row sees keys [lo, hi)
+      const int lo = window > 0 ? max(0, hi - window) : 0;
+      const bool warp_valid = __any_sync(0xffffffffu, valid);
+      float m = -INFINITY, l = 0.f;  // m: the reference, in units of the scores
+      const int step = dual ? 1 : 2;
+      int units = 0;
+      for (int u = sg.u0 + (dual ? 0 : t); u < sg.u1; u += step) {
+        alive = alive && warp_wait(&sh.s_full[t], seen_s & 1);
+        if (!alive) break;
+        if (warp_valid) {
+          tc_fence_after();
+          uint32_t s[UNIT];
+#pragma unroll
+          for (int i = 0; i < UNIT; i += 32) ld32(s_addr + i, s + i);
+          ld_wait();
+#pragma unroll
+          for (int i = 0; i < UNIT; i += 32) hold32(s + i);
+          const int k0 = u * UNIT;
+          if (__any_sync(0xffffffffu, k0 + UNIT > hi || k0 < lo)) {
+            const int from = lo - k0, to = hi - k0;
+#pragma unroll
+            for (int i = 0; i < UNIT; ++i)
+              if (i < from || i >= to) s[i] = 0xff800000u;  // -inf
+          }
+          float top = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < UNIT; ++i) top = fmaxf(top, __uint_as_float(s[i]));
+          const bool first = units == 0;
+          const bool grown = top > m && (top - m) * c > SLACK;  // m = -inf: any key
+          if (__any_sync(0xffffffffu, grown)) {
+            const float fade = grown ? ex2((m - top) * c) : 1.f;
+            if (grown) m = top;
+            l *= fade;
+            if (!first) {
+              alive = warp_wait(&sh.o_done[t], (seen_s - 1) & 1);
+              if (!alive) break;
+              tc_fence_after();
+#pragma unroll
+              for (int i = 0; i < D; i += 32) {
+                uint32_t o[32];
+                ld32(o_addr + i, o);
+                ld_wait();
+                hold32(o);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * fade);
+                st32(o_addr + i, o);
+              }
+            }
+          }
+          const float base = m == -INFINITY ? 0.f : -m * c;
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < UNIT; i += 64) {
+            uint32_t w2[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const float e0 = ex2(fmaf(__uint_as_float(s[i + 2 * j]), c, base));
+              const float e1 = ex2(fmaf(__uint_as_float(s[i + 2 * j + 1]), c, base));
+              sum[j & 1] += e0;
+              sum[2 + (j & 1)] += e1;
+              w2[j] = pack_bf16x2(e0, e1);
+            }
+            st32(s_addr + i / 2, w2);
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tmem_st_wait();
+          tc_fence_before();
+        }
+        ++seen_s;
+        ++units;
+        mbar_arrive(&sh.p_full[t]);
+      }
+
+      // ---- the end of the run
+      if (alive && units > 0) alive = warp_wait(&sh.o_done[t], (seen_s - 1) & 1);
+      if (units > 0) tc_fence_after();
+      float fade0 = 1.f;  // what the O of this thread's tensor memory is scaled by
+      float fade1 = 0.f;
+      if (!dual && t == 1) {
+        sh.m1[x] = m;
+        sh.l1[x] = l;
+      }
+      if (bar_any(1, SOFTMAX_THREADS, !alive)) {
+        alive = false;
+        break;
+      }
+      if (!dual && t == 0) {
+        const float mo = sh.m1[x], mm = fmaxf(m, mo), mb = mm == -INFINITY ? 0.f : mm;
+        fade0 = ex2((m - mb) * c);
+        fade1 = ex2((mo - mb) * c);
+        l = l * fade0 + sh.l1[x] * fade1;
+        m = mm;
+      }
+      const bool direct = sg.parts == 1;
+      const bool writes = (dual || t == 0) && valid;
+      const int64_t row = (int64_t)sg.row0 + tok;
+      const int qh = sg.head * g + head_of_row;
+      const int slot_id = sg.part == 0 ? 2 * (int)cta + 1 : 2 * (int)cta;
+      float* const part = direct ? nullptr : part_slot<D>(a, slot_id) + (size_t)((dual ? t * TILE : 0) + x) * D;
+      const bool none = l == 0.f;  // no key: zeros
+      const float inv = 1.f / l;
+      float* const other = reinterpret_cast<float*>(smem + S::Q1);  // the second group's O, half the columns at a time
+      const bool two = !dual && sg.u1 - sg.u0 > 1;  // the second group has one
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (two) {
+          if (t == 1 && warp_valid) {
+#pragma unroll
+            for (int i = 0; i < D / 2; i += 32) {
+              uint32_t o[32];
+              ld32(o_addr + h * (D / 2) + i, o);
+              ld_wait();
+              hold32(o);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) other[(i + j) * TILE + x] = __uint_as_float(o[j]);
+            }
+          }
+          bar_sync(2, SOFTMAX_THREADS);
+        }
+        if (warp_valid && (dual || t == 0)) {
+#pragma unroll
+          for (int i = 0; i < D / 2; i += 32) {
+            uint32_t o[32];
+            ld32(o_addr + h * (D / 2) + i, o);
+            ld_wait();
+            hold32(o);
+            float f[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(o[j]);
+            if (two) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) f[j] = f[j] * fade0 + other[(i + j) * TILE + x] * fade1;
+            }
+            if (writes) {
+              const int col = h * (D / 2) + i;
+              if (direct) {
+                uint16_t* const dst = static_cast<uint16_t*>(p.out) + row * p.out_b_stride + (int64_t)qh * p.out_h_stride + col;
+                uint32_t b[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) b[j] = none ? 0u : pack_bf16x2(f[2 * j] * inv, f[2 * j + 1] * inv);
+                if (a.out_wide) {
+#pragma unroll
+                  for (int j = 0; j < 4; ++j)
+                    reinterpret_cast<uint4*>(dst)[j] = make_uint4(b[4 * j], b[4 * j + 1], b[4 * j + 2], b[4 * j + 3]);
+                } else {
+#pragma unroll
+                  for (int j = 0; j < 16; ++j) {
+                    dst[2 * j] = (uint16_t)b[j];
+                    dst[2 * j + 1] = (uint16_t)(b[j] >> 16);
+                  }
+                }
+              } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                  reinterpret_cast<float4*>(part + col)[j] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+              }
+            }
+          }
+        }
+        if (two && h == 0) bar_sync(2, SOFTMAX_THREADS);
+      }
+      tc_fence_before();
+      if (writes) {
+        if (direct) {
+          if (p.lse != nullptr) p.lse[row * p.num_q_heads + qh] = m == -INFINITY ? -INFINITY : m * p.scale + logf(l);
+        } else {
+          float* const ml = part_slot<D>(a, slot_id) + (size_t)(2 * TILE) * D + 2 * ((dual ? t * TILE : 0) + x);
+          ml[0] = m;
+          ml[1] = l;
+        }
+      }
+      if (!direct) {
+        __threadfence();
+        bar_sync(1, SOFTMAX_THREADS);
+        if (tid == 0) {
+          const unsigned done = atomicAdd(&a.counters[sg.cta0], 1u);
+          sh.last_part = done + 1 == (unsigned)sg.parts;
+          if (sh.last_part) a.counters[sg.cta0] = 0;
+          __threadfence();
+        }
+        bar_sync(2, SOFTMAX_THREADS);
+        if (sh.last_part) {
+          // join the parts in their order: a thread takes four columns of a row
+          __threadfence();
+          const int tiles = dual ? 2 : 1;
+          for (int i = tid; i < tiles * TILE * (D / 4); i += SOFTMAX_THREADS) {
+            const int pr = i / (D / 4), col = (i % (D / 4)) * 4;
+            const int tile = pr / TILE, rr = pr % TILE, tk = rr / g;
+            const int token = tile * tpt + tk;
+            if (tk >= tpt || token >= sg.ntok) continue;
+            float mm = -INFINITY;
+            for (int q = 0; q < sg.parts; ++q) {
+              const int sid = q == 0 ? 2 * sg.cta0 + 1 : 2 * (sg.cta0 + q);
+              mm = fmaxf(mm, __ldcg(part_slot<D>(a, sid) + (size_t)(2 * TILE) * D + 2 * pr));
+            }
+            const float mb = mm == -INFINITY ? 0.f : mm;
+            float ll = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int q = 0; q < sg.parts; ++q) {
+              const int sid = q == 0 ? 2 * sg.cta0 + 1 : 2 * (sg.cta0 + q);
+              const float* const slot_base = part_slot<D>(a, sid);
+              const float2 z = __ldcg(reinterpret_cast<const float2*>(slot_base + (size_t)(2 * TILE) * D + 2 * pr));
+              const float4 v = __ldcg(reinterpret_cast<const float4*>(slot_base + (size_t)pr * D + col));
+              const float f = ex2((z.x - mb) * c);
+              ll = fmaf(z.y, f, ll);
+              acc[0] = fmaf(v.x, f, acc[0]);
+              acc[1] = fmaf(v.y, f, acc[1]);
+              acc[2] = fmaf(v.z, f, acc[2]);
+              acc[3] = fmaf(v.w, f, acc[3]);
+            }
+            const float iv = 1.f / ll;
+            const int64_t orow = (int64_t)sg.row0 + token;
+            const int oh = sg.head * g + (rr - tk * g);
+            uint16_t* const dst = static_cast<uint16_t*>(p.out) + orow * p.out_b_stride + (int64_t)oh * p.out_h_stride + col;
+            const uint32_t b0 = ll == 0.f ? 0u : pack_bf16x2(acc[0] * iv, acc[1] * iv);
+            const uint32_t b1 = ll == 0.f ? 0u : pack_bf16x2(acc[2] * iv, acc[3] * iv);
+            if (a.out_wide) {
+              *reinterpret_cast<uint2*>(dst) = make_uint2(b0, b1);
+            } else {
+              dst[0] = (uint16_t)b0;
+              dst[1] = (uint16_t)(b0 >> 16);
+              dst[2] = (uint16_t)b1;
+              dst[3] = (uint16_t)(b1 >> 16);
+            }
+            if (p.lse != nullptr && col == 0)
+              p.lse[orow * p.num_q_heads + oh] = mm == -INFINITY ? -INFINITY : mm * p.scale + logf(ll);
+          }
+        }
+      }
+    }
+    if (!alive && x == 0 && p.error_word) atomicOr(p.error_word, KDA_ERR_TIMEOUT);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == MMA_WARP) tmem_dealloc(tmem, 512);
+}
+
+size_t paged_attention_parts_bytes(int head_dim, int ctas) {
+  return (size_t)ctas * 2 * (2 * TILE) * (head_dim + 2) * sizeof(float);
+}
+
+bool paged_attention_on_tensor_cores(const kda_paged_cache& c) {
+  auto rows16 = [](const kda_pages& g) {
+    return (reinterpret_cast<uintptr_t>(g.ptr) & 15) == 0 && g.page_stride % 8 == 0 && g.token_stride % 8 == 0 &&
+           g.head_stride % 8 == 0;
+  };
+  return (c.head_dim == 64 || c.head_dim == 128) && c.num_pages > 0 && c.page_size >= 16 &&
+         (c.page_size & (c.page_size - 1)) == 0 && rows16(c.k) && rows16(c.v);
+}
+
+template <int D>
+static cudaError_t launch_tc(const CUtensorMap& km, const CUtensorMap& vm, const AttnArgs& a, int ctas, cudaStream_t s) {
+  constexpr size_t bytes = Shape<D>::END + sizeof(Shared) + 1024;
+  static_assert(bytes <= 232448, "shared memory of one CTA");
+  static std::atomic<bool> done{false};
+  const cudaError_t e = set_smem_limit_once(kda_paged_attention_tc_kernel<D>, bytes, done);
+  if (e != cudaSuccess) return e;
+  kda_paged_attention_tc_kernel<D><<<ctas, THREADS, bytes, s>>>(km, vm, a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_paged_attention_tc(const kda_attention_params& p, void* workspace, int ctas, cudaStream_t s) {
+  AttnArgs a;
+  a.p = p;
+  a.counters = static_cast<unsigned*>(workspace);
+  a.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + KDA_ATTENTION_WORKSPACE_ZEROED);
+  auto rows16 = [](const void* x, int64_t b, int64_t h) {
+    return (reinterpret_cast<uintptr_t>(x) & 15) == 0 && b % 8 == 0 && h % 8 == 0;
+  };
+  a.q_wide = rows16(p.q.ptr, p.q.b_stride, p.q.h_stride);
+  a.out_wide = rows16(p.out, p.out_b_stride, p.out_h_stride);
+  a.box = p.cache.page_size < UNIT ? p.cache.page_size : UNIT;
+  CUtensorMap km, vm;
+  cudaError_t e = pages_tensor_map(p.cache.k, p.cache, a.box, &km);
+  if (e == cudaSuccess) e = pages_tensor_map(p.cache.v, p.cache, a.box, &vm);
+  if (e != cudaSuccess) return e;
+  return p.cache.head_dim == 64 ? launch_tc<64>(km, vm, a, ctas, s) : launch_tc<128>(km, vm, a, ctas, s);
+}
+
+}  // namespace kda

@@ -6,6 +6,7 @@
 
 #include "kda_device.cuh"
 #include "kda_launch.h"
+#include "kda_paged_launch.h"
 
 namespace kda {
 
@@ -148,6 +149,26 @@ cudaError_t token_tensor_map_bt(const kda_view& v, int B, int T, int H, int TT, 
   c.map = map;
   *out = map;
   return cudaSuccess;
+}
+
+// One side of a paged cache as a 4-D tensor {head_dim, page_size tokens, heads,
+// pages} read in {64, box, 1, 1} boxes with the 128-byte swizzle: 64 columns of
+// `box` tokens of one page and head. Formed per call (a serving step has a cache
+// per layer); cudaErrorNotSupported where the strides have no such map.
+cudaError_t pages_tensor_map(const kda_pages& g, const kda_paged_cache& c, int box, CUtensorMap* out) {
+  const EncodeTiledFn fn = encode_tiled();
+  if (fn == nullptr) return cudaErrorNotSupported;
+  const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.page_size, (cuuint64_t)c.num_heads,
+                              (cuuint64_t)c.num_pages};
+  // the stride of a dimension of one entry is never used
+  const int64_t head = c.num_heads > 1 ? g.head_stride : c.head_dim, page = c.num_pages > 1 ? g.page_stride : c.head_dim;
+  const cuuint64_t strides[3] = {(cuuint64_t)g.token_stride * 2, (cuuint64_t)head * 2, (cuuint64_t)page * 2};
+  const cuuint32_t boxes[4] = {64, (cuuint32_t)box, 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = fn(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, g.ptr, dims, strides, boxes, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorNotSupported;
 }
 
 }  // namespace kda

@@ -247,7 +247,7 @@ def test_attention_empty_rows(dev, D, page):
 @pytest.mark.parametrize("D", [128, 64, 72])
 def test_attention_bad_requests_are_skipped_and_reported(dev, D):
     a = Attention([4, 3, 6, 2], [40, 3, 90, 20], 4, 2, D, 16, seed=6)
-    a.cu = np.array([0, 4, 7, 5, 15])        # request 2's bounds go backwards
+    a.cu = np.array([0, 4, 7, 99, 15])       # request 2 ends past the rows, request 3's bounds go backwards
     a.kv[1] = 10 ** 6                        # over its block table
     ref = a.oracle()
     err = err_word(dev)
