@@ -210,15 +210,21 @@ constexpr float SLACK = 8.f;  // growth of the maximum (log2) that the reference
 
 struct AttnArgs {
   kda_attention_params p;
-  float* parts;        // workspace: 2 slots a CTA of TILE x 2 rows of D sums, then m and l of each row
+  float* parts;        // workspace: 2 slots a CTA, each [D / 4][2 TILE] float4 of unnormalised O, then [2 TILE] of (m, l)
   unsigned* counters;  // one a CTA, zero between calls
   int q_wide, out_wide;
   int box;             // keys a copy brings: min(page_size, UNIT)
 };
 
+// A part's O by groups of four columns, the rows of a group side by side: a warp's threads (a row each) write and read
+// whole lines.
 template <int D>
-__device__ __forceinline__ float* part_slot(const AttnArgs& a, int slot) {
-  return a.parts + (size_t)slot * (2 * TILE) * (D + 2);
+__device__ __forceinline__ float4* part_o(const AttnArgs& a, int slot) {
+  return reinterpret_cast<float4*>(a.parts + (size_t)slot * (2 * TILE) * (D + 2));
+}
+template <int D>
+__device__ __forceinline__ float2* part_ml(const AttnArgs& a, int slot) {
+  return reinterpret_cast<float2*>(a.parts + (size_t)slot * (2 * TILE) * (D + 2) + (size_t)(2 * TILE) * D);
 }
 
 }  // namespace
@@ -694,7 +700,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int64_t row = (int64_t)sg.row0 + tok;
       const int qh = sg.head * g + head_of_row;
       const int slot_id = sg.part == 0 ? 2 * (int)cta + 1 : 2 * (int)cta;
-      float* const part = direct ? nullptr : part_slot<D>(a, slot_id) + (size_t)((dual ? t * TILE : 0) + x) * D;
+      const int part_row = (dual ? t * TILE : 0) + x;
       const bool none = l == 0.f;  // no key: zeros
       const float inv = 1.f / l;
       float* const other = reinterpret_cast<float*>(smem + S::Q1);  // the second group's O, half the columns at a time
@@ -750,7 +756,8 @@ __global__ void __launch_bounds__(THREADS, 1)
               } else {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                  reinterpret_cast<float4*>(part + col)[j] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+                  part_o<D>(a, slot_id)[(col / 4 + j) * (2 * TILE) + part_row] =
+                      make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
               }
             }
           }
@@ -762,9 +769,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (direct) {
           if (p.lse != nullptr) p.lse[row * p.num_q_heads + qh] = m == -INFINITY ? -INFINITY : m * p.scale + logf(l);
         } else {
-          float* const ml = part_slot<D>(a, slot_id) + (size_t)(2 * TILE) * D + 2 * ((dual ? t * TILE : 0) + x);
-          ml[0] = m;
-          ml[1] = l;
+          part_ml<D>(a, slot_id)[part_row] = make_float2(m, l);
         }
       }
       if (!direct) {
@@ -778,49 +783,90 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         bar_sync(2, SOFTMAX_THREADS);
         if (sh.last_part) {
-          // join the parts in their order: a thread takes four columns of a row
+          // join the parts in their order; first every row's maximum and sum, a thread a row
           __threadfence();
-          const int tiles = dual ? 2 : 1;
-          for (int i = tid; i < tiles * TILE * (D / 4); i += SOFTMAX_THREADS) {
-            const int pr = i / (D / 4), col = (i % (D / 4)) * 4;
-            const int tile = pr / TILE, rr = pr % TILE, tk = rr / g;
-            const int token = tile * tpt + tk;
-            if (tk >= tpt || token >= sg.ntok) continue;
-            float mm = -INFINITY;
+          auto slot_of = [&](int q) { return q == 0 ? 2 * sg.cta0 + 1 : 2 * (sg.cta0 + q); };
+          const int rows = dual ? TILE + (sg.ntok - tpt) * g : sg.ntok * g;
+          float* const jm = reinterpret_cast<float*>(smem + S::Q0);  // the queries are done with
+          float* const jl = jm + 2 * TILE;
+          const bool is_row = tid < rows && tid % TILE < tpt * g;
+          if (is_row) {
+            float mm = -INFINITY, ll = 0.f;
+            for (int q = 0; q < sg.parts; q += 8) {
+              float2 z[8];
+              float top = mm;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                z[i] = q + i < sg.parts ? __ldcg(part_ml<D>(a, slot_of(q + i)) + tid) : make_float2(-INFINITY, 0.f);
+                top = fmaxf(top, z[i].x);
+              }
+              const float mb = top == -INFINITY ? 0.f : top;
+              ll *= ex2((mm - mb) * c);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) ll = fmaf(z[i].y, ex2((z[i].x - mb) * c), ll);
+              mm = top;
+            }
+            jm[tid] = mm == -INFINITY ? 0.f : mm;
+            jl[tid] = ll;
+            if (p.lse != nullptr) {
+              const int tk = tid % TILE / g;
+              const int64_t orow = (int64_t)sg.row0 + tid / TILE * tpt + tk;
+              p.lse[orow * p.num_q_heads + sg.head * g + (tid % TILE - tk * g)] =
+                  mm == -INFINITY ? -INFINITY : mm * p.scale + logf(ll);
+            }
+          }
+          bar_sync(1, SOFTMAX_THREADS);
+          // then four columns of a row at a time; `pad` rows a group of columns, so that neighbours read neighbours
+          const int pad = (rows + 7) & ~7;
+          constexpr int U = 4;
+          for (int i0 = tid; i0 < pad * (D / 4); i0 += U * SOFTMAX_THREADS) {
+            float acc[U][4];
+            int at[U];
+            float mb[U];
+            bool on[U];
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+              const int i = i0 + k * SOFTMAX_THREADS;
+              const int col = i / pad, row2 = i - col * pad;
+              on[k] = col < D / 4 && row2 < rows && row2 % TILE < tpt * g;
+              at[k] = on[k] ? col * (2 * TILE) + row2 : 0;
+              mb[k] = on[k] ? jm[row2] : 0.f;
+              acc[k][0] = acc[k][1] = acc[k][2] = acc[k][3] = 0.f;
+            }
+#pragma unroll 2
             for (int q = 0; q < sg.parts; ++q) {
-              const int sid = q == 0 ? 2 * sg.cta0 + 1 : 2 * (sg.cta0 + q);
-              mm = fmaxf(mm, __ldcg(part_slot<D>(a, sid) + (size_t)(2 * TILE) * D + 2 * pr));
+              const int sid = slot_of(q);
+#pragma unroll
+              for (int k = 0; k < U; ++k) {
+                if (!on[k]) continue;
+                const float4 v = __ldcg(part_o<D>(a, sid) + at[k]);
+                const float f = ex2((__ldcg(&part_ml<D>(a, sid)[at[k] % (2 * TILE)].x) - mb[k]) * c);
+                acc[k][0] = fmaf(v.x, f, acc[k][0]);
+                acc[k][1] = fmaf(v.y, f, acc[k][1]);
+                acc[k][2] = fmaf(v.z, f, acc[k][2]);
+                acc[k][3] = fmaf(v.w, f, acc[k][3]);
+              }
             }
-            const float mb = mm == -INFINITY ? 0.f : mm;
-            float ll = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-            for (int q = 0; q < sg.parts; ++q) {
-              const int sid = q == 0 ? 2 * sg.cta0 + 1 : 2 * (sg.cta0 + q);
-              const float* const slot_base = part_slot<D>(a, sid);
-              const float2 z = __ldcg(reinterpret_cast<const float2*>(slot_base + (size_t)(2 * TILE) * D + 2 * pr));
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(slot_base + (size_t)pr * D + col));
-              const float f = ex2((z.x - mb) * c);
-              ll = fmaf(z.y, f, ll);
-              acc[0] = fmaf(v.x, f, acc[0]);
-              acc[1] = fmaf(v.y, f, acc[1]);
-              acc[2] = fmaf(v.z, f, acc[2]);
-              acc[3] = fmaf(v.w, f, acc[3]);
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+              if (!on[k]) continue;
+              const int row2 = at[k] % (2 * TILE), col = at[k] / (2 * TILE) * 4;
+              const float ll = jl[row2], iv = 1.f / ll;
+              const int tk = row2 % TILE / g;
+              const int64_t orow = (int64_t)sg.row0 + row2 / TILE * tpt + tk;
+              const int oh = sg.head * g + (row2 % TILE - tk * g);
+              uint16_t* const dst = static_cast<uint16_t*>(p.out) + orow * p.out_b_stride + (int64_t)oh * p.out_h_stride + col;
+              const uint32_t b0 = ll == 0.f ? 0u : pack_bf16x2(acc[k][0] * iv, acc[k][1] * iv);
+              const uint32_t b1 = ll == 0.f ? 0u : pack_bf16x2(acc[k][2] * iv, acc[k][3] * iv);
+              if (a.out_wide) {
+                *reinterpret_cast<uint2*>(dst) = make_uint2(b0, b1);
+              } else {
+                dst[0] = (uint16_t)b0;
+                dst[1] = (uint16_t)(b0 >> 16);
+                dst[2] = (uint16_t)b1;
+                dst[3] = (uint16_t)(b1 >> 16);
+              }
             }
-            const float iv = 1.f / ll;
-            const int64_t orow = (int64_t)sg.row0 + token;
-            const int oh = sg.head * g + (rr - tk * g);
-            uint16_t* const dst = static_cast<uint16_t*>(p.out) + orow * p.out_b_stride + (int64_t)oh * p.out_h_stride + col;
-            const uint32_t b0 = ll == 0.f ? 0u : pack_bf16x2(acc[0] * iv, acc[1] * iv);
-            const uint32_t b1 = ll == 0.f ? 0u : pack_bf16x2(acc[2] * iv, acc[3] * iv);
-            if (a.out_wide) {
-              *reinterpret_cast<uint2*>(dst) = make_uint2(b0, b1);
-            } else {
-              dst[0] = (uint16_t)b0;
-              dst[1] = (uint16_t)(b0 >> 16);
-              dst[2] = (uint16_t)b1;
-              dst[3] = (uint16_t)(b1 >> 16);
-            }
-            if (p.lse != nullptr && col == 0)
-              p.lse[orow * p.num_q_heads + oh] = mm == -INFINITY ? -INFINITY : mm * p.scale + logf(ll);
           }
         }
       }
