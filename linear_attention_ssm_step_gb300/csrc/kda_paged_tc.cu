@@ -46,6 +46,8 @@ constexpr int THREADS = 384;
 constexpr int SOFTMAX_THREADS = 256;
 constexpr int K_WARP = 8, V_WARP = 9, MMA_WARP = 10, WALK_WARP = 11;
 constexpr int RING = 4;  // segments the walking warp may be ahead
+// What an item costs beside its units (its queries, its end), in units: each item takes LEAD + its units of the line.
+constexpr int LEAD = 2;
 // Registers a thread after the split: 256 x 208 + 128 x 88 = 384 x 168, what the block launches with.
 constexpr int SOFTMAX_REGS = 208, OTHER_REGS = 88;
 
@@ -84,6 +86,12 @@ struct Shared {
   int last_part;
 };
 
+// x y / z for x < 2^31, y <= 1024, z > 0: 32-bit where it fits (a 64-bit division takes over a hundred instructions).
+__device__ __forceinline__ long long mul_div(long long x, int y, long long z) {
+  if (x < (1 << 22) && z < (1LL << 32)) return (uint32_t)((uint32_t)x * (uint32_t)y) / (uint32_t)z;
+  return x * y / z;
+}
+
 // The keys [lo, hi) that item i (tokens i w .. of n, the first at position pos) sees, and its units.
 struct Span {
   int lo, hi, u0, u1;
@@ -99,7 +107,7 @@ __device__ __forceinline__ Span item_span(int pos, int n, int i, int w, int wind
   return s;
 }
 
-// Units of one key-value head of a request: n tokens, w an item. Called by whole warps, one request a lane; a request
+// Length on the line of one key-value head of a request: n tokens, w an item. Called by whole warps, one request a lane; a request
 // of many items (a long chunk) is summed by the warp together.
 __device__ __forceinline__ long long head_units(int pos, int n, int w, int window) {
   const int items = (n + w - 1) / w;
@@ -107,7 +115,7 @@ __device__ __forceinline__ long long head_units(int pos, int n, int w, int windo
   if (items <= 4)
     for (int i = 0; i < items; ++i) {
       const Span s = item_span(pos, n, i, w, window);
-      units += s.u1 - s.u0;
+      units += LEAD + s.u1 - s.u0;
     }
   unsigned many = __ballot_sync(0xffffffffu, items > 4);
   const int lane = threadIdx.x & 31;
@@ -119,7 +127,7 @@ __device__ __forceinline__ long long head_units(int pos, int n, int w, int windo
     long long part = 0;
     for (int i = lane; i < ni; i += 32) {
       const Span s = item_span(pn, nn, i, w, window);
-      part += s.u1 - s.u0;
+      part += LEAD + s.u1 - s.u0;
     }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
@@ -195,6 +203,8 @@ __device__ __forceinline__ bool bar_any(uint32_t id, uint32_t count, bool x) {
       : "memory");
   return any != 0;
 }
+
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
 
 // The value operand: 64-column regions of TILE rows (keys) x 128 bytes, N (the columns) contiguous. Leading byte
 // offset: the next 64 columns, TILE * 128 bytes on; stride byte offset: the next 8 keys, 1024 bytes on. A K step of
@@ -303,10 +313,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   };
   for (int base = 0; base < R; base += THREADS) total += block_units(base);
   if (blockIdx.x == 0 && bad && p.error_word) atomicOr(p.error_word, bad);
-  const long long ctas = total < (long long)gridDim.x ? total : (long long)gridDim.x;
-  const long long cta = blockIdx.x;
+  const int ctas = total < (long long)gridDim.x ? (int)total : (int)gridDim.x;
+  const int cta = blockIdx.x;
   if (cta >= ctas) return;  // the whole CTA: nothing allocated yet
-  const long long begin = total * cta / ctas, end = total * (cta + 1) / ctas;
+  const long long begin = mul_div(total, cta, ctas), end = mul_div(total, cta + 1, ctas);
   {
     long long prefix = 0;
     for (int base = 0; base < R; base += THREADS) {
@@ -344,7 +354,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           // whole heads first, then 32 items at a time
           const long long per_head = head_units(pos, lane == 0 ? q.n : 0, w, window);
           const long long uh = __shfl_sync(0xffffffffu, per_head, 0);
-          head = (int)((at - prefix) / uh);
+          head = (int)mul_div(at - prefix, 1, uh);
           prefix += uh * head;
           item = 0;
           for (int base = 0; base < items; base += 32) {
@@ -352,7 +362,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             long long u = 0;
             if (i < items) {
               const Span s = item_span(pos, q.n, i, w, window);
-              u = s.u1 - s.u0;
+              u = LEAD + s.u1 - s.u0;
             }
             long long scan = u;
 #pragma unroll
@@ -375,24 +385,32 @@ __global__ void __launch_bounds__(THREADS, 1)
         // `prefix` is the first unit of item `item` of head `head`
         while (alive && at < end && head < Hkv && items > 0) {
           const Span s = item_span(pos, q.n, item, w, window);
-          const long long item_end = prefix + (s.u1 - s.u0);
+          const long long units0 = prefix + LEAD, item_end = units0 + (s.u1 - s.u0);
+          const long long from = at > units0 ? at : units0, stop = end < item_end ? end : item_end;
+          at = stop;
+          prefix = item_end;
+          const int i = item;
+          if (++item == items) {
+            item = 0;
+            ++head;
+          }
+          if (from >= stop) continue;  // the share ends before the item's first unit
           Segment g2;
-          g2.row0 = q.row0 + item * w;
-          g2.ntok = min(q.n - item * w, w);
-          g2.head = head;
-          g2.pos0 = pos + item * w;
+          g2.row0 = q.row0 + i * w;
+          g2.ntok = min(q.n - i * w, w);
+          g2.head = item == 0 ? head - 1 : head;
+          g2.pos0 = pos + i * w;
           g2.request = r;
           g2.lo = s.lo;
           g2.hi = s.hi;
-          g2.u0 = s.u0 + (int)(at - prefix);
-          const long long stop = end < item_end ? end : item_end;
-          g2.u1 = s.u0 + (int)(stop - prefix);
+          g2.u0 = s.u0 + (int)(from - units0);
+          g2.u1 = s.u0 + (int)(stop - units0);
           g2.dual = g2.ntok > tpt;
-          // the CTA that holds unit x: the last whose share begins at or before it
-          const long long c0 = ((prefix + 1) * ctas - 1) / total, c1 = (item_end * ctas - 1) / total;
-          g2.cta0 = (int)c0;
-          g2.parts = (int)(c1 - c0) + 1;
-          g2.part = (int)(cta - c0);
+          // the CTA that holds unit x of the line: the last whose share begins at or before it
+          auto holder = [&](long long x) { return x >= begin && x < end ? cta : (int)(((x + 1) * ctas - 1) / total); };
+          g2.cta0 = holder(units0);
+          g2.parts = holder(item_end - 1) - g2.cta0 + 1;
+          g2.part = cta - g2.cta0;
           const uint32_t slot = out % RING;
           alive = warp_wait(&sh.seg_empty[slot], (out / RING + 1) & 1);
           if (!alive) break;
@@ -402,12 +420,6 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           __syncwarp();
           ++out;
-          at = stop;
-          prefix = item_end;
-          if (++item == items) {
-            item = 0;
-            ++head;
-          }
         }
         ++r;
         head = item = 0;
@@ -559,7 +571,15 @@ __global__ void __launch_bounds__(THREADS, 1)
     const float c = p.scale * LOG2E;
     uint32_t seen_s = 0;  // scores waited for; as many products with values were asked for
     bool alive = true;
-    const int token_of_row = x / g, head_of_row = x - token_of_row * g;
+    // row / g for row < 128 and g <= 128: the product's excess is below 128 / 2^16 < 1 / g
+    const uint32_t inv_g = 65536u / (uint32_t)g + 1u;
+    auto div_g = [&](int row) { return (int)((uint32_t)row * inv_g >> 16); };
+    // 16-byte chunks of a tile in shared memory, as the products read them
+    auto tile_chunk = [](int row, int ch) { return (uint32_t)((ch >> 3) * (TILE * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4)); };
+    const int token_of_row = div_g(x), head_of_row = x - token_of_row * g;
+    // a group copies a tile with D / 8 threads a row
+    constexpr int ROWS_A_ROUND = TILE / (D / 8), ROUNDS = TILE / ROWS_A_ROUND;
+    const int my_row = x / (D / 8), my_ch = x % (D / 8);
     for (uint32_t in = 0;; ++in) {
       const uint32_t slot = in % RING;
       alive = warp_wait(&sh.seg_full[slot], (in / RING) & 1);
@@ -579,22 +599,35 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int rows = min(sg.ntok - tile0, tpt) * g;
         uint8_t* const qs = smem + (dual && t ? S::Q1 : S::Q0);
         const int from = dual ? 0 : t * (TILE / 2), to = min(rows, dual ? TILE : from + TILE / 2);
-        const uint16_t* const qg = static_cast<const uint16_t*>(p.q.ptr);
-        for (int i = from * (D / 8) + x; i < to * (D / 8); i += TILE) {
-          const int row = i / (D / 8), ch = i % (D / 8);
-          const int tok = row / g, hd = row - tok * g;
-          const uint16_t* const src = qg + (int64_t)(sg.row0 + tile0 + tok) * p.q.b_stride +
-                                      (int64_t)(sg.head * g + hd) * p.q.h_stride + ch * 8;
-          uint4 val;
-          if (a.q_wide) {
-            val = __ldg(reinterpret_cast<const uint4*>(src));
-          } else {
-            uint32_t e[4];
+        const uint16_t* const qg = static_cast<const uint16_t*>(p.q.ptr) + (int64_t)(sg.row0 + tile0) * p.q.b_stride +
+                                   (int64_t)(sg.head * g) * p.q.h_stride + my_ch * 8;
+        // BATCH rows in flight before the first is stored; a round on, a row stands ROWS_A_ROUND (a multiple of 8) lower
+        constexpr int BATCH = ROUNDS < 8 ? ROUNDS : 8;
+        uint32_t row = from + my_row;
+        const uint32_t at0 = tile_chunk(my_row, my_ch) - my_row * 128;
+#pragma unroll 1
+        for (int k0 = 0; k0 < ROUNDS; k0 += BATCH, row += BATCH * ROWS_A_ROUND) {
+          if (row >= (uint32_t)to) break;
+          uint4 val[BATCH];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) e[j] = (uint32_t)src[2 * j] | ((uint32_t)src[2 * j + 1] << 16);
-            val = make_uint4(e[0], e[1], e[2], e[3]);
+          for (int k = 0; k < BATCH; ++k) {
+            const int r2 = row + k * ROWS_A_ROUND;
+            if (r2 >= to) continue;
+            const int tok = div_g(r2);
+            const uint16_t* const src = qg + (int64_t)tok * p.q.b_stride + (int64_t)(r2 - tok * g) * p.q.h_stride;
+            if (a.q_wide) {
+              val[k] = __ldg(reinterpret_cast<const uint4*>(src));
+            } else {
+              uint32_t e[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) e[j] = (uint32_t)src[2 * j] | ((uint32_t)src[2 * j + 1] << 16);
+              val[k] = make_uint4(e[0], e[1], e[2], e[3]);
+            }
           }
-          *reinterpret_cast<uint4*>(qs + (ch >> 3) * (TILE * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4)) = val;
+#pragma unroll
+          for (int k = 0; k < BATCH; ++k)
+            if ((int)row + k * ROWS_A_ROUND < to)
+              *reinterpret_cast<uint4*>(qs + at0 + (row + k * ROWS_A_ROUND) * 128) = val[k];
         }
         fence_proxy_async_smem();
         mbar_arrive(&sh.q_full[t]);
@@ -623,8 +656,14 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (__any_sync(0xffffffffu, k0 + UNIT > hi || k0 < lo)) {
             const int from = lo - k0, to = hi - k0;
 #pragma unroll
-            for (int i = 0; i < UNIT; ++i)
-              if (i < from || i >= to) s[i] = 0xff800000u;  // -inf
+            for (int b = 0; b < UNIT; b += 32) {
+              // bits [from, to) of this block
+              const int f0 = min(max(from - b, 0), 32), t0 = min(max(to - b, 0), 32);
+              const uint32_t bits = low_bits(t0) & ~low_bits(f0);
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!(bits >> i & 1u)) s[b + i] = 0xff800000u;  // -inf
+            }
           }
           float top = -INFINITY;
 #pragma unroll
@@ -639,15 +678,14 @@ __global__ void __launch_bounds__(THREADS, 1)
               alive = warp_wait(&sh.o_done[t], (seen_s - 1) & 1);
               if (!alive) break;
               tc_fence_after();
+#pragma unroll 1
+              for (int i = 0; i < D; i += 16) {  // 16 columns at a time: the 128 scores stay in registers
+                float o[16];
+                tmem_ld16(o_addr + i, o);
+                uint32_t o2[16];
 #pragma unroll
-              for (int i = 0; i < D; i += 32) {
-                uint32_t o[32];
-                ld32(o_addr + i, o);
-                ld_wait();
-                hold32(o);
-#pragma unroll
-                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * fade);
-                st32(o_addr + i, o);
+                for (int j = 0; j < 16; ++j) o2[j] = __float_as_uint(o[j] * fade);
+                tmem_st16(o_addr + i, o2);
               }
             }
           }
@@ -699,8 +737,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       const bool writes = (dual || t == 0) && valid;
       const int64_t row = (int64_t)sg.row0 + tok;
       const int qh = sg.head * g + head_of_row;
-      const int slot_id = sg.part == 0 ? 2 * (int)cta + 1 : 2 * (int)cta;
+      const int slot_id = sg.part == 0 ? 2 * cta + 1 : 2 * cta;
       const int part_row = (dual ? t * TILE : 0) + x;
+      uint8_t* const tile = smem + (dual && t ? S::Q1 : S::Q0);
       const bool none = l == 0.f;  // no key: zeros
       const float inv = 1.f / l;
       float* const other = reinterpret_cast<float*>(smem + S::Q1);  // the second group's O, half the columns at a time
@@ -737,21 +776,14 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             if (writes) {
               const int col = h * (D / 2) + i;
-              if (direct) {
-                uint16_t* const dst = static_cast<uint16_t*>(p.out) + row * p.out_b_stride + (int64_t)qh * p.out_h_stride + col;
-                uint32_t b[16];
+              if (direct) {  // into the tile's own queries' place, which the products are done with
 #pragma unroll
-                for (int j = 0; j < 16; ++j) b[j] = none ? 0u : pack_bf16x2(f[2 * j] * inv, f[2 * j + 1] * inv);
-                if (a.out_wide) {
+                for (int j = 0; j < 4; ++j) {
+                  uint32_t b[4];
 #pragma unroll
-                  for (int j = 0; j < 4; ++j)
-                    reinterpret_cast<uint4*>(dst)[j] = make_uint4(b[4 * j], b[4 * j + 1], b[4 * j + 2], b[4 * j + 3]);
-                } else {
-#pragma unroll
-                  for (int j = 0; j < 16; ++j) {
-                    dst[2 * j] = (uint16_t)b[j];
-                    dst[2 * j + 1] = (uint16_t)(b[j] >> 16);
-                  }
+                  for (int e = 0; e < 4; ++e)
+                    b[e] = none ? 0u : pack_bf16x2(f[8 * j + 2 * e] * inv, f[8 * j + 2 * e + 1] * inv);
+                  *reinterpret_cast<uint4*>(tile + tile_chunk(x, col / 8 + j)) = make_uint4(b[0], b[1], b[2], b[3]);
                 }
               } else {
 #pragma unroll
@@ -765,6 +797,32 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (two && h == 0) bar_sync(2, SOFTMAX_THREADS);
       }
       tc_fence_before();
+      if (direct && (dual || t == 0)) {
+        if (t == 0)
+          bar_sync(3, TILE);
+        else
+          bar_sync(4, TILE);
+        const int tile0 = dual ? t * tpt : 0, rows = min(sg.ntok - tile0, tpt) * g;
+        uint16_t* const og = static_cast<uint16_t*>(p.out) + (int64_t)(sg.row0 + tile0) * p.out_b_stride +
+                             (int64_t)(sg.head * g) * p.out_h_stride + my_ch * 8;
+        const uint32_t at0 = tile_chunk(my_row, my_ch) - my_row * 128;
+#pragma unroll 4
+        for (int row2 = my_row; row2 < rows; row2 += ROWS_A_ROUND) {
+          const uint4 v = *reinterpret_cast<const uint4*>(tile + at0 + row2 * 128);
+          const int tk = div_g(row2);
+          uint16_t* const dst = og + (int64_t)tk * p.out_b_stride + (int64_t)(row2 - tk * g) * p.out_h_stride;
+          if (a.out_wide) {
+            *reinterpret_cast<uint4*>(dst) = v;
+          } else {
+            const uint32_t e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              dst[2 * j] = (uint16_t)e[j];
+              dst[2 * j + 1] = (uint16_t)(e[j] >> 16);
+            }
+          }
+        }
+      }
       if (writes) {
         if (direct) {
           if (p.lse != nullptr) p.lse[row * p.num_q_heads + qh] = m == -INFINITY ? -INFINITY : m * p.scale + logf(l);
