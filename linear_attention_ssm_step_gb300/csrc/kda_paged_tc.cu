@@ -24,7 +24,7 @@
 //
 // A CTA is twelve warps: two softmax groups of four (a thread per row), a warp
 // each that loads keys and values (one tensor-map copy per page and 64
-// columns), that issues the products, and that walks the line. With two row
+// columns), that issues either product, and that walks the line. With two row
 // tiles, group t owns tile t; a single tile (decode, verify) takes the units in
 // turn with the groups, each with its own O, joined at the end, so that in
 // either case one group's exponentials run while the other's products do.
@@ -44,7 +44,7 @@ constexpr int UNIT = 128;   // keys a unit
 constexpr int TILE = 128;   // rows a tile
 constexpr int THREADS = 384;
 constexpr int SOFTMAX_THREADS = 256;
-constexpr int K_WARP = 8, V_WARP = 9, MMA_WARP = 10, WALK_WARP = 11;
+constexpr int LOAD_WARP = 8, VALUE_WARP = 9, SCORE_WARP = 10, WALK_WARP = 11;
 constexpr int RING = 4;  // segments the walking warp may be ahead
 // What an item costs beside its units (its queries, its end), in units: each item takes LEAD + its units of the line.
 constexpr int LEAD = 2;
@@ -76,7 +76,7 @@ struct Segment {
 
 struct Shared {
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
-  uint64_t v_tail, q_full[2], s_full[2], p_full[2], o_done[2], seg_full[RING], seg_empty[RING], drain;
+  uint64_t v_tail, q_full[2], s_full[2], p_full[2][2], o_done[2], seg_full[RING], seg_empty[RING], drain[2];
   Segment seg[RING];
   float m1[TILE], l1[TILE];  // the second group's m and l when both groups share a tile
   long long warp_sum[THREADS / 32];
@@ -183,13 +183,61 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// Two fp32 at once: x y + z, x + y.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
+// The largest of three (a NaN among them is passed over).
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
+
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
+// mbar_wait_bounded with the clock read only after some tries: a wait here is mostly for what is just about to come,
+// and reading the clock takes longer than the wait.
+__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity) {
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait_bounded(bar, parity);
+}
+
 // A wait of a whole warp; false for every lane if it gave up for any.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity));
+  return __all_sync(0xffffffffu, wait_bounded(bar, parity));
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t on;
+  asm volatile("{\n\t.reg .pred p;\n\t.reg .b32 r;\n\telect.sync r|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(on));
+  return on != 0;
+}
+
+// Lane 0's value, for the compiler to keep as one of the whole warp.
+template <typename T>
+__device__ __forceinline__ T uniform(T x) {
+  return __shfl_sync(0xffffffffu, x, 0);
 }
 
 // A barrier of `count` threads that tells all of them whether `x` held for any.
@@ -263,16 +311,17 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(&sh.v_empty[i], 1);
     }
     mbar_init(&sh.v_tail, 1);
-    mbar_init(&sh.drain, 1);
+    mbar_init(&sh.drain[0], 1);
+    mbar_init(&sh.drain[1], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.q_full[i], TILE);
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_full[i], TILE);
+      for (int h = 0; h < 2; ++h) mbar_init(&sh.p_full[i][h], TILE / 32);  // an arrival a warp
       mbar_init(&sh.o_done[i], 1);
     }
     for (int i = 0; i < RING; ++i) {
       mbar_init(&sh.seg_full[i], 1);
-      mbar_init(&sh.seg_empty[i], 5);  // key, value and product warps, both softmax groups
+      mbar_init(&sh.seg_empty[i], 5);  // the loading warp, two product warps, both softmax groups
     }
     sh.start_request = -1;
   }
@@ -328,7 +377,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       prefix += all;
     }
   }
-  if (warp == MMA_WARP) tmem_alloc(&sh.tmem, 512);
+  if (warp == SCORE_WARP) tmem_alloc(&sh.tmem, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -432,19 +481,31 @@ __global__ void __launch_bounds__(THREADS, 1)
           mbar_arrive(&sh.seg_full[slot]);
         }
       }
-    } else if (warp == K_WARP || warp == V_WARP) {
-      // ---- keys or values of the CTA's units, a lane per copy
-      const bool values = warp == V_WARP;
-      const CUtensorMap* const map = values ? &vmap : &kmap;
-      const int stages = values ? S::V_STAGES : S::K_STAGES;
-      uint8_t* const ring = smem + (values ? S::V0 : S::K0);
-      uint64_t* const full = values ? sh.v_full : sh.k_full;
-      uint64_t* const empty = values ? sh.v_empty : sh.k_empty;
+    } else if (warp == LOAD_WARP) {
+      // ---- keys and values of the CTA's units, a lane per copy; keys one unit ahead
       const int P = p.cache.page_size, box = a.box;
       const int copies = (UNIT / box) * (D / 64);
       const int piece = lane / (D / 64), half = lane % (D / 64);  // which keys of the unit, which columns
-      uint32_t n = 0, tails = 0;
-      bool bad_page = false;
+      uint32_t kn = 0, vn = 0, tails = 0;
+      bool bad_page = false, pending = false;  // pending: a ragged unit of values is on its way
+      int first = 0, last = UNIT;              // the keys of it that are in use
+      // Weights of unseen keys are zero, but zero times what lies there need not be: clear those rows. Done when the next
+      // values are to be loaded, so that the keys of the next run do not wait for it.
+      auto clear_tail = [&]() {
+        pending = false;
+        if (!warp_wait(&sh.v_tail, tails & 1)) return false;
+        ++tails;
+        const uint32_t st = (vn - 1) % S::V_STAGES;
+        uint8_t* const dst = smem + S::V0 + st * S::TILE_BYTES;
+        for (int x = lane; x < TILE * (D / 8); x += 32) {
+          const int row = (x >> 3) & (TILE - 1);
+          if (row < first || row >= last) *reinterpret_cast<uint4*>(dst + x * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.v_full[st]);
+        return true;
+      };
       for (uint32_t in = 0; alive; ++in) {
         const uint32_t slot = in % RING;
         alive = warp_wait(&sh.seg_full[slot], (in / RING) & 1);
@@ -454,8 +515,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (lane == 0) mbar_arrive(&sh.seg_empty[slot]);
         if (sg.ntok < 0) break;
         const int32_t* const table = p.table + (int64_t)sg.request * p.table_stride;
-        for (int u = sg.u0; u < sg.u1; ++u) {
-          // up to 32 copies a round; a unit of 128 keys in pages of 16 has 8 pieces, 16 copies
+        // up to 32 copies: a unit of 128 keys of 128 columns in pages of 16 is 8 pieces, 16 copies
+        auto load = [&](int u, bool values) {
           const int key = u * UNIT + piece * box;
           const bool wanted = lane < copies && key < sg.hi && key + box > sg.lo;
           int page = 0;
@@ -466,102 +527,125 @@ __global__ void __launch_bounds__(THREADS, 1)
               bad_page = true;
             }
           }
-          const uint32_t st = n % stages;
-          alive = warp_wait(&empty[st], (n / stages + 1) & 1);
-          if (!alive) break;
-          uint8_t* const dst = ring + st * S::TILE_BYTES;
+          const uint32_t n = values ? vn : kn, stages = values ? S::V_STAGES : S::K_STAGES, st = n % stages;
+          if (!warp_wait(values ? &sh.v_empty[st] : &sh.k_empty[st], (n / stages + 1) & 1)) return false;
+          uint8_t* const dst = smem + (values ? S::V0 : S::K0) + st * S::TILE_BYTES;
           const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, wanted)) * (uint32_t)box * 128u;
-          const int first = max(sg.lo - u * UNIT, 0), last = min(sg.hi - u * UNIT, UNIT);  // the unit's keys in use
-          const bool ragged = values && (first > 0 || last < UNIT);
-          uint64_t* const bar = ragged ? &sh.v_tail : &full[st];
+          uint64_t* bar = values ? &sh.v_full[st] : &sh.k_full[st];
+          if (values) {
+            first = max(sg.lo - u * UNIT, 0);
+            last = min(sg.hi - u * UNIT, UNIT);
+            pending = first > 0 || last < UNIT;
+            if (pending) bar = &sh.v_tail;
+            ++vn;
+          } else {
+            ++kn;
+          }
           if (lane == 0) mbar_expect_tx(bar, bytes);
           __syncwarp();
           if (wanted)
-            tma_load_4d(dst + half * (TILE * 128) + piece * box * 128, map, half * 64, key % P, sg.head, page, bar);
-          if (ragged) {
-            // weights of unseen keys are zero, but zero times what lies there need not be: clear those rows
-            alive = warp_wait(&sh.v_tail, tails & 1);
-            if (!alive) break;
-            ++tails;
-            for (int x = lane; x < TILE * (D / 8); x += 32) {
-              const int row = (x >> 3) & (TILE - 1);
-              if (row < first || row >= last) *reinterpret_cast<uint4*>(dst + x * 16) = make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&full[st]);
-          }
-          ++n;
+            tma_load_4d(dst + half * (TILE * 128) + piece * box * 128, values ? &vmap : &kmap, half * 64, key % P, sg.head,
+                        page, bar);
+          return true;
+        };
+        alive = load(sg.u0, false);
+        for (int u = sg.u0; alive && u < sg.u1; ++u) {
+          if (u + 1 < sg.u1) alive = load(u + 1, false);
+          if (alive && pending) alive = clear_tail();
+          if (alive) alive = load(u, true);
         }
       }
+      if (alive && pending) alive = clear_tail();
       if (bad_page && p.error_word) atomicOr(p.error_word, KDA_ERR_PAGES);
       if (!alive) {  // copies in flight land before the CTA leaves
-        if (values) mbar_drain_bounded(&sh.v_tail, tails & 1);
-        for (uint32_t i = n > (uint32_t)stages ? n - stages : 0; i < n; ++i)
-          mbar_drain_bounded(&full[i % stages], (i / stages) & 1);
+        mbar_drain_bounded(&sh.v_tail, tails & 1);
+        for (uint32_t i = kn > (uint32_t)S::K_STAGES ? kn - S::K_STAGES : 0; i < kn; ++i)
+          mbar_drain_bounded(&sh.k_full[i % S::K_STAGES], (i / S::K_STAGES) & 1);
+        for (uint32_t i = vn > (uint32_t)S::V_STAGES ? vn - S::V_STAGES : 0; i < vn; ++i)
+          mbar_drain_bounded(&sh.v_full[i % S::V_STAGES], (i / S::V_STAGES) & 1);
       }
     } else {
-      // ---- the products
-      uint32_t kn = 0, vn = 0, seen_p[2] = {0, 0}, segs = 0;  // units of keys and values taken, weights waited for
-      const uint32_t smem_base = smem_addr(smem);
+      // ---- the products: one warp issues the scores', the other the values', so that either's waits pass while the other's
+      // products run (a product takes 64 cycles of the tensor core, and its issue waits for room in a short queue). The
+      // warps stay together, what they read from shared memory broadcast from one lane, and an elected lane issues.
+      const bool values = warp == VALUE_WARP;
+      uint32_t n0 = 0, seen0 = 0, seen1 = 0, segs = 0;  // units taken from the ring; products of each tile asked for
+      const uint32_t smem_base = uniform(smem_addr(smem)), sc = uniform(S_COL), oc = uniform(O_COL);
       constexpr uint32_t IDESC_S = idesc_bf16_f32(TILE, UNIT);
       constexpr uint32_t IDESC_O = idesc_bf16_f32(TILE, D) | B_MN_MAJOR;
       for (uint32_t in = 0; alive; ++in) {
         const uint32_t slot = in % RING;
         alive = warp_wait(&sh.seg_full[slot], (in / RING) & 1);
         if (!alive) break;
-        const Segment sg = sh.seg[slot];
+        const int ntok = uniform(sh.seg[slot].ntok), n = uniform(sh.seg[slot].u1 - sh.seg[slot].u0);
+        const int dual = uniform(sh.seg[slot].dual);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.seg_empty[slot]);
-        if (sg.ntok < 0) break;
-        alive = warp_wait(&sh.q_full[0], segs & 1) && warp_wait(&sh.q_full[1], segs & 1);
-        ++segs;
-        if (!alive) break;
-        const int n = sg.u1 - sg.u0, dual = sg.dual, steps = dual ? 2 * n : n;
-        const uint32_t k0 = kn, v0 = vn;  // the run's first units in the rings
-        kn += n;
-        vn += n;
-        auto scores = [&](int s) {  // S of step s: tile s & 1
-          const int t = s & 1;
-          const uint32_t u = k0 + (dual ? s >> 1 : s), st = u % S::K_STAGES;
-          if (!dual || t == 0) {
-            if (!warp_wait(&sh.k_full[st], (u / S::K_STAGES) & 1)) return false;
-            tc_fence_after();
-          }
-          const uint32_t q = smem_base + (dual && t ? S::Q1 : S::Q0), k = smem_base + S::K0 + st * S::TILE_BYTES;
-#pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
-            const uint32_t off = (i >> 2) * (TILE * 128) + (i & 3) * 32;
-            tc_mma_bf16_w(S_COL + t * TILE, sw128_desc(q + off), sw128_desc(k + off), IDESC_S, i > 0);
-          }
-          if (!dual || t == 1) tc_commit_w(&sh.k_empty[st]);
-          tc_commit_w(&sh.s_full[t]);
-          return true;
-        };
-        alive = scores(0) && (steps < 2 || scores(1));
-        for (int s = 0; alive && s < steps; ++s) {
-          const int t = s & 1;
-          const uint32_t u = v0 + (dual ? s >> 1 : s), st = u % S::V_STAGES;
-          if (!dual || t == 0) alive = warp_wait(&sh.v_full[st], (u / S::V_STAGES) & 1);
-          alive = alive && warp_wait(&sh.p_full[t], seen_p[t] & 1);
-          if (!alive) break;
-          ++seen_p[t];
-          tc_fence_after();
-          const uint32_t v = smem_base + S::V0 + st * S::TILE_BYTES;
-#pragma unroll
-          for (int i = 0; i < UNIT / 16; ++i)
-            tc_mma_bf16_ta_w(O_COL + t * D, S_COL + t * TILE + i * 8, value_desc(v + i * 2048), IDESC_O, s > 1 || i > 0);
-          if (!dual || t == 1) tc_commit_w(&sh.v_empty[st]);
-          tc_commit_w(&sh.o_done[t]);
-          if (s + 2 < steps) alive = scores(s + 2);
+        if (ntok < 0) break;
+        const int steps = dual ? 2 * n : n;
+        if (!values) {
+          alive = warp_wait(&sh.q_full[0], segs & 1) && warp_wait(&sh.q_full[1], segs & 1);
+          ++segs;
         }
+        for (int s = 0; alive && s < steps; ++s) {  // step s: tile s & 1
+          const int t = s & 1;
+          const uint32_t u = n0 + (dual ? s >> 1 : s);
+          const bool first_use = !dual || t == 0, last_use = !dual || t == 1;
+          if (!values) {
+            const uint32_t st = u % S::K_STAGES;
+            if (first_use) alive = warp_wait(&sh.k_full[st], (u / S::K_STAGES) & 1);
+            // the tile's weights before these scores are used up (before its first, the queries' arrival says so)
+            if (alive && s >= 2) alive = warp_wait(&sh.o_done[t], ((t ? seen1 : seen0) + 1) & 1);
+            if (!alive) break;
+            tc_fence_after();
+            const uint32_t q = smem_base + (dual && t ? S::Q1 : S::Q0), k = smem_base + S::K0 + st * S::TILE_BYTES;
+            if (elect_one()) {
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) {
+                const uint32_t off = (i >> 2) * (TILE * 128) + (i & 3) * 32;
+                tc_mma_bf16(sc + t * TILE, sw128_desc(q + off), sw128_desc(k + off), IDESC_S, i > 0);
+              }
+              tc_commit(&sh.s_full[t]);
+              if (last_use) tc_commit(&sh.k_empty[st]);
+            }
+            __syncwarp();
+          } else {
+            const uint32_t st = u % S::V_STAGES;
+            const uint32_t v = smem_base + S::V0 + st * S::TILE_BYTES;
+            if (first_use) alive = warp_wait(&sh.v_full[st], (u / S::V_STAGES) & 1);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              alive = alive && warp_wait(&sh.p_full[t][h], (t ? seen1 : seen0) & 1);
+              if (!alive) break;
+              tc_fence_after();
+              if (elect_one()) {
+#pragma unroll
+                for (int i = h * (UNIT / 32); i < (h + 1) * (UNIT / 32); ++i)
+                  tc_mma_bf16_ta(oc + t * D, sc + t * TILE + i * 8, value_desc(v + i * 2048), IDESC_O, s > 1 || i > 0);
+                if (h == 1) {
+                  tc_commit(&sh.o_done[t]);
+                  if (last_use) tc_commit(&sh.v_empty[st]);
+                }
+              }
+              __syncwarp();
+            }
+            if (!alive) break;
+          }
+          if (t)
+            ++seen1;
+          else
+            ++seen0;
+        }
+        n0 += n;
       }
       if (!alive) {  // products in flight end before the tensor memory goes
-        tc_commit_w(&sh.drain);
-        mbar_drain_bounded(&sh.drain, 0);
+        uint64_t* const drain = &sh.drain[values ? 1 : 0];
+        tc_commit_w(drain);
+        mbar_drain_bounded(drain, 0);
       }
     }
     if (!alive && lane == 0 && p.error_word) atomicOr(p.error_word, KDA_ERR_TIMEOUT);
+    __syncwarp();
   } else {
     // ---- softmax: group t, thread (row) x
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SOFTMAX_REGS));
@@ -569,7 +653,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_addr = S_COL + t * TILE + lane_base, o_addr = O_COL + t * D + lane_base;
     const float c = p.scale * LOG2E;
-    uint32_t seen_s = 0;  // scores waited for; as many products with values were asked for
+    uint32_t seen_s = 0;  // scores waited for: as many products with values were asked for
     bool alive = true;
     // row / g for row < 128 and g <= 128: the product's excess is below 128 / 2^16 < 1 / g
     const uint32_t inv_g = 65536u / (uint32_t)g + 1u;
@@ -665,19 +749,20 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (!(bits >> i & 1u)) s[b + i] = 0xff800000u;  // -inf
             }
           }
-          float top = -INFINITY;
+          float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int i = 0; i < UNIT; ++i) top = fmaxf(top, __uint_as_float(s[i]));
+          for (int i = 0; i < UNIT; i += 8)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              tops[j] = max3(tops[j], __uint_as_float(s[i + 2 * j]), __uint_as_float(s[i + 2 * j + 1]));
+          const float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]);
           const bool first = units == 0;
           const bool grown = top > m && (top - m) * c > SLACK;  // m = -inf: any key
           if (__any_sync(0xffffffffu, grown)) {
             const float fade = grown ? ex2((m - top) * c) : 1.f;
             if (grown) m = top;
             l *= fade;
-            if (!first) {
-              alive = warp_wait(&sh.o_done[t], (seen_s - 1) & 1);
-              if (!alive) break;
-              tc_fence_after();
+            if (!first) {  // the product of the unit before is done: these scores waited for it
 #pragma unroll 1
               for (int i = 0; i < D; i += 16) {  // 16 columns at a time: the 128 scores stay in registers
                 float o[16];
@@ -690,27 +775,36 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
           }
           const float base = m == -INFINITY ? 0.f : -m * c;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          const uint64_t c2 = pair(c, c), base2 = pair(base, base);
+          uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
-          for (int i = 0; i < UNIT; i += 64) {
+          for (int i = 0; i < UNIT; i += UNIT / 2) {
+            // half the weights, then the products that take them may start
             uint32_t w2[32];
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
-              const float e0 = ex2(fmaf(__uint_as_float(s[i + 2 * j]), c, base));
-              const float e1 = ex2(fmaf(__uint_as_float(s[i + 2 * j + 1]), c, base));
-              sum[j & 1] += e0;
-              sum[2 + (j & 1)] += e1;
+              float e0, e1;
+              unpair(fma2(pair(__uint_as_float(s[i + 2 * j]), __uint_as_float(s[i + 2 * j + 1])), c2, base2), e0, e1);
+              e0 = ex2(e0);
+              e1 = ex2(e1);
+              sum[j & 3] = add2(sum[j & 3], pair(e0, e1));
               w2[j] = pack_bf16x2(e0, e1);
             }
             st32(s_addr + i / 2, w2);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.p_full[t][i / (UNIT / 2)]);
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-          tmem_st_wait();
-          tc_fence_before();
+          float l0, l1;
+          unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), l0, l1);
+          l += l0 + l1;
+        } else if (lane == 0) {
+          mbar_arrive(&sh.p_full[t][0]);
+          mbar_arrive(&sh.p_full[t][1]);
         }
         ++seen_s;
         ++units;
-        mbar_arrive(&sh.p_full[t]);
       }
 
       // ---- the end of the run
@@ -935,7 +1029,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == MMA_WARP) tmem_dealloc(tmem, 512);
+  if (warp == SCORE_WARP) tmem_dealloc(tmem, 512);
 }
 
 size_t paged_attention_parts_bytes(int head_dim, int ctas) {
