@@ -45,6 +45,7 @@ constexpr int TILE = 128;   // rows a tile
 constexpr int THREADS = 384;
 constexpr int SOFTMAX_THREADS = 256;
 constexpr int LOAD_WARP = 8, VALUE_WARP = 9, SCORE_WARP = 10, WALK_WARP = 11;
+constexpr int FIRST = 96;   // keys of a unit whose weights are handed over first, while the others' are formed
 constexpr int RING = 4;  // segments the walking warp may be ahead
 // What an item costs beside its units (its queries, its end), in units: each item takes LEAD + its units of the line.
 constexpr int LEAD = 2;
@@ -177,6 +178,15 @@ __device__ __forceinline__ void st32(uint32_t taddr, const uint32_t* v) {
       : "memory");
 }
 
+__device__ __forceinline__ void st16(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -207,6 +217,26 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
   return r;
+}
+
+// -m c twice; 0 for a row that has seen no key.
+__device__ __forceinline__ uint64_t reference(float m, float c) {
+  const float base = m == -INFINITY ? 0.f : -m * c;
+  return pair(base, base);
+}
+
+// Weights exp2(c s + base) of N scores, in bf16 pairs; their fp32 sums are added to `sum`.
+template <int N>
+__device__ __forceinline__ void weights(const uint32_t* s, uint64_t c2, uint64_t base2, uint64_t (&sum)[4], uint32_t* w) {
+#pragma unroll
+  for (int j = 0; j < N / 2; ++j) {
+    float e0, e1;
+    unpair(fma2(pair(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), c2, base2), e0, e1);
+    e0 = ex2(e0);
+    e1 = ex2(e1);
+    sum[j & 3] = add2(sum[j & 3], pair(e0, e1));
+    w[j] = pack_bf16x2(e0, e1);
+  }
 }
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
@@ -620,7 +650,7 @@ __global__ void __launch_bounds__(THREADS, 1)
               tc_fence_after();
               if (elect_one()) {
 #pragma unroll
-                for (int i = h * (UNIT / 32); i < (h + 1) * (UNIT / 32); ++i)
+                for (int i = h ? FIRST / 16 : 0; i < (h ? UNIT : FIRST) / 16; ++i)
                   tc_mma_bf16_ta(oc + t * D, sc + t * TILE + i * 8, value_desc(v + i * 2048), IDESC_O, s > 1 || i > 0);
                 if (h == 1) {
                   tc_commit(&sh.o_done[t]);
@@ -719,8 +749,10 @@ __global__ void __launch_bounds__(THREADS, 1)
 
       const int tok = (dual ? t * tpt : 0) + token_of_row;
       const bool valid = token_of_row < tpt && tok < sg.ntok;
-      const int hi = valid ? sg.pos0 + tok + 1 : 0;  // this row sees keys [lo, hi)
-      const int lo = window > 0 ? max(0, hi - window) : 0;
+      // this row sees keys [lo, hi); a row of no token is carried along unmasked and goes nowhere
+      const int hi = valid ? sg.pos0 + tok + 1 : 0x7fffffff;
+      const int lo = valid && window > 0 ? max(0, hi - window) : 0;
+      const int all_lo = __reduce_max_sync(0xffffffffu, lo), all_hi = __reduce_min_sync(0xffffffffu, hi);
       const bool warp_valid = __any_sync(0xffffffffu, valid);
       float m = -INFINITY, l = 0.f;  // m: the reference, in units of the scores
       const int step = dual ? 1 : 2;
@@ -737,18 +769,23 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
           for (int i = 0; i < UNIT; i += 32) hold32(s + i);
           const int k0 = u * UNIT;
-          if (__any_sync(0xffffffffu, k0 + UNIT > hi || k0 < lo)) {
+          if (k0 + UNIT > all_hi || k0 < all_lo) {
             const int from = lo - k0, to = hi - k0;
 #pragma unroll
             for (int b = 0; b < UNIT; b += 32) {
               // bits [from, to) of this block
-              const int f0 = min(max(from - b, 0), 32), t0 = min(max(to - b, 0), 32);
-              const uint32_t bits = low_bits(t0) & ~low_bits(f0);
+              const uint32_t bits = low_bits(min(max(to - b, 0), 32)) & ~low_bits(min(max(from - b, 0), 32));
 #pragma unroll
               for (int i = 0; i < 32; ++i)
                 if (!(bits >> i & 1u)) s[b + i] = 0xff800000u;  // -inf
             }
           }
+          // The first weights by the reference so far, and beside them (in another pipe) the maximum: only if that has
+          // grown past the slack are they formed again.
+          const uint64_t c2 = pair(c, c);
+          uint64_t sum[4] = {0, 0, 0, 0}, base2 = reference(m, c);
+          uint32_t wa[16];
+          weights<32>(s, c2, base2, sum, wa);
           float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
           for (int i = 0; i < UNIT; i += 8)
@@ -756,13 +793,12 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int j = 0; j < 4; ++j)
               tops[j] = max3(tops[j], __uint_as_float(s[i + 2 * j]), __uint_as_float(s[i + 2 * j + 1]));
           const float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]);
-          const bool first = units == 0;
-          const bool grown = top > m && (top - m) * c > SLACK;  // m = -inf: any key
+          const bool grown = valid && top > m && (top - m) * c > SLACK;  // m = -inf: any key
           if (__any_sync(0xffffffffu, grown)) {
             const float fade = grown ? ex2((m - top) * c) : 1.f;
             if (grown) m = top;
             l *= fade;
-            if (!first) {  // the product of the unit before is done: these scores waited for it
+            if (units > 0) {  // the product of the unit before is done: these scores waited for it
 #pragma unroll 1
               for (int i = 0; i < D; i += 16) {  // 16 columns at a time: the 128 scores stay in registers
                 float o[16];
@@ -773,29 +809,25 @@ __global__ void __launch_bounds__(THREADS, 1)
                 tmem_st16(o_addr + i, o2);
               }
             }
+            base2 = reference(m, c);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sum[j] = 0;
+            weights<32>(s, c2, base2, sum, wa);
           }
-          const float base = m == -INFINITY ? 0.f : -m * c;
-          const uint64_t c2 = pair(c, c), base2 = pair(base, base);
-          uint64_t sum[4] = {0, 0, 0, 0};
-#pragma unroll
-          for (int i = 0; i < UNIT; i += UNIT / 2) {
-            // half the weights, then the products that take them may start
-            uint32_t w2[32];
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              float e0, e1;
-              unpair(fma2(pair(__uint_as_float(s[i + 2 * j]), __uint_as_float(s[i + 2 * j + 1])), c2, base2), e0, e1);
-              e0 = ex2(e0);
-              e1 = ex2(e1);
-              sum[j & 3] = add2(sum[j & 3], pair(e0, e1));
-              w2[j] = pack_bf16x2(e0, e1);
-            }
-            st32(s_addr + i / 2, w2);
+          auto give = [&](int h) {  // these weights are there: the products that take them may start
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.p_full[t][i / (UNIT / 2)]);
-          }
+            if (lane == 0) mbar_arrive(&sh.p_full[t][h]);
+          };
+          st16(s_addr, wa);
+          uint32_t wb[32];
+          weights<64>(s + 32, c2, base2, sum, wb);
+          st32(s_addr + 16, wb);
+          give(0);
+          weights<32>(s + FIRST, c2, base2, sum, wa);
+          st16(s_addr + FIRST / 2, wa);
+          give(1);
           float l0, l1;
           unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), l0, l1);
           l += l0 + l1;
