@@ -24,12 +24,14 @@
 //
 // A CTA is twelve warps: two softmax groups of four (a thread per row), a warp
 // each that loads keys and values (one tensor-map copy per page and 64
-// columns), that issues either product, and that walks the line. With two row
+// columns), that issues the products, and that walks the line. With two row
 // tiles, group t owns tile t; a single tile (decode, verify) takes the units in
 // turn with the groups, each with its own O, joined at the end, so that in
 // either case one group's exponentials run while the other's products do.
-// S and P share tensor-memory columns: P (bf16) overwrites the S it came from
-// and enters the second product from there.
+// Tensor memory holds one S that both groups take in turn (a group has its row
+// in registers 250 cycles after the product, and the next product may start), P
+// (bf16) and O of each: 128 + 2 x 64 + 2 x D columns. So the first product never
+// waits for a group's exponentials or its second product.
 #include <math.h>
 
 #include "kda_paged.cuh"
@@ -44,8 +46,7 @@ constexpr int UNIT = 128;   // keys a unit
 constexpr int TILE = 128;   // rows a tile
 constexpr int THREADS = 384;
 constexpr int SOFTMAX_THREADS = 256;
-constexpr int LOAD_WARP = 8, VALUE_WARP = 9, SCORE_WARP = 10, WALK_WARP = 11;
-constexpr int FIRST = 96;   // keys of a unit whose weights are handed over first, while the others' are formed
+constexpr int LOAD_WARP = 8, PRODUCT_WARP = 9, WALK_WARP = 10;  // the twelfth idles
 constexpr int RING = 4;  // segments the walking warp may be ahead
 // What an item costs beside its units (its queries, its end), in units: each item takes LEAD + its units of the line.
 constexpr int LEAD = 2;
@@ -77,7 +78,7 @@ struct Segment {
 
 struct Shared {
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
-  uint64_t v_tail, q_full[2], s_full[2], p_full[2][2], o_done[2], seg_full[RING], seg_empty[RING], drain[2];
+  uint64_t v_tail, q_full[2], s_full[2], p_full[2], s_free, o_done[2], seg_full[RING], seg_empty[RING], drain;
   Segment seg[RING];
   float m1[TILE], l1[TILE];  // the second group's m and l when both groups share a tile
   long long warp_sum[THREADS / 32];
@@ -178,15 +179,6 @@ __device__ __forceinline__ void st32(uint32_t taddr, const uint32_t* v) {
       : "memory");
 }
 
-__device__ __forceinline__ void st16(uint32_t taddr, const uint32_t* v) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15, %16};" ::"r"(taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-      : "memory");
-}
-
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -243,13 +235,19 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
-// mbar_wait_bounded with the clock read only after some tries: a wait here is mostly for what is just about to come,
-// and reading the clock takes longer than the wait.
+// mbar_wait_bounded with the clock read only every 64th try: reading it takes longer than most of the waits here last.
 __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity) {
+  unsigned long long t0 = 0;
 #pragma unroll 1
-  for (int i = 0; i < 64; ++i)
+  for (unsigned it = 1; it < WAIT_LIMIT_ITERS; ++it) {
     if (mbar_try_wait(bar, parity)) return true;
-  return mbar_wait_bounded(bar, parity);
+    if ((it & 63u) == 0) {
+      const unsigned long long now = global_timer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > WAIT_LIMIT_NS) return false;
+    }
+  }
+  return false;
 }
 
 // A wait of a whole warp; false for every lane if it gave up for any.
@@ -257,18 +255,70 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, wait_bounded(bar, parity));
 }
 
-// One lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t on;
-  asm volatile("{\n\t.reg .pred p;\n\t.reg .b32 r;\n\telect.sync r|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(on));
-  return on != 0;
+// D = A B^T over N / 16 K steps, issued by one elected lane of a converged warp, and then an arrival on `done` (and on
+// `free` if it is not 0) once they are complete. One statement, so that the descriptors of all steps are formed by adding
+// constants: the warp that issues runs on its own, and every instruction of it costs the tensor core five cycles or more.
+// A in shared memory, both operands K-major: a K step is 32 bytes, the fifth step on in the next 64-column region.
+template <int N>
+__device__ __forceinline__ void issue_scores(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t done, uint32_t free) {
+  static_assert(N == 64 || N == 128, "");
+  if constexpr (N == 128)
+    asm volatile(
+        "{\n\t.reg .pred p, q, t;\n\t.reg .b32 r;\n\t.reg .b64 x, y;\n\t"
+        "elect.sync r|p, 0xffffffff;\n\tsetp.ne.b32 t, 0, 0;\n\tsetp.eq.b32 q, 0, 0;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, t;\n\t"
+        "add.s64 x, %1, 2;\n\tadd.s64 y, %2, 2;\n\t@p tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, q;\n\t"
+        "add.s64 x, %1, 4;\n\tadd.s64 y, %2, 4;\n\t@p tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, q;\n\t"
+        "add.s64 x, %1, 6;\n\tadd.s64 y, %2, 6;\n\t@p tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, q;\n\t"
+        "add.s64 x, %1, 1024;\n\tadd.s64 y, %2, 1024;\n\t@p tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, q;\n\t"
+        "add.s64 x, %1, 1026;\n\tadd.s64 y, %2, 1026;\n\t@p tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, q;\n\t"
+        "add.s64 x, %1, 1028;\n\tadd.s64 y, %2, 1028;\n\t@p tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, q;\n\t"
+        "add.s64 x, %1, 1030;\n\tadd.s64 y, %2, 1030;\n\t@p tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, q;\n\t"
+        "@p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n\t"
+        "setp.ne.and.b32 p, %5, 0, p;\n\t"
+        "@p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(done), "r"(free)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p, q, t;\n\t.reg .b32 r;\n\t.reg .b64 x, y;\n\t"
+        "elect.sync r|p, 0xffffffff;\n\tsetp.ne.b32 t, 0, 0;\n\tsetp.eq.b32 q, 0, 0;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, t;\n\t"
+        "add.s64 x, %1, 2;\n\tadd.s64 y, %2, 2;\n\t@p tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, q;\n\t"
+        "add.s64 x, %1, 4;\n\tadd.s64 y, %2, 4;\n\t@p tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, q;\n\t"
+        "add.s64 x, %1, 6;\n\tadd.s64 y, %2, 6;\n\t@p tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, q;\n\t"
+        "@p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n\t"
+        "setp.ne.and.b32 p, %5, 0, p;\n\t"
+        "@p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(done), "r"(free)
+        : "memory");
 }
 
-// Lane 0's value, for the compiler to keep as one of the whole warp.
-template <typename T>
-__device__ __forceinline__ T uniform(T x) {
-  return __shfl_sync(0xffffffffu, x, 0);
+// D += A B over 128 keys (D = on the first if `fresh`), A (bf16 pairs) in tensor memory, 8 columns a K step; B with N
+// contiguous, 2048 bytes a K step.
+__device__ __forceinline__ void issue_values(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t fresh, uint32_t done,
+                                             uint32_t free) {
+  asm volatile(
+      "{\n\t.reg .pred p, q, t;\n\t.reg .b32 r, x;\n\t.reg .b64 y;\n\t"
+      "elect.sync r|p, 0xffffffff;\n\tsetp.eq.b32 t, %4, 0;\n\tsetp.eq.b32 q, 0, 0;\n\t"
+      "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, t;\n\t"
+      "add.u32 x, %1, 8;\n\tadd.s64 y, %2, 128;\n\t@p tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, q;\n\t"
+      "add.u32 x, %1, 16;\n\tadd.s64 y, %2, 256;\n\t@p tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, q;\n\t"
+      "add.u32 x, %1, 24;\n\tadd.s64 y, %2, 384;\n\t@p tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, q;\n\t"
+      "add.u32 x, %1, 32;\n\tadd.s64 y, %2, 512;\n\t@p tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, q;\n\t"
+      "add.u32 x, %1, 40;\n\tadd.s64 y, %2, 640;\n\t@p tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, q;\n\t"
+      "add.u32 x, %1, 48;\n\tadd.s64 y, %2, 768;\n\t@p tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, q;\n\t"
+      "add.u32 x, %1, 56;\n\tadd.s64 y, %2, 896;\n\t@p tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, q;\n\t"
+      "@p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t"
+      "setp.ne.and.b32 p, %6, 0, p;\n\t"
+      "@p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%6];\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(fresh), "r"(done), "r"(free)
+      : "memory");
 }
+
+// A value that all lanes hold, for the compiler to keep in a uniform register.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_max_sync(0xffffffffu, x); }
+__device__ __forceinline__ int uniform(int x) { return __reduce_max_sync(0xffffffffu, x); }
 
 // A barrier of `count` threads that tells all of them whether `x` held for any.
 __device__ __forceinline__ bool bar_any(uint32_t id, uint32_t count, bool x) {
@@ -322,8 +372,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                                   const __grid_constant__ AttnArgs a) {
   using S = Shape<D>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];  // the swizzle's atoms are 1024-byte aligned
   Shared& sh = *reinterpret_cast<Shared*>(smem + S::END);
   const kda_attention_params& p = a.p;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -341,17 +390,17 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(&sh.v_empty[i], 1);
     }
     mbar_init(&sh.v_tail, 1);
-    mbar_init(&sh.drain[0], 1);
-    mbar_init(&sh.drain[1], 1);
+    mbar_init(&sh.s_free, TILE / 32);
+    mbar_init(&sh.drain, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.q_full[i], TILE);
       mbar_init(&sh.s_full[i], 1);
-      for (int h = 0; h < 2; ++h) mbar_init(&sh.p_full[i][h], TILE / 32);  // an arrival a warp
+      mbar_init(&sh.p_full[i], TILE / 32);  // an arrival a warp
       mbar_init(&sh.o_done[i], 1);
     }
     for (int i = 0; i < RING; ++i) {
       mbar_init(&sh.seg_full[i], 1);
-      mbar_init(&sh.seg_empty[i], 5);  // the loading warp, two product warps, both softmax groups
+      mbar_init(&sh.seg_empty[i], 4);  // the loading warp, the product warp, both softmax groups
     }
     sh.start_request = -1;
   }
@@ -407,12 +456,14 @@ __global__ void __launch_bounds__(THREADS, 1)
       prefix += all;
     }
   }
-  if (warp == SCORE_WARP) tmem_alloc(&sh.tmem, 512);
+  if (warp == PRODUCT_WARP) tmem_alloc(&sh.tmem, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
-  const uint32_t S_COL = tmem, O_COL = tmem + 2 * TILE;
+  // columns: P of the first group, S, P of the second, O of either
+  const uint32_t P_COL = tmem, S_COL = tmem + UNIT / 2, O_COL = tmem + 2 * UNIT;
+  constexpr uint32_t P_STEP = UNIT / 2 + UNIT;
 
   if (warp >= SOFTMAX_THREADS / 32) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
@@ -594,15 +645,18 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (uint32_t i = vn > (uint32_t)S::V_STAGES ? vn - S::V_STAGES : 0; i < vn; ++i)
           mbar_drain_bounded(&sh.v_full[i % S::V_STAGES], (i / S::V_STAGES) & 1);
       }
-    } else {
-      // ---- the products: one warp issues the scores', the other the values', so that either's waits pass while the other's
-      // products run (a product takes 64 cycles of the tensor core, and its issue waits for room in a short queue). The
-      // warps stay together, what they read from shared memory broadcast from one lane, and an elected lane issues.
-      const bool values = warp == VALUE_WARP;
-      uint32_t n0 = 0, seen0 = 0, seen1 = 0, segs = 0;  // units taken from the ring; products of each tile asked for
-      const uint32_t smem_base = uniform(smem_addr(smem)), sc = uniform(S_COL), oc = uniform(O_COL);
+    } else if (warp == PRODUCT_WARP) {
+      // ---- the products, in one order: the scores of step s, then the values of a step before. The scores' 512 cycles are
+      // followed by their way into registers (300 more before the next may overwrite them), which the values' 512 cover;
+      // the weights of two steps before are ready by then. (A product takes 64 cycles, and its issue waits for room in a
+      // short queue. The warp stays together, what it reads from shared memory broadcast from one lane; an elected lane
+      // issues.)
+      const uint32_t base = smem_addr(smem), tm = uniform(tmem);
+      const uint32_t sc = tm + UNIT / 2;
       constexpr uint32_t IDESC_S = idesc_bf16_f32(TILE, UNIT);
       constexpr uint32_t IDESC_O = idesc_bf16_f32(TILE, D) | B_MN_MAJOR;
+      // Each ring's stage and phase; the phase of the scores' buffer and of either tile's weights; the runs' of the queries.
+      uint32_t ks = 0, kp = 0, vs = 0, vp = 0, sp = 1, wp[2] = {0, 0}, qp = 0;
       for (uint32_t in = 0; alive; ++in) {
         const uint32_t slot = in % RING;
         alive = warp_wait(&sh.seg_full[slot], (in / RING) & 1);
@@ -612,66 +666,57 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.seg_empty[slot]);
         if (ntok < 0) break;
-        const int steps = dual ? 2 * n : n;
-        if (!values) {
-          alive = warp_wait(&sh.q_full[0], segs & 1) && warp_wait(&sh.q_full[1], segs & 1);
-          ++segs;
-        }
-        for (int s = 0; alive && s < steps; ++s) {  // step s: tile s & 1
-          const int t = s & 1;
-          const uint32_t u = n0 + (dual ? s >> 1 : s);
-          const bool first_use = !dual || t == 0, last_use = !dual || t == 1;
-          if (!values) {
-            const uint32_t st = u % S::K_STAGES;
-            if (first_use) alive = warp_wait(&sh.k_full[st], (u / S::K_STAGES) & 1);
-            // the tile's weights before these scores are used up (before its first, the queries' arrival says so)
-            if (alive && s >= 2) alive = warp_wait(&sh.o_done[t], ((t ? seen1 : seen0) + 1) & 1);
-            if (!alive) break;
-            tc_fence_after();
-            const uint32_t q = smem_base + (dual && t ? S::Q1 : S::Q0), k = smem_base + S::K0 + st * S::TILE_BYTES;
-            if (elect_one()) {
-#pragma unroll
-              for (int i = 0; i < D / 16; ++i) {
-                const uint32_t off = (i >> 2) * (TILE * 128) + (i & 3) * 32;
-                tc_mma_bf16(sc + t * TILE, sw128_desc(q + off), sw128_desc(k + off), IDESC_S, i > 0);
-              }
-              tc_commit(&sh.s_full[t]);
-              if (last_use) tc_commit(&sh.k_empty[st]);
-            }
-            __syncwarp();
-          } else {
-            const uint32_t st = u % S::V_STAGES;
-            const uint32_t v = smem_base + S::V0 + st * S::TILE_BYTES;
-            if (first_use) alive = warp_wait(&sh.v_full[st], (u / S::V_STAGES) & 1);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              alive = alive && warp_wait(&sh.p_full[t][h], (t ? seen1 : seen0) & 1);
-              if (!alive) break;
-              tc_fence_after();
-              if (elect_one()) {
-#pragma unroll
-                for (int i = h ? FIRST / 16 : 0; i < (h ? UNIT : FIRST) / 16; ++i)
-                  tc_mma_bf16_ta(oc + t * D, sc + t * TILE + i * 8, value_desc(v + i * 2048), IDESC_O, s > 1 || i > 0);
-                if (h == 1) {
-                  tc_commit(&sh.o_done[t]);
-                  if (last_use) tc_commit(&sh.v_empty[st]);
-                }
-              }
-              __syncwarp();
-            }
-            if (!alive) break;
+        alive = warp_wait(&sh.q_full[0], qp) && warp_wait(&sh.q_full[1], qp);
+        qp ^= 1;
+        const uint64_t dq0 = sw128_desc(base + S::Q0), dq1 = dual ? sw128_desc(base + S::Q1) : dq0;
+        // with two tiles the second's step is the last of a unit, else every step is the first and the last
+        auto scores = [&](int t) {
+          const bool first = !dual || t == 0, last = !dual || t == 1;
+          if (first && !warp_wait(&sh.k_full[ks], kp)) return false;
+          if (!warp_wait(&sh.s_free, sp)) return false;  // the scores before are read
+          sp ^= 1;
+          tc_fence_after();
+          issue_scores<D>(sc, t ? dq1 : dq0, sw128_desc(base + S::K0 + ks * S::TILE_BYTES), IDESC_S, smem_addr(&sh.s_full[t]),
+                          last ? smem_addr(&sh.k_empty[ks]) : 0u);
+          if (last && ++ks == S::K_STAGES) {
+            ks = 0;
+            kp ^= 1;
           }
-          if (t)
-            ++seen1;
-          else
-            ++seen0;
+          return true;
+        };
+        auto values = [&](int t, bool fresh) {
+          const bool first = !dual || t == 0, last = !dual || t == 1;
+          if (first && !warp_wait(&sh.v_full[vs], vp)) return false;
+          if (!warp_wait(&sh.p_full[t], wp[t])) return false;
+          wp[t] ^= 1;
+          tc_fence_after();
+          issue_values(tm + 2 * UNIT + t * D, tm + t * P_STEP, value_desc(base + S::V0 + vs * S::TILE_BYTES), IDESC_O, fresh,
+                       smem_addr(&sh.o_done[t]), last ? smem_addr(&sh.v_empty[vs]) : 0u);
+          if (last && ++vs == S::V_STAGES) {
+            vs = 0;
+            vp ^= 1;
+          }
+          return true;
+        };
+        if (dual) {
+          for (int i = 0; alive && i <= n; ++i) {
+            alive = alive && (i == n || scores(0));
+            alive = alive && (i == 0 || values(0, i == 1));
+            alive = alive && (i == n || scores(1));
+            alive = alive && (i == 0 || values(1, i == 1));
+          }
+        } else {
+          for (int i = 0; alive && i <= n; i += 2) {
+            alive = alive && (i >= n || scores(0));
+            alive = alive && (i == 0 || values(1, i == 2));
+            alive = alive && (i + 1 >= n || scores(1));
+            alive = alive && (i >= n || values(0, i == 0));
+          }
         }
-        n0 += n;
       }
       if (!alive) {  // products in flight end before the tensor memory goes
-        uint64_t* const drain = &sh.drain[values ? 1 : 0];
-        tc_commit_w(drain);
-        mbar_drain_bounded(drain, 0);
+        tc_commit_w(&sh.drain);
+        mbar_drain_bounded(&sh.drain, 0);
       }
     }
     if (!alive && lane == 0 && p.error_word) atomicOr(p.error_word, KDA_ERR_TIMEOUT);
@@ -681,7 +726,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SOFTMAX_REGS));
     const int t = warp >> 2, x = tid & (TILE - 1);
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t s_addr = S_COL + t * TILE + lane_base, o_addr = O_COL + t * D + lane_base;
+    const uint32_t s_addr = S_COL + lane_base, p_addr = P_COL + t * P_STEP + lane_base, o_addr = O_COL + t * D + lane_base;
     const float c = p.scale * LOG2E;
     uint32_t seen_s = 0;  // scores waited for: as many products with values were asked for
     bool alive = true;
@@ -701,9 +746,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         alive = false;
         break;
       }
-      const Segment sg = sh.seg[slot];
-      bar_sync(2, SOFTMAX_THREADS);
-      if (x == 0) mbar_arrive(&sh.seg_empty[slot]);
+      const Segment& sg = sh.seg[slot];  // read again where needed: registers are short
       if (sg.ntok < 0) break;
       const int dual = sg.dual;
 
@@ -769,7 +812,10 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
           for (int i = 0; i < UNIT; i += 32) hold32(s + i);
           const int k0 = u * UNIT;
-          if (k0 + UNIT > all_hi || k0 < all_lo) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.s_free);
+          if (__builtin_expect(k0 + UNIT > all_hi || k0 < all_lo, 0)) {
             const int from = lo - k0, to = hi - k0;
 #pragma unroll
             for (int b = 0; b < UNIT; b += 32) {
@@ -780,12 +826,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (!(bits >> i & 1u)) s[b + i] = 0xff800000u;  // -inf
             }
           }
-          // The first weights by the reference so far, and beside them (in another pipe) the maximum: only if that has
-          // grown past the slack are they formed again.
-          const uint64_t c2 = pair(c, c);
-          uint64_t sum[4] = {0, 0, 0, 0}, base2 = reference(m, c);
-          uint32_t wa[16];
-          weights<32>(s, c2, base2, sum, wa);
           float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
           for (int i = 0; i < UNIT; i += 8)
@@ -794,11 +834,16 @@ __global__ void __launch_bounds__(THREADS, 1)
               tops[j] = max3(tops[j], __uint_as_float(s[i + 2 * j]), __uint_as_float(s[i + 2 * j + 1]));
           const float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]);
           const bool grown = valid && top > m && (top - m) * c > SLACK;  // m = -inf: any key
-          if (__any_sync(0xffffffffu, grown)) {
+          if (units > 0) {  // the product of the unit before is done with P and O
+            alive = warp_wait(&sh.o_done[t], (seen_s - 1) & 1);
+            if (!alive) break;
+          }
+          if (__builtin_expect(__any_sync(0xffffffffu, grown), 0)) {
             const float fade = grown ? ex2((m - top) * c) : 1.f;
             if (grown) m = top;
             l *= fade;
-            if (units > 0) {  // the product of the unit before is done: these scores waited for it
+            if (units > 0) {
+              tc_fence_after();
 #pragma unroll 1
               for (int i = 0; i < D; i += 16) {  // 16 columns at a time: the 128 scores stay in registers
                 float o[16];
@@ -809,31 +854,29 @@ __global__ void __launch_bounds__(THREADS, 1)
                 tmem_st16(o_addr + i, o2);
               }
             }
-            base2 = reference(m, c);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) sum[j] = 0;
-            weights<32>(s, c2, base2, sum, wa);
           }
-          auto give = [&](int h) {  // these weights are there: the products that take them may start
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.p_full[t][h]);
-          };
-          st16(s_addr, wa);
-          uint32_t wb[32];
-          weights<64>(s + 32, c2, base2, sum, wb);
-          st32(s_addr + 16, wb);
-          give(0);
-          weights<32>(s + FIRST, c2, base2, sum, wa);
-          st16(s_addr + FIRST / 2, wa);
-          give(1);
+          const uint64_t c2 = pair(c, c), base2 = reference(m, c);
+          uint64_t sum[4] = {0, 0, 0, 0};
+#pragma unroll
+          for (int i = 0; i < UNIT; i += 64) {
+            uint32_t w2[32];
+            weights<64>(s + i, c2, base2, sum, w2);
+            st32(p_addr + i / 2, w2);
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.p_full[t]);  // the product that takes these weights may start
           float l0, l1;
           unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), l0, l1);
           l += l0 + l1;
-        } else if (lane == 0) {
-          mbar_arrive(&sh.p_full[t][0]);
-          mbar_arrive(&sh.p_full[t][1]);
+        } else {  // the same arrivals, none of them before the unit's own
+          if (lane == 0) mbar_arrive(&sh.s_free);
+          if (units > 0) {
+            alive = warp_wait(&sh.o_done[t], (seen_s - 1) & 1);
+            if (!alive) break;
+          }
+          if (lane == 0) mbar_arrive(&sh.p_full[t]);
         }
         ++seen_s;
         ++units;
@@ -1054,6 +1097,11 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
         }
       }
+      if (t == 0)
+        bar_sync(3, TILE);
+      else
+        bar_sync(4, TILE);
+      if (x == 0) mbar_arrive(&sh.seg_empty[slot]);
     }
     if (!alive && x == 0 && p.error_word) atomicOr(p.error_word, KDA_ERR_TIMEOUT);
   }
@@ -1061,7 +1109,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == SCORE_WARP) tmem_dealloc(tmem, 512);
+  if (warp == PRODUCT_WARP) tmem_dealloc(tmem, 512);
 }
 
 size_t paged_attention_parts_bytes(int head_dim, int ctas) {
@@ -1079,7 +1127,7 @@ bool paged_attention_on_tensor_cores(const kda_paged_cache& c) {
 
 template <int D>
 static cudaError_t launch_tc(const CUtensorMap& km, const CUtensorMap& vm, const AttnArgs& a, int ctas, cudaStream_t s) {
-  constexpr size_t bytes = Shape<D>::END + sizeof(Shared) + 1024;
+  constexpr size_t bytes = Shape<D>::END + sizeof(Shared);
   static_assert(bytes <= 232448, "shared memory of one CTA");
   static std::atomic<bool> done{false};
   const cudaError_t e = set_smem_limit_once(kda_paged_attention_tc_kernel<D>, bytes, done);
