@@ -24,14 +24,12 @@
 //
 // A CTA is twelve warps: two softmax groups of four (a thread per row), a warp
 // each that loads keys and values (one tensor-map copy per page and 64
-// columns), that issues the products, and that walks the line. With two row
+// columns), that issues either product, and that walks the line. With two row
 // tiles, group t owns tile t; a single tile (decode, verify) takes the units in
 // turn with the groups, each with its own O, joined at the end, so that in
 // either case one group's exponentials run while the other's products do.
-// Tensor memory holds one S that both groups take in turn (a group has its row
-// in registers 250 cycles after the product, and the next product may start), P
-// (bf16) and O of each: 128 + 2 x 64 + 2 x D columns. So the first product never
-// waits for a group's exponentials or its second product.
+// S and P share tensor-memory columns: P (bf16) overwrites the S it came from
+// and enters the second product from there.
 #include <math.h>
 
 #include "kda_paged.cuh"
@@ -47,9 +45,11 @@ constexpr int TILE = 128;   // rows a tile
 constexpr int THREADS = 384;
 constexpr int SOFTMAX_THREADS = 256;
 constexpr int LOAD_WARP = 8, PRODUCT_WARP = 9, WALK_WARP = 10;  // the twelfth idles
+constexpr int FIRST = 96;   // keys of a unit whose weights are handed over first, while the others' are formed
 constexpr int RING = 4;  // segments the walking warp may be ahead
-// What an item costs beside its units (its queries, its end), in units: each item takes LEAD + its units of the line.
-constexpr int LEAD = 2;
+// What an item costs beside its units (its queries, its end), in units: each item takes LEAD + its units of the line. A
+// first chunk of 4096 tokens, whose items have 1 to 32 units: 168 us at 2, 144 at 4, 148 at 7.
+constexpr int LEAD = 4;
 // Registers a thread after the split: 256 x 208 + 128 x 88 = 384 x 168, what the block launches with.
 constexpr int SOFTMAX_REGS = 208, OTHER_REGS = 88;
 
@@ -78,7 +78,7 @@ struct Segment {
 
 struct Shared {
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
-  uint64_t v_tail, q_full[2], s_full[2], p_full[2], s_free, o_done[2], seg_full[RING], seg_empty[RING], drain;
+  uint64_t v_tail, q_full[2], s_full[2], p_full[2][2], o_done[2], seg_full[RING], seg_empty[RING], drain;
   Segment seg[RING];
   float m1[TILE], l1[TILE];  // the second group's m and l when both groups share a tile
   long long warp_sum[THREADS / 32];
@@ -161,9 +161,8 @@ __device__ __forceinline__ void hold32(uint32_t* r) {
                  "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
                  "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
                  "+r"(r[29])
-               :
-               : "memory");
-  asm volatile("" : "+r"(r[30]), "+r"(r[31]) : : "memory");
+               :);
+  asm volatile("" : "+r"(r[30]), "+r"(r[31]));
 }
 
 __device__ __forceinline__ void ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
@@ -176,6 +175,15 @@ __device__ __forceinline__ void st32(uint32_t taddr, const uint32_t* v) {
       "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
       "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
       "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+
+__device__ __forceinline__ void st16(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
 
@@ -294,25 +302,35 @@ __device__ __forceinline__ void issue_scores(uint32_t d, uint64_t a, uint64_t b,
         : "memory");
 }
 
-// D += A B over 128 keys (D = on the first if `fresh`), A (bf16 pairs) in tensor memory, 8 columns a K step; B with N
-// contiguous, 2048 bytes a K step.
-__device__ __forceinline__ void issue_values(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t fresh, uint32_t done,
-                                             uint32_t free) {
+// D += A B over keys [0, 96) or [96, 128) of a unit (D = on the first if `fresh`), A (bf16 pairs) in tensor memory, 8
+// columns a K step; B with N contiguous, 2048 bytes a K step. The second part is followed by the arrivals.
+__device__ __forceinline__ void issue_values_first(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t fresh) {
   asm volatile(
       "{\n\t.reg .pred p, q, t;\n\t.reg .b32 r, x;\n\t.reg .b64 y;\n\t"
       "elect.sync r|p, 0xffffffff;\n\tsetp.eq.b32 t, %4, 0;\n\tsetp.eq.b32 q, 0, 0;\n\t"
-      "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, t;\n\t"
-      "add.u32 x, %1, 8;\n\tadd.s64 y, %2, 128;\n\t@p tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, q;\n\t"
-      "add.u32 x, %1, 16;\n\tadd.s64 y, %2, 256;\n\t@p tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, q;\n\t"
-      "add.u32 x, %1, 24;\n\tadd.s64 y, %2, 384;\n\t@p tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, q;\n\t"
-      "add.u32 x, %1, 32;\n\tadd.s64 y, %2, 512;\n\t@p tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, q;\n\t"
-      "add.u32 x, %1, 40;\n\tadd.s64 y, %2, 640;\n\t@p tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, q;\n\t"
-      "add.u32 x, %1, 48;\n\tadd.s64 y, %2, 768;\n\t@p tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, q;\n\t"
-      "add.u32 x, %1, 56;\n\tadd.s64 y, %2, 896;\n\t@p tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, q;\n\t"
-      "@p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t"
-      "setp.ne.and.b32 p, %6, 0, p;\n\t"
-      "@p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%6];\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(fresh), "r"(done), "r"(free)
+"@p tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, t;\n\t"
+"add.u32 x, %1, 8;\n\tadd.s64 y, %2, 128;\n\t@p tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, q;\n\t"
+"add.u32 x, %1, 16;\n\tadd.s64 y, %2, 256;\n\t@p tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, q;\n\t"
+"add.u32 x, %1, 24;\n\tadd.s64 y, %2, 384;\n\t@p tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, q;\n\t"
+"add.u32 x, %1, 32;\n\tadd.s64 y, %2, 512;\n\t@p tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, q;\n\t"
+"add.u32 x, %1, 40;\n\tadd.s64 y, %2, 640;\n\t@p tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, q;\n\t"
+"}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(fresh)
+      : "memory");
+}
+__device__ __forceinline__ void issue_values_last(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t done,
+                                                  uint32_t free) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b32 r, x;\n\t.reg .b64 y;\n\t"
+      "elect.sync r|p, 0xffffffff;\n\tsetp.eq.b32 q, 0, 0;\n\t"
+"add.u32 x, %1, 48;\n\tadd.s64 y, %2, 768;\n\t@p tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, q;\n\t"
+"add.u32 x, %1, 56;\n\tadd.s64 y, %2, 896;\n\t@p tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, q;\n\t"
+
+      "setp.ne.and.b32 q, %4, 0, p;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n\t"
+      "setp.ne.and.b32 p, %5, 0, p;\n\t"
+      "@p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(done), "r"(free)
       : "memory");
 }
 
@@ -390,12 +408,11 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(&sh.v_empty[i], 1);
     }
     mbar_init(&sh.v_tail, 1);
-    mbar_init(&sh.s_free, TILE / 32);
     mbar_init(&sh.drain, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.q_full[i], TILE);
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_full[i], TILE / 32);  // an arrival a warp
+      for (int h = 0; h < 2; ++h) mbar_init(&sh.p_full[i][h], TILE / 32);  // an arrival a warp
       mbar_init(&sh.o_done[i], 1);
     }
     for (int i = 0; i < RING; ++i) {
@@ -461,9 +478,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
-  // columns: P of the first group, S, P of the second, O of either
-  const uint32_t P_COL = tmem, S_COL = tmem + UNIT / 2, O_COL = tmem + 2 * UNIT;
-  constexpr uint32_t P_STEP = UNIT / 2 + UNIT;
+  const uint32_t S_COL = tmem, O_COL = tmem + 2 * TILE;
 
   if (warp >= SOFTMAX_THREADS / 32) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
@@ -646,17 +661,10 @@ __global__ void __launch_bounds__(THREADS, 1)
           mbar_drain_bounded(&sh.v_full[i % S::V_STAGES], (i / S::V_STAGES) & 1);
       }
     } else if (warp == PRODUCT_WARP) {
-      // ---- the products, in one order: the scores of step s, then the values of a step before. The scores' 512 cycles are
-      // followed by their way into registers (300 more before the next may overwrite them), which the values' 512 cover;
-      // the weights of two steps before are ready by then. (A product takes 64 cycles, and its issue waits for room in a
-      // short queue. The warp stays together, what it reads from shared memory broadcast from one lane; an elected lane
-      // issues.)
       const uint32_t base = smem_addr(smem), tm = uniform(tmem);
-      const uint32_t sc = tm + UNIT / 2;
       constexpr uint32_t IDESC_S = idesc_bf16_f32(TILE, UNIT);
       constexpr uint32_t IDESC_O = idesc_bf16_f32(TILE, D) | B_MN_MAJOR;
-      // Each ring's stage and phase; the phase of the scores' buffer and of either tile's weights; the runs' of the queries.
-      uint32_t ks = 0, kp = 0, vs = 0, vp = 0, sp = 1, wp[2] = {0, 0}, qp = 0;
+      uint32_t ks = 0, kp = 0, vs = 0, vp = 0, wp[2] = {0, 0}, qp = 0;
       for (uint32_t in = 0; alive; ++in) {
         const uint32_t slot = in % RING;
         alive = warp_wait(&sh.seg_full[slot], (in / RING) & 1);
@@ -669,29 +677,33 @@ __global__ void __launch_bounds__(THREADS, 1)
         alive = warp_wait(&sh.q_full[0], qp) && warp_wait(&sh.q_full[1], qp);
         qp ^= 1;
         const uint64_t dq0 = sw128_desc(base + S::Q0), dq1 = dual ? sw128_desc(base + S::Q1) : dq0;
-        // with two tiles the second's step is the last of a unit, else every step is the first and the last
-        auto scores = [&](int t) {
+        auto scores = [&](int t, bool early = false) {
           const bool first = !dual || t == 0, last = !dual || t == 1;
-          if (first && !warp_wait(&sh.k_full[ks], kp)) return false;
-          if (!warp_wait(&sh.s_free, sp)) return false;  // the scores before are read
-          sp ^= 1;
-          tc_fence_after();
-          issue_scores<D>(sc, t ? dq1 : dq0, sw128_desc(base + S::K0 + ks * S::TILE_BYTES), IDESC_S, smem_addr(&sh.s_full[t]),
-                          last ? smem_addr(&sh.k_empty[ks]) : 0u);
+          if (first && !early) {
+            if (!warp_wait(&sh.k_full[ks], kp)) return false;
+            tc_fence_after();
+          }
+          issue_scores<D>(tm + t * TILE, t ? dq1 : dq0, sw128_desc(base + S::K0 + ks * S::TILE_BYTES), IDESC_S,
+                          smem_addr(&sh.s_full[t]), last ? smem_addr(&sh.k_empty[ks]) : 0u);
           if (last && ++ks == S::K_STAGES) {
             ks = 0;
             kp ^= 1;
           }
           return true;
         };
-        auto values = [&](int t, bool fresh) {
+        auto values = [&](int t, bool fresh, bool end) {
           const bool first = !dual || t == 0, last = !dual || t == 1;
           if (first && !warp_wait(&sh.v_full[vs], vp)) return false;
-          if (!warp_wait(&sh.p_full[t], wp[t])) return false;
-          wp[t] ^= 1;
+          if (dual && t == 0 && !end && !warp_wait(&sh.k_full[ks], kp)) return false;
+          if (!warp_wait(&sh.p_full[t][0], wp[t])) return false;
           tc_fence_after();
-          issue_values(tm + 2 * UNIT + t * D, tm + t * P_STEP, value_desc(base + S::V0 + vs * S::TILE_BYTES), IDESC_O, fresh,
-                       smem_addr(&sh.o_done[t]), last ? smem_addr(&sh.v_empty[vs]) : 0u);
+          const uint64_t v = value_desc(base + S::V0 + vs * S::TILE_BYTES);
+          issue_values_first(tm + 2 * TILE + t * D, tm + t * TILE, v, IDESC_O, fresh);
+          if (!warp_wait(&sh.p_full[t][1], wp[t])) return false;
+          tc_fence_after();
+          issue_values_last(tm + 2 * TILE + t * D, tm + t * TILE, v, IDESC_O, end ? smem_addr(&sh.o_done[t]) : 0u,
+                            last ? smem_addr(&sh.v_empty[vs]) : 0u);
+          wp[t] ^= 1;
           if (last && ++vs == S::V_STAGES) {
             vs = 0;
             vp ^= 1;
@@ -699,18 +711,16 @@ __global__ void __launch_bounds__(THREADS, 1)
           return true;
         };
         if (dual) {
-          for (int i = 0; alive && i <= n; ++i) {
-            alive = alive && (i == n || scores(0));
-            alive = alive && (i == 0 || values(0, i == 1));
-            alive = alive && (i == n || scores(1));
-            alive = alive && (i == 0 || values(1, i == 1));
+          alive = alive && scores(0) && scores(1);
+          for (int i = 0; alive && i < n; ++i) {
+            alive = values(0, i == 0, i + 1 == n) && (i + 1 == n || scores(0, true)) && values(1, i == 0, i + 1 == n) &&
+                    (i + 1 == n || scores(1));
           }
         } else {
-          for (int i = 0; alive && i <= n; i += 2) {
-            alive = alive && (i >= n || scores(0));
-            alive = alive && (i == 0 || values(1, i == 2));
-            alive = alive && (i + 1 >= n || scores(1));
-            alive = alive && (i >= n || values(0, i == 0));
+          alive = alive && scores(0) && (n < 2 || scores(1));
+          for (int i = 0; alive && i < n; i += 2) {
+            alive = values(0, i == 0, i + 2 >= n) && (i + 2 >= n || scores(0)) &&
+                    (i + 1 >= n || (values(1, i == 0, i + 3 >= n) && (i + 3 >= n || scores(1))));
           }
         }
       }
@@ -726,9 +736,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SOFTMAX_REGS));
     const int t = warp >> 2, x = tid & (TILE - 1);
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t s_addr = S_COL + lane_base, p_addr = P_COL + t * P_STEP + lane_base, o_addr = O_COL + t * D + lane_base;
+    const uint32_t s_addr = S_COL + t * TILE + lane_base, o_addr = O_COL + t * D + lane_base;
     const float c = p.scale * LOG2E;
-    uint32_t seen_s = 0;  // scores waited for: as many products with values were asked for
+    uint32_t seen_s = 0, runs = 0;  // scores waited for; ends of runs
     bool alive = true;
     // row / g for row < 128 and g <= 128: the product's excess is below 128 / 2^16 < 1 / g
     const uint32_t inv_g = 65536u / (uint32_t)g + 1u;
@@ -812,9 +822,6 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
           for (int i = 0; i < UNIT; i += 32) hold32(s + i);
           const int k0 = u * UNIT;
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.s_free);
           if (__builtin_expect(k0 + UNIT > all_hi || k0 < all_lo, 0)) {
             const int from = lo - k0, to = hi - k0;
 #pragma unroll
@@ -826,6 +833,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (!(bits >> i & 1u)) s[b + i] = 0xff800000u;  // -inf
             }
           }
+          // The first weights by the reference so far, and beside them (in another pipe) the maximum: only if that has
+          // grown past the slack are they formed again.
+          const uint64_t c2 = pair(c, c);
+          uint64_t sum[4] = {0, 0, 0, 0}, base2 = reference(m, c);
+          uint32_t wa[16];
+          weights<32>(s, c2, base2, sum, wa);
           float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
           for (int i = 0; i < UNIT; i += 8)
@@ -834,16 +847,11 @@ __global__ void __launch_bounds__(THREADS, 1)
               tops[j] = max3(tops[j], __uint_as_float(s[i + 2 * j]), __uint_as_float(s[i + 2 * j + 1]));
           const float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]);
           const bool grown = valid && top > m && (top - m) * c > SLACK;  // m = -inf: any key
-          if (units > 0) {  // the product of the unit before is done with P and O
-            alive = warp_wait(&sh.o_done[t], (seen_s - 1) & 1);
-            if (!alive) break;
-          }
           if (__builtin_expect(__any_sync(0xffffffffu, grown), 0)) {
             const float fade = grown ? ex2((m - top) * c) : 1.f;
             if (grown) m = top;
             l *= fade;
-            if (units > 0) {
-              tc_fence_after();
+            if (units > 0) {  // the product of the unit before is done: these scores waited for it
 #pragma unroll 1
               for (int i = 0; i < D; i += 16) {  // 16 columns at a time: the 128 scores stay in registers
                 float o[16];
@@ -854,36 +862,39 @@ __global__ void __launch_bounds__(THREADS, 1)
                 tmem_st16(o_addr + i, o2);
               }
             }
-          }
-          const uint64_t c2 = pair(c, c), base2 = reference(m, c);
-          uint64_t sum[4] = {0, 0, 0, 0};
+            base2 = reference(m, c);
 #pragma unroll
-          for (int i = 0; i < UNIT; i += 64) {
-            uint32_t w2[32];
-            weights<64>(s + i, c2, base2, sum, w2);
-            st32(p_addr + i / 2, w2);
+            for (int j = 0; j < 4; ++j) sum[j] = 0;
+            weights<32>(s, c2, base2, sum, wa);
           }
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.p_full[t]);  // the product that takes these weights may start
+          auto give = [&](int h) {  // these weights are there: the products that take them may start
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.p_full[t][h]);
+          };
+          st16(s_addr, wa);
+          weights<32>(s + 32, c2, base2, sum, wa);
+          st16(s_addr + 16, wa);
+          weights<32>(s + 64, c2, base2, sum, wa);
+          st16(s_addr + 32, wa);
+          give(0);
+          weights<32>(s + FIRST, c2, base2, sum, wa);
+          st16(s_addr + FIRST / 2, wa);
+          give(1);
           float l0, l1;
           unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), l0, l1);
           l += l0 + l1;
-        } else {  // the same arrivals, none of them before the unit's own
-          if (lane == 0) mbar_arrive(&sh.s_free);
-          if (units > 0) {
-            alive = warp_wait(&sh.o_done[t], (seen_s - 1) & 1);
-            if (!alive) break;
-          }
-          if (lane == 0) mbar_arrive(&sh.p_full[t]);
+        } else if (lane == 0) {
+          mbar_arrive(&sh.p_full[t][0]);
+          mbar_arrive(&sh.p_full[t][1]);
         }
         ++seen_s;
         ++units;
       }
 
       // ---- the end of the run
-      if (alive && units > 0) alive = warp_wait(&sh.o_done[t], (seen_s - 1) & 1);
+      if (alive && units > 0) alive = warp_wait(&sh.o_done[t], runs++ & 1);
       if (units > 0) tc_fence_after();
       float fade0 = 1.f;  // what the O of this thread's tensor memory is scaled by
       float fade1 = 0.f;
