@@ -44,14 +44,14 @@ constexpr int UNIT = 128;   // keys a unit
 constexpr int TILE = 128;   // rows a tile
 constexpr int THREADS = 384;
 constexpr int SOFTMAX_THREADS = 256;
-constexpr int LOAD_WARP = 8, PRODUCT_WARP = 9, WALK_WARP = 10;  // the twelfth idles
+constexpr int LOAD_WARP = 8, PRODUCT_WARP = 9, WALK_WARP = 10, AHEAD_WARP = 11;
 constexpr int FIRST = 96;   // keys of a unit whose weights are handed over first, while the others' are formed
 constexpr int RING = 4;  // segments the walking warp may be ahead
 // What an item costs beside its units (its queries, its end), in units: each item takes LEAD + its units of the line. A
 // first chunk of 4096 tokens, whose items have 1 to 32 units: 168 us at 2, 144 at 4, 148 at 7.
 constexpr int LEAD = 4;
-// Registers a thread after the split: 256 x 208 + 128 x 88 = 384 x 168, what the block launches with.
-constexpr int SOFTMAX_REGS = 208, OTHER_REGS = 88;
+// Registers a thread after the split: 256 x 216 + 128 x 72 = 384 x 168, what the block launches with.
+constexpr int SOFTMAX_REGS = 216, OTHER_REGS = 72;
 
 template <int D>
 struct Shape {
@@ -167,17 +167,6 @@ __device__ __forceinline__ void hold32(uint32_t* r) {
 
 __device__ __forceinline__ void ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
-__device__ __forceinline__ void st32(uint32_t taddr, const uint32_t* v) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
-      "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
-      "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
-      : "memory");
-}
-
 __device__ __forceinline__ void st16(uint32_t taddr, const uint32_t* v) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
@@ -191,6 +180,19 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// 1 / x and ln x to 2^-22 or better, for sums of weights (from 2^-8 on): bf16 outputs and a log of fp32 terms need no more,
+// and the exact forms are long code for once a run.
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float ln(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y * 0.6931471805599453f;
 }
 
 // Two fp32 at once: x y + z, x + y.
@@ -338,6 +340,21 @@ __device__ __forceinline__ void issue_values_last(uint32_t d, uint32_t a, uint64
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_max_sync(0xffffffffu, x); }
 __device__ __forceinline__ int uniform(int x) { return __reduce_max_sync(0xffffffffu, x); }
 
+// 16 bytes from global to shared memory, asynchronously (both 16-byte aligned); the wait for all of this thread's.
+__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+__device__ __forceinline__ void prefetch_l2(const void* src) { asm volatile("prefetch.global.L2 [%0];" ::"l"(src)); }
+
+// The thread's number, read again.
+__device__ __forceinline__ uint32_t fresh_tid() {
+  uint32_t x;
+  asm volatile("mov.u32 %0, %%tid.x;" : "=r"(x));
+  return x;
+}
+
 // A barrier of `count` threads that tells all of them whether `x` held for any.
 __device__ __forceinline__ bool bar_any(uint32_t id, uint32_t count, bool x) {
   uint32_t any;
@@ -370,6 +387,8 @@ struct AttnArgs {
   unsigned* counters;  // one a CTA, zero between calls
   int q_wide, out_wide;
   int box;             // keys a copy brings: min(page_size, UNIT)
+  int group, tile_tokens;  // query heads a key-value head, tokens a tile
+  unsigned inv_group;      // row / group = row * inv_group >> 16
 };
 
 // A part's O by groups of four columns, the rows of a group side by side: a warp's threads (a row each) write and read
@@ -394,8 +413,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   Shared& sh = *reinterpret_cast<Shared*>(smem + S::END);
   const kda_attention_params& p = a.p;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int g = p.num_q_heads / p.cache.num_heads, Hkv = p.cache.num_heads;
-  const int tpt = TILE / g, w = 2 * tpt;  // tokens a tile, an item
+  const int g = a.group, Hkv = p.cache.num_heads;
+  const int tpt = a.tile_tokens, w = 2 * tpt;  // tokens a tile, an item
   const int window = p.window;
 
   if (tid == 0) {
@@ -417,7 +436,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     for (int i = 0; i < RING; ++i) {
       mbar_init(&sh.seg_full[i], 1);
-      mbar_init(&sh.seg_empty[i], 4);  // the loading warp, the product warp, both softmax groups
+      mbar_init(&sh.seg_empty[i], 5);  // the loading, product and prefetching warps, both softmax groups
     }
     sh.start_request = -1;
   }
@@ -456,23 +475,37 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     return all;
   };
-  for (int base = 0; base < R; base += THREADS) total += block_units(base);
-  if (blockIdx.x == 0 && bad && p.error_word) atomicOr(p.error_word, bad);
-  const int ctas = total < (long long)gridDim.x ? (int)total : (int)gridDim.x;
+  // The requests in one block: their units once. Else once for the sum and once to find where the share begins.
+  int ctas = 0;
   const int cta = blockIdx.x;
-  if (cta >= ctas) return;  // the whole CTA: nothing allocated yet
-  const long long begin = mul_div(total, cta, ctas), end = mul_div(total, cta + 1, ctas);
-  {
+  long long begin = 0, end = 0;
+  for (int pass = one_block ? 1 : 0; pass < 2; ++pass) {
     long long prefix = 0;
     for (int base = 0; base < R; base += THREADS) {
-      const long long all = one_block ? total : block_units(base);
+      const long long all = block_units(base);
+      if (pass == 0 || one_block) total += all;
+      if (pass == 0) continue;
+      if (one_block) {
+        ctas = total < (long long)gridDim.x ? (int)total : (int)gridDim.x;
+        if (cta >= ctas) break;
+        begin = mul_div(total, cta, ctas);
+        end = mul_div(total, cta + 1, ctas);
+      }
       if (begin >= prefix + before && begin < prefix + before + mine) {
         sh.start_request = base + tid;
         sh.start_prefix = prefix + before;
       }
       prefix += all;
     }
+    if (pass == 0) {
+      ctas = total < (long long)gridDim.x ? (int)total : (int)gridDim.x;
+      if (cta >= ctas) break;
+      begin = mul_div(total, cta, ctas);
+      end = mul_div(total, cta + 1, ctas);
+    }
   }
+  if (blockIdx.x == 0 && bad && p.error_word) atomicOr(p.error_word, bad);
+  if (cta >= ctas) return;  // the whole CTA: nothing allocated yet
   if (warp == PRODUCT_WARP) tmem_alloc(&sh.tmem, 512);
   tc_fence_before();
   __syncthreads();
@@ -660,6 +693,23 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (uint32_t i = vn > (uint32_t)S::V_STAGES ? vn - S::V_STAGES : 0; i < vn; ++i)
           mbar_drain_bounded(&sh.v_full[i % S::V_STAGES], (i / S::V_STAGES) & 1);
       }
+    } else if (warp == AHEAD_WARP) {
+      // ---- the queries of the runs to come into L2: from memory they take 2400 cycles, in which a run could not start
+      for (uint32_t in = 0; alive; ++in) {
+        const uint32_t slot = in % RING;
+        alive = warp_wait(&sh.seg_full[slot], (in / RING) & 1);
+        if (!alive) break;
+        const int ntok = sh.seg[slot].ntok, row0 = sh.seg[slot].row0, head = sh.seg[slot].head;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.seg_empty[slot]);
+        if (ntok < 0) break;
+        if (in == 0) continue;  // being fetched
+        const uint16_t* const q = static_cast<const uint16_t*>(p.q.ptr) + (int64_t)row0 * p.q.b_stride + (int64_t)(head * g) * p.q.h_stride;
+        for (int r = lane; r < ntok * g; r += 32) {
+          const uint16_t* const src = q + (int64_t)(r / g) * p.q.b_stride + (int64_t)(r % g) * p.q.h_stride;
+          for (int ch = 0; ch < D; ch += 64) prefetch_l2(src + ch);
+        }
+      }
     } else if (warp == PRODUCT_WARP) {
       const uint32_t base = smem_addr(smem), tm = uniform(tmem);
       constexpr uint32_t IDESC_S = idesc_bf16_f32(TILE, UNIT);
@@ -734,21 +784,62 @@ __global__ void __launch_bounds__(THREADS, 1)
   } else {
     // ---- softmax: group t, thread (row) x
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SOFTMAX_REGS));
-    const int t = warp >> 2, x = tid & (TILE - 1);
-    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t s_addr = S_COL + t * TILE + lane_base, o_addr = O_COL + t * D + lane_base;
+    const int t = warp >> 2;
     const float c = p.scale * LOG2E;
     uint32_t seen_s = 0, runs = 0;  // scores waited for; ends of runs
     bool alive = true;
-    // row / g for row < 128 and g <= 128: the product's excess is below 128 / 2^16 < 1 / g
-    const uint32_t inv_g = 65536u / (uint32_t)g + 1u;
-    auto div_g = [&](int row) { return (int)((uint32_t)row * inv_g >> 16); };
-    // 16-byte chunks of a tile in shared memory, as the products read them
-    auto tile_chunk = [](int row, int ch) { return (uint32_t)((ch >> 3) * (TILE * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4)); };
-    const int token_of_row = div_g(x), head_of_row = x - token_of_row * g;
-    // a group copies a tile with D / 8 threads a row
-    constexpr int ROWS_A_ROUND = TILE / (D / 8), ROUNDS = TILE / ROWS_A_ROUND;
-    const int my_row = x / (D / 8), my_ch = x % (D / 8);
+    auto div_g = [&](int row) { return (int)((uint32_t)row * a.inv_group >> 16); };
+    // Where a thread stands is worked out anew for each part of a run: kept over the units, it would cost them registers.
+    // Row (tensor-memory lane) of the tile; when copying a tile, with D / 8 threads a row, row and 16-byte chunk.
+    constexpr int ROWS_A_ROUND = TILE / (D / 8), ROUNDS = TILE / ROWS_A_ROUND;  // a multiple of 8 rows a round
+    struct Place {
+      int x, row, ch;
+      uint32_t at;  // of the chunk in a tile in shared memory, as the products read it
+    };
+    auto place = [] {
+      Place q;
+      q.x = (int)(fresh_tid() & (TILE - 1));
+      q.row = q.x / (D / 8);
+      q.ch = q.x % (D / 8);
+      q.at = (uint32_t)((q.ch >> 3) * (TILE * 128) + q.row * 128 + (((q.ch ^ q.row) & 7) << 4));
+      return q;
+    };
+    // Offset of row r of a tile (token r / g, head r % g) in a tensor of those strides (below 2^31, so one multiplication each).
+    auto row_offset = [&](int r, int64_t b_stride, int64_t h_stride) {
+      const int tk = div_g(r);
+      return (int64_t)tk * (int)b_stride + (int64_t)(r - tk * g) * (int)h_stride;
+    };
+    // The queries of a run: a group's tile, or its half of the tile that both share.
+    auto fetch_q = [&](const Segment& n) {
+      const Place me = place();
+      const int tile0 = n.dual ? t * tpt : 0;  // first token of the tile
+      const int from = n.dual ? 0 : t * (TILE / 2);
+      const int to = min(min(n.ntok - tile0, tpt) * g, n.dual ? TILE : from + TILE / 2);
+      const uint16_t* const qg = static_cast<const uint16_t*>(p.q.ptr) + (int64_t)(n.row0 + tile0) * p.q.b_stride +
+                                 (int64_t)(n.head * g) * p.q.h_stride + me.ch * 8;
+      uint8_t* const qs = smem + (n.dual && t ? S::Q1 : S::Q0) + me.at + from * 128;
+      if (a.q_wide) {  // asynchronously, all rounds in flight
+#pragma unroll 4
+        for (int k = 0; k < ROUNDS; ++k) {
+          const int r = from + me.row + k * ROWS_A_ROUND;
+          if (r < to) copy_async16(qs + k * (ROWS_A_ROUND * 128), qg + row_offset(r, p.q.b_stride, p.q.h_stride));
+        }
+        copy_async_wait();
+      } else {
+#pragma unroll 1
+        for (int k = 0; k < ROUNDS; ++k) {
+          const int r = from + me.row + k * ROWS_A_ROUND;
+          if (r >= to) break;
+          const uint16_t* const src = qg + row_offset(r, p.q.b_stride, p.q.h_stride);
+          uint32_t e[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) e[j] = (uint32_t)src[2 * j] | ((uint32_t)src[2 * j + 1] << 16);
+          *reinterpret_cast<uint4*>(qs + k * (ROWS_A_ROUND * 128)) = make_uint4(e[0], e[1], e[2], e[3]);
+        }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&sh.q_full[t]);
+    };
     for (uint32_t in = 0;; ++in) {
       const uint32_t slot = in % RING;
       alive = warp_wait(&sh.seg_full[slot], (in / RING) & 1);
@@ -759,54 +850,34 @@ __global__ void __launch_bounds__(THREADS, 1)
       const Segment& sg = sh.seg[slot];  // read again where needed: registers are short
       if (sg.ntok < 0) break;
       const int dual = sg.dual;
+      fetch_q(sg);
 
-      // queries: this group's tile, or its half of the shared one
+      // Keys [lo, hi) that this thread's row sees; a row of no token is carried along unmasked and goes nowhere.
+      struct Row {
+        int tok;  // of the item
+        bool valid;
+        int lo, hi;
+      };
+      auto my_row = [&] {
+        Row r;
+        const int tk = div_g((int)(fresh_tid() & (TILE - 1)));
+        r.tok = (sg.dual ? t * tpt : 0) + tk;
+        r.valid = tk < tpt && r.tok < sg.ntok;
+        r.hi = r.valid ? sg.pos0 + r.tok + 1 : 0x7fffffff;
+        r.lo = r.valid && window > 0 ? max(0, r.hi - window) : 0;
+        return r;
+      };
+      bool valid;
+      int all_lo, all_hi;
       {
-        const int tile0 = dual ? t * tpt : 0;  // first token of the tile
-        const int rows = min(sg.ntok - tile0, tpt) * g;
-        uint8_t* const qs = smem + (dual && t ? S::Q1 : S::Q0);
-        const int from = dual ? 0 : t * (TILE / 2), to = min(rows, dual ? TILE : from + TILE / 2);
-        const uint16_t* const qg = static_cast<const uint16_t*>(p.q.ptr) + (int64_t)(sg.row0 + tile0) * p.q.b_stride +
-                                   (int64_t)(sg.head * g) * p.q.h_stride + my_ch * 8;
-        // BATCH rows in flight before the first is stored; a round on, a row stands ROWS_A_ROUND (a multiple of 8) lower
-        constexpr int BATCH = ROUNDS < 8 ? ROUNDS : 8;
-        uint32_t row = from + my_row;
-        const uint32_t at0 = tile_chunk(my_row, my_ch) - my_row * 128;
-#pragma unroll 1
-        for (int k0 = 0; k0 < ROUNDS; k0 += BATCH, row += BATCH * ROWS_A_ROUND) {
-          if (row >= (uint32_t)to) break;
-          uint4 val[BATCH];
-#pragma unroll
-          for (int k = 0; k < BATCH; ++k) {
-            const int r2 = row + k * ROWS_A_ROUND;
-            if (r2 >= to) continue;
-            const int tok = div_g(r2);
-            const uint16_t* const src = qg + (int64_t)tok * p.q.b_stride + (int64_t)(r2 - tok * g) * p.q.h_stride;
-            if (a.q_wide) {
-              val[k] = __ldg(reinterpret_cast<const uint4*>(src));
-            } else {
-              uint32_t e[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j) e[j] = (uint32_t)src[2 * j] | ((uint32_t)src[2 * j + 1] << 16);
-              val[k] = make_uint4(e[0], e[1], e[2], e[3]);
-            }
-          }
-#pragma unroll
-          for (int k = 0; k < BATCH; ++k)
-            if ((int)row + k * ROWS_A_ROUND < to)
-              *reinterpret_cast<uint4*>(qs + at0 + (row + k * ROWS_A_ROUND) * 128) = val[k];
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(&sh.q_full[t]);
+        const Row r = my_row();
+        valid = r.valid;
+        all_lo = __reduce_max_sync(0xffffffffu, r.lo);
+        all_hi = __reduce_min_sync(0xffffffffu, r.hi);
       }
-
-      const int tok = (dual ? t * tpt : 0) + token_of_row;
-      const bool valid = token_of_row < tpt && tok < sg.ntok;
-      // this row sees keys [lo, hi); a row of no token is carried along unmasked and goes nowhere
-      const int hi = valid ? sg.pos0 + tok + 1 : 0x7fffffff;
-      const int lo = valid && window > 0 ? max(0, hi - window) : 0;
-      const int all_lo = __reduce_max_sync(0xffffffffu, lo), all_hi = __reduce_min_sync(0xffffffffu, hi);
       const bool warp_valid = __any_sync(0xffffffffu, valid);
+      const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+      const uint32_t s_addr = S_COL + t * TILE + lane_base, o_addr = O_COL + t * D + lane_base;
       float m = -INFINITY, l = 0.f;  // m: the reference, in units of the scores
       const int step = dual ? 1 : 2;
       int units = 0;
@@ -823,7 +894,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int i = 0; i < UNIT; i += 32) hold32(s + i);
           const int k0 = u * UNIT;
           if (__builtin_expect(k0 + UNIT > all_hi || k0 < all_lo, 0)) {
-            const int from = lo - k0, to = hi - k0;
+            const Row r = my_row();
+            const int from = r.lo - k0, to = r.hi - k0;
 #pragma unroll
             for (int b = 0; b < UNIT; b += 32) {
               // bits [from, to) of this block
@@ -894,6 +966,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
 
       // ---- the end of the run
+      const Place me = place();
+      const int x = me.x;
       if (alive && units > 0) alive = warp_wait(&sh.o_done[t], runs++ & 1);
       if (units > 0) tc_fence_after();
       float fade0 = 1.f;  // what the O of this thread's tensor memory is scaled by
@@ -915,66 +989,50 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       const bool direct = sg.parts == 1;
       const bool writes = (dual || t == 0) && valid;
-      const int64_t row = (int64_t)sg.row0 + tok;
-      const int qh = sg.head * g + head_of_row;
       const int slot_id = sg.part == 0 ? 2 * cta + 1 : 2 * cta;
       const int part_row = (dual ? t * TILE : 0) + x;
       uint8_t* const tile = smem + (dual && t ? S::Q1 : S::Q0);
       const bool none = l == 0.f;  // no key: zeros
-      const float inv = 1.f / l;
+      const float inv = rcp(l);
       float* const other = reinterpret_cast<float*>(smem + S::Q1);  // the second group's O, half the columns at a time
       const bool two = !dual && sg.u1 - sg.u0 > 1;  // the second group has one
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      // 32 columns at a time, in a loop that is not unrolled: this runs once a run, and its instructions come from afar
+      const uint32_t tile_at = (uint32_t)(x * 128);
+#pragma unroll 1
+      for (int col = 0; col < D; col += 32) {
+        float* const o1 = other + (col & (D / 2 - 1)) * TILE + x;
+        float f[32];
+        if (warp_valid && (dual || t == 0 || two)) tmem_ld32(o_addr + col, f);
         if (two) {
           if (t == 1 && warp_valid) {
 #pragma unroll
-            for (int i = 0; i < D / 2; i += 32) {
-              uint32_t o[32];
-              ld32(o_addr + h * (D / 2) + i, o);
-              ld_wait();
-              hold32(o);
-#pragma unroll
-              for (int j = 0; j < 32; ++j) other[(i + j) * TILE + x] = __uint_as_float(o[j]);
-            }
+            for (int j = 0; j < 32; ++j) o1[j * TILE] = f[j];
           }
           bar_sync(2, SOFTMAX_THREADS);
+          if (t == 0 && warp_valid) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) f[j] = f[j] * fade0 + o1[j * TILE] * fade1;
+          }
+          if (D == 64 || col == 32) bar_sync(2, SOFTMAX_THREADS);  // half the columns fill the buffer
         }
-        if (warp_valid && (dual || t == 0)) {
+        if (writes) {
+          if (direct) {  // into the tile's own queries' place, which the products are done with
 #pragma unroll
-          for (int i = 0; i < D / 2; i += 32) {
-            uint32_t o[32];
-            ld32(o_addr + h * (D / 2) + i, o);
-            ld_wait();
-            hold32(o);
-            float f[32];
+            for (int j = 0; j < 4; ++j) {
+              uint32_t b[4];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(o[j]);
-            if (two) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j) f[j] = f[j] * fade0 + other[(i + j) * TILE + x] * fade1;
+              for (int e = 0; e < 4; ++e)
+                b[e] = none ? 0u : pack_bf16x2(f[8 * j + 2 * e] * inv, f[8 * j + 2 * e + 1] * inv);
+              const uint32_t ch = col / 8 + j;
+              *reinterpret_cast<uint4*>(tile + (ch >> 3) * (TILE * 128) + tile_at + (((ch ^ x) & 7) << 4)) =
+                  make_uint4(b[0], b[1], b[2], b[3]);
             }
-            if (writes) {
-              const int col = h * (D / 2) + i;
-              if (direct) {  // into the tile's own queries' place, which the products are done with
+          } else {
+            float4* const o = part_o<D>(a, slot_id) + (col / 4) * (2 * TILE) + part_row;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  uint32_t b[4];
-#pragma unroll
-                  for (int e = 0; e < 4; ++e)
-                    b[e] = none ? 0u : pack_bf16x2(f[8 * j + 2 * e] * inv, f[8 * j + 2 * e + 1] * inv);
-                  *reinterpret_cast<uint4*>(tile + tile_chunk(x, col / 8 + j)) = make_uint4(b[0], b[1], b[2], b[3]);
-                }
-              } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                  part_o<D>(a, slot_id)[(col / 4 + j) * (2 * TILE) + part_row] =
-                      make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
-              }
-            }
+            for (int j = 0; j < 8; ++j) o[j * (2 * TILE)] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
           }
         }
-        if (two && h == 0) bar_sync(2, SOFTMAX_THREADS);
       }
       tc_fence_before();
       if (direct && (dual || t == 0)) {
@@ -984,28 +1042,37 @@ __global__ void __launch_bounds__(THREADS, 1)
           bar_sync(4, TILE);
         const int tile0 = dual ? t * tpt : 0, rows = min(sg.ntok - tile0, tpt) * g;
         uint16_t* const og = static_cast<uint16_t*>(p.out) + (int64_t)(sg.row0 + tile0) * p.out_b_stride +
-                             (int64_t)(sg.head * g) * p.out_h_stride + my_ch * 8;
-        const uint32_t at0 = tile_chunk(my_row, my_ch) - my_row * 128;
-#pragma unroll 4
-        for (int row2 = my_row; row2 < rows; row2 += ROWS_A_ROUND) {
-          const uint4 v = *reinterpret_cast<const uint4*>(tile + at0 + row2 * 128);
-          const int tk = div_g(row2);
-          uint16_t* const dst = og + (int64_t)tk * p.out_b_stride + (int64_t)(row2 - tk * g) * p.out_h_stride;
-          if (a.out_wide) {
-            *reinterpret_cast<uint4*>(dst) = v;
-          } else {
-            const uint32_t e[4] = {v.x, v.y, v.z, v.w};
+                             (int64_t)(sg.head * g) * p.out_h_stride + me.ch * 8;
+#pragma unroll 1
+        for (int k0 = 0; k0 < ROUNDS; k0 += 4) {
+          if (me.row + k0 * ROWS_A_ROUND >= rows) break;
+          uint4 v[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              dst[2 * j] = (uint16_t)e[j];
-              dst[2 * j + 1] = (uint16_t)(e[j] >> 16);
+          for (int k = 0; k < 4; ++k) v[k] = *reinterpret_cast<const uint4*>(tile + me.at + (k0 + k) * (ROWS_A_ROUND * 128));
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int r = me.row + (k0 + k) * ROWS_A_ROUND;
+            if (r >= rows) continue;
+            uint16_t* const dst = og + row_offset(r, p.out_b_stride, p.out_h_stride);
+            if (a.out_wide) {
+              *reinterpret_cast<uint4*>(dst) = v[k];
+            } else {
+              const uint32_t e[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                dst[2 * j] = (uint16_t)e[j];
+                dst[2 * j + 1] = (uint16_t)(e[j] >> 16);
+              }
             }
           }
         }
       }
       if (writes) {
         if (direct) {
-          if (p.lse != nullptr) p.lse[row * p.num_q_heads + qh] = m == -INFINITY ? -INFINITY : m * p.scale + logf(l);
+          const Row r = my_row();
+          if (p.lse != nullptr)
+            p.lse[((int64_t)sg.row0 + r.tok) * p.num_q_heads + sg.head * g + (x - div_g(x) * g)] =
+                m == -INFINITY ? -INFINITY : m * p.scale + ln(l);
         } else {
           part_ml<D>(a, slot_id)[part_row] = make_float2(m, l);
         }
@@ -1050,13 +1117,14 @@ __global__ void __launch_bounds__(THREADS, 1)
               const int tk = tid % TILE / g;
               const int64_t orow = (int64_t)sg.row0 + tid / TILE * tpt + tk;
               p.lse[orow * p.num_q_heads + sg.head * g + (tid % TILE - tk * g)] =
-                  mm == -INFINITY ? -INFINITY : mm * p.scale + logf(ll);
+                  mm == -INFINITY ? -INFINITY : mm * p.scale + ln(ll);
             }
           }
           bar_sync(1, SOFTMAX_THREADS);
           // then four columns of a row at a time; `pad` rows a group of columns, so that neighbours read neighbours
           const int pad = (rows + 7) & ~7;
           constexpr int U = 4;
+#pragma unroll 1
           for (int i0 = tid; i0 < pad * (D / 4); i0 += U * SOFTMAX_THREADS) {
             float acc[U][4];
             int at[U];
@@ -1089,7 +1157,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int k = 0; k < U; ++k) {
               if (!on[k]) continue;
               const int row2 = at[k] % (2 * TILE), col = at[k] / (2 * TILE) * 4;
-              const float ll = jl[row2], iv = 1.f / ll;
+              const float ll = jl[row2], iv = rcp(ll);
               const int tk = row2 % TILE / g;
               const int64_t orow = (int64_t)sg.row0 + row2 / TILE * tpt + tk;
               const int oh = sg.head * g + (row2 % TILE - tk * g);
@@ -1114,7 +1182,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         bar_sync(4, TILE);
       if (x == 0) mbar_arrive(&sh.seg_empty[slot]);
     }
-    if (!alive && x == 0 && p.error_word) atomicOr(p.error_word, KDA_ERR_TIMEOUT);
+    if (!alive && lane == 0 && p.error_word) atomicOr(p.error_word, KDA_ERR_TIMEOUT);
   }
 
   tc_fence_before();
@@ -1148,6 +1216,7 @@ static cudaError_t launch_tc(const CUtensorMap& km, const CUtensorMap& vm, const
 }
 
 cudaError_t launch_paged_attention_tc(const kda_attention_params& p, void* workspace, int ctas, cudaStream_t s) {
+  if ((p.q.b_stride | p.q.h_stride | p.out_b_stride | p.out_h_stride) >> 31) return cudaErrorNotSupported;
   AttnArgs a;
   a.p = p;
   a.counters = static_cast<unsigned*>(workspace);
@@ -1158,6 +1227,9 @@ cudaError_t launch_paged_attention_tc(const kda_attention_params& p, void* works
   a.q_wide = rows16(p.q.ptr, p.q.b_stride, p.q.h_stride);
   a.out_wide = rows16(p.out, p.out_b_stride, p.out_h_stride);
   a.box = p.cache.page_size < UNIT ? p.cache.page_size : UNIT;
+  a.group = p.num_q_heads / p.cache.num_heads;
+  a.tile_tokens = TILE / a.group;
+  a.inv_group = 65536u / (unsigned)a.group + 1u;  // for row < 128 and group <= 128 the excess is below 128 / 2^16 < 1 / group
   CUtensorMap km, vm;
   cudaError_t e = pages_tensor_map(p.cache.k, p.cache, a.box, &km);
   if (e == cudaSuccess) e = pages_tensor_map(p.cache.v, p.cache, a.box, &vm);
