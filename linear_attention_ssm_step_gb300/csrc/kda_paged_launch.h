@@ -24,7 +24,7 @@ bool paged_attention_on_tensor_cores(const kda_paged_cache& c);
 size_t paged_attention_parts_bytes(int head_dim, int ctas);
 
 // Attention on the tensor cores, persistent on `ctas` CTAs (one an SM); cudaErrorNotSupported, with nothing launched,
-// when the cache's strides have no tensor map or a stride of q or out is 2^31 or more.
+// when the cache's strides have no tensor map, a stride of q or out is 2^31 or more, or the work is past 32 bits.
 cudaError_t launch_paged_attention_tc(const kda_attention_params& p, void* workspace, int ctas, cudaStream_t s);
 
 }  // namespace kda

@@ -50,8 +50,8 @@ constexpr int RING = 4;  // segments the walking warp may be ahead
 // What an item costs beside its units (its queries, its end), in units: each item takes LEAD + its units of the line. A
 // first chunk of 4096 tokens, whose items have 1 to 32 units: 168 us at 2, 144 at 4, 148 at 7.
 constexpr int LEAD = 4;
-// Registers a thread after the split: 256 x 216 + 128 x 72 = 384 x 168, what the block launches with.
-constexpr int SOFTMAX_REGS = 216, OTHER_REGS = 72;
+// Registers a thread after the split: 256 x 208 + 128 x 88 = 384 x 168, what the block launches with.
+constexpr int SOFTMAX_REGS = 208, OTHER_REGS = 88;
 
 template <int D>
 struct Shape {
@@ -81,18 +81,13 @@ struct Shared {
   uint64_t v_tail, q_full[2], s_full[2], p_full[2][2], o_done[2], seg_full[RING], seg_empty[RING], drain;
   Segment seg[RING];
   float m1[TILE], l1[TILE];  // the second group's m and l when both groups share a tile
-  long long warp_sum[THREADS / 32];
-  long long start_prefix;
+  int warp_sum[THREADS / 32];
+  AttnRequest start;  // the request in which this CTA's share begins, and its first unit
+  int start_prefix;
   uint32_t tmem;
   int start_request;
   int last_part;
 };
-
-// x y / z for x < 2^31, y <= 1024, z > 0: 32-bit where it fits (a 64-bit division takes over a hundred instructions).
-__device__ __forceinline__ long long mul_div(long long x, int y, long long z) {
-  if (x < (1 << 22) && z < (1LL << 32)) return (uint32_t)((uint32_t)x * (uint32_t)y) / (uint32_t)z;
-  return x * y / z;
-}
 
 // The keys [lo, hi) that item i (tokens i w .. of n, the first at position pos) sees, and its units.
 struct Span {
@@ -111,9 +106,9 @@ __device__ __forceinline__ Span item_span(int pos, int n, int i, int w, int wind
 
 // Length on the line of one key-value head of a request: n tokens, w an item. Called by whole warps, one request a lane; a request
 // of many items (a long chunk) is summed by the warp together.
-__device__ __forceinline__ long long head_units(int pos, int n, int w, int window) {
+__device__ __forceinline__ int head_units(int pos, int n, int w, int window) {
   const int items = (n + w - 1) / w;
-  long long units = 0;
+  int units = 0;
   if (items <= 4)
     for (int i = 0; i < items; ++i) {
       const Span s = item_span(pos, n, i, w, window);
@@ -126,7 +121,7 @@ __device__ __forceinline__ long long head_units(int pos, int n, int w, int windo
     many &= many - 1;
     const int pn = __shfl_sync(0xffffffffu, pos, src), nn = __shfl_sync(0xffffffffu, n, src);
     const int ni = (nn + w - 1) / w;
-    long long part = 0;
+    int part = 0;
     for (int i = lane; i < ni; i += 32) {
       const Span s = item_span(pn, nn, i, w, window);
       part += LEAD + s.u1 - s.u0;
@@ -346,6 +341,10 @@ __device__ __forceinline__ void copy_async16(void* dst, const void* src) {
 }
 __device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
+__device__ __forceinline__ void mbar_init_only(uint64_t* bar, uint32_t count) {  // the fence follows
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(count) : "memory");
+}
+
 __device__ __forceinline__ void prefetch_l2(const void* src) { asm volatile("prefetch.global.L2 [%0];" ::"l"(src)); }
 
 // The thread's number, read again.
@@ -417,57 +416,58 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int tpt = a.tile_tokens, w = 2 * tpt;  // tokens a tile, an item
   const int window = p.window;
 
-  if (tid == 0) {
-    for (int i = 0; i < S::K_STAGES; ++i) {
-      mbar_init(&sh.k_full[i], 1);
-      mbar_init(&sh.k_empty[i], 1);
+  if (warp == 0) {  // a lane a stage: one thread would take a microsecond
+    if (lane < S::K_STAGES) {
+      mbar_init_only(&sh.k_full[lane], 1);
+      mbar_init_only(&sh.k_empty[lane], 1);
     }
-    for (int i = 0; i < S::V_STAGES; ++i) {
-      mbar_init(&sh.v_full[i], 1);
-      mbar_init(&sh.v_empty[i], 1);
+    if (lane < S::V_STAGES) {
+      mbar_init_only(&sh.v_full[lane], 1);
+      mbar_init_only(&sh.v_empty[lane], 1);
     }
-    mbar_init(&sh.v_tail, 1);
-    mbar_init(&sh.drain, 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.q_full[i], TILE);
-      mbar_init(&sh.s_full[i], 1);
-      for (int h = 0; h < 2; ++h) mbar_init(&sh.p_full[i][h], TILE / 32);  // an arrival a warp
-      mbar_init(&sh.o_done[i], 1);
+    if (lane < RING) {
+      mbar_init_only(&sh.seg_full[lane], 1);
+      mbar_init_only(&sh.seg_empty[lane], 5);  // the loading, product and prefetching warps, both softmax groups
     }
-    for (int i = 0; i < RING; ++i) {
-      mbar_init(&sh.seg_full[i], 1);
-      mbar_init(&sh.seg_empty[i], 5);  // the loading, product and prefetching warps, both softmax groups
+    if (lane < 2) {
+      mbar_init_only(&sh.q_full[lane], TILE);
+      mbar_init_only(&sh.s_full[lane], 1);
+      mbar_init_only(&sh.p_full[lane][0], TILE / 32);  // an arrival a warp
+      mbar_init_only(&sh.p_full[lane][1], TILE / 32);
+      mbar_init_only(&sh.o_done[lane], 1);
     }
-    sh.start_request = -1;
+    if (lane == 2) mbar_init_only(&sh.v_tail, 1);
+    if (lane == 3) mbar_init_only(&sh.drain, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  } else if (warp == LOAD_WARP && lane == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&kmap) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&vmap) : "memory");
   }
 
   // ---- this CTA's share of the line of units
-  long long total = 0;
+  int total = 0;
   unsigned bad = 0;
-  long long mine = 0, before = 0;  // the units of this thread's request in the latest block, and those before it
+  AttnRequest mine_r{0, 0, 0, 0u};
+  int mine = 0, before = 0;  // the units of this thread's request in the latest block, and those before it
   const int R = p.num_requests;
   const bool one_block = R <= THREADS;
   auto block_units = [&](int base) {
     const int r = base + tid;
-    int n = 0, pos = 0;
-    if (r < R) {
-      const AttnRequest q = attn_request(p, r);
-      bad |= q.bad;
-      n = q.n;
-      pos = q.kv - q.n;
-    }
-    mine = head_units(pos, n, w, window) * Hkv;
-    long long scan = mine;
+    mine_r = AttnRequest{0, 0, 0, 0u};
+    if (r < R) mine_r = attn_request(p, r);
+    bad |= mine_r.bad;
+    mine = head_units(mine_r.kv - mine_r.n, mine_r.n, w, window) * Hkv;
+    int scan = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, scan, o);
+      const int x = __shfl_up_sync(0xffffffffu, scan, o);
       if (lane >= o) scan += x;
     }
     __syncthreads();
     if (lane == 31) sh.warp_sum[warp] = scan;
     __syncthreads();
     before = scan - mine;
-    long long all = 0;
+    int all = 0;
 #pragma unroll
     for (int i = 0; i < THREADS / 32; ++i) {
       if (i < warp) before += sh.warp_sum[i];
@@ -475,34 +475,32 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     return all;
   };
-  // The requests in one block: their units once. Else once for the sum and once to find where the share begins.
-  int ctas = 0;
+  // The line is shared evenly: the first `rest` CTAs have share + 1 units. Requests in one block are looked at once; else
+  // once for the sum and once to find where this CTA's share begins.
   const int cta = blockIdx.x;
-  long long begin = 0, end = 0;
+  int ctas = 0, share = 0, rest = 0, begin = 0, end = 0;
   for (int pass = one_block ? 1 : 0; pass < 2; ++pass) {
-    long long prefix = 0;
+    int prefix = 0;
     for (int base = 0; base < R; base += THREADS) {
-      const long long all = block_units(base);
+      const int all = block_units(base);
       if (pass == 0 || one_block) total += all;
-      if (pass == 0) continue;
-      if (one_block) {
-        ctas = total < (long long)gridDim.x ? (int)total : (int)gridDim.x;
+      if (pass == 0 && base + THREADS < R) continue;
+      if (pass == 0 || one_block) {
+        ctas = min(total, (int)gridDim.x);
         if (cta >= ctas) break;
-        begin = mul_div(total, cta, ctas);
-        end = mul_div(total, cta + 1, ctas);
+        share = total / ctas;
+        rest = total - share * ctas;
+        begin = cta * share + min(cta, rest);
+        end = begin + share + (cta < rest ? 1 : 0);
       }
-      if (begin >= prefix + before && begin < prefix + before + mine) {
+      if (pass == 1 && begin >= prefix + before && begin < prefix + before + mine) {
+        sh.start = mine_r;
         sh.start_request = base + tid;
         sh.start_prefix = prefix + before;
       }
       prefix += all;
     }
-    if (pass == 0) {
-      ctas = total < (long long)gridDim.x ? (int)total : (int)gridDim.x;
-      if (cta >= ctas) break;
-      begin = mul_div(total, cta, ctas);
-      end = mul_div(total, cta + 1, ctas);
-    }
+    if (cta >= ctas) break;
   }
   if (blockIdx.x == 0 && bad && p.error_word) atomicOr(p.error_word, bad);
   if (cta >= ctas) return;  // the whole CTA: nothing allocated yet
@@ -520,32 +518,31 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (warp == WALK_WARP) {
       // ---- the line of units, cut into segments
       int r = sh.start_request;
-      long long at = begin;
-      long long prefix = sh.start_prefix;  // first unit of the current head's first item
+      int at = begin;
+      int prefix = sh.start_prefix;  // first unit of the current head's first item
       uint32_t out = 0;
       int head = 0, item = 0;
       bool fresh = true;  // the place inside request r is still to be found
       while (alive && at < end && r < R) {
-        const AttnRequest q = attn_request(p, r);
+        const AttnRequest q = fresh ? sh.start : attn_request(p, r);
         const int pos = q.kv - q.n, items = (q.n + w - 1) / w;
         if (fresh) {
           // whole heads first, then 32 items at a time
-          const long long per_head = head_units(pos, lane == 0 ? q.n : 0, w, window);
-          const long long uh = __shfl_sync(0xffffffffu, per_head, 0);
-          head = (int)mul_div(at - prefix, 1, uh);
+          const int uh = __shfl_sync(0xffffffffu, head_units(pos, lane == 0 ? q.n : 0, w, window), 0);
+          head = (at - prefix) / uh;
           prefix += uh * head;
           item = 0;
           for (int base = 0; base < items; base += 32) {
             const int i = base + lane;
-            long long u = 0;
+            int u = 0;
             if (i < items) {
               const Span s = item_span(pos, q.n, i, w, window);
               u = LEAD + s.u1 - s.u0;
             }
-            long long scan = u;
+            int scan = u;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-              const long long x = __shfl_up_sync(0xffffffffu, scan, o);
+              const int x = __shfl_up_sync(0xffffffffu, scan, o);
               if (lane >= o) scan += x;
             }
             const bool here = i < items && prefix + scan > at;
@@ -563,8 +560,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         // `prefix` is the first unit of item `item` of head `head`
         while (alive && at < end && head < Hkv && items > 0) {
           const Span s = item_span(pos, q.n, item, w, window);
-          const long long units0 = prefix + LEAD, item_end = units0 + (s.u1 - s.u0);
-          const long long from = at > units0 ? at : units0, stop = end < item_end ? end : item_end;
+          const int units0 = prefix + LEAD, item_end = units0 + (s.u1 - s.u0);
+          const int from = max(at, units0), stop = min(end, item_end);
           at = stop;
           prefix = item_end;
           const int i = item;
@@ -581,11 +578,15 @@ __global__ void __launch_bounds__(THREADS, 1)
           g2.request = r;
           g2.lo = s.lo;
           g2.hi = s.hi;
-          g2.u0 = s.u0 + (int)(from - units0);
-          g2.u1 = s.u0 + (int)(stop - units0);
+          g2.u0 = s.u0 + (from - units0);
+          g2.u1 = s.u0 + (stop - units0);
           g2.dual = g2.ntok > tpt;
-          // the CTA that holds unit x of the line: the last whose share begins at or before it
-          auto holder = [&](long long x) { return x >= begin && x < end ? cta : (int)(((x + 1) * ctas - 1) / total); };
+          // the CTA that holds unit x of the line
+          auto holder = [&](int x) {
+            if (x >= begin && x < end) return cta;
+            const int longer = rest * (share + 1);
+            return x < longer ? x / (share + 1) : rest + (x - longer) / share;
+          };
           g2.cta0 = holder(units0);
           g2.parts = holder(item_end - 1) - g2.cta0 + 1;
           g2.part = cta - g2.cta0;
@@ -905,12 +906,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (!(bits >> i & 1u)) s[b + i] = 0xff800000u;  // -inf
             }
           }
-          // The first weights by the reference so far, and beside them (in another pipe) the maximum: only if that has
-          // grown past the slack are they formed again.
           const uint64_t c2 = pair(c, c);
           uint64_t sum[4] = {0, 0, 0, 0}, base2 = reference(m, c);
           uint32_t wa[16];
-          weights<32>(s, c2, base2, sum, wa);
           float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
           for (int i = 0; i < UNIT; i += 8)
@@ -935,10 +933,8 @@ __global__ void __launch_bounds__(THREADS, 1)
               }
             }
             base2 = reference(m, c);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) sum[j] = 0;
-            weights<32>(s, c2, base2, sum, wa);
           }
+          weights<32>(s, c2, base2, sum, wa);
           auto give = [&](int h) {  // these weights are there: the products that take them may start
             tmem_st_wait();
             tc_fence_before();
@@ -1217,6 +1213,12 @@ static cudaError_t launch_tc(const CUtensorMap& km, const CUtensorMap& vm, const
 
 cudaError_t launch_paged_attention_tc(const kda_attention_params& p, void* workspace, int ctas, cudaStream_t s) {
   if ((p.q.b_stride | p.q.h_stride | p.out_b_stride | p.out_h_stride) >> 31) return cudaErrorNotSupported;
+  // the line of units is counted in 32 bits: at most so many items of so many units a key-value head
+  const long long tokens = 2 * (TILE / (p.num_q_heads / p.cache.num_heads));
+  long long keys = (long long)p.table_width * p.cache.page_size;
+  if (p.window > 0 && p.window + tokens < keys) keys = p.window + tokens;
+  const long long items = p.num_tokens / tokens + p.num_requests;
+  if (items * (keys / UNIT + 2 + LEAD) > 0x7fffffffLL / p.cache.num_heads) return cudaErrorNotSupported;
   AttnArgs a;
   a.p = p;
   a.counters = static_cast<unsigned*>(workspace);
