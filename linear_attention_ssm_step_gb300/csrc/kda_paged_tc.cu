@@ -992,8 +992,20 @@ __global__ void __launch_bounds__(THREADS, 1)
       const float inv = rcp(l);
       float* const other = reinterpret_cast<float*>(smem + S::Q1);  // the second group's O, half the columns at a time
       const bool two = !dual && sg.u1 - sg.u0 > 1;  // the second group has one
+      // 32 columns of this thread's row, scaled, into the tile's own queries' place, which the products are done with.
+      auto stage = [&](const float (&f)[32], int col, float scale, bool zero) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t b[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            b[e] = zero ? 0u : pack_bf16x2(f[8 * j + 2 * e] * scale, f[8 * j + 2 * e + 1] * scale);
+          const uint32_t ch = col / 8 + j;
+          *reinterpret_cast<uint4*>(tile + (ch >> 3) * (TILE * 128) + x * 128 + (((ch ^ x) & 7) << 4)) =
+              make_uint4(b[0], b[1], b[2], b[3]);
+        }
+      };
       // 32 columns at a time, in a loop that is not unrolled: this runs once a run, and its instructions come from afar
-      const uint32_t tile_at = (uint32_t)(x * 128);
 #pragma unroll 1
       for (int col = 0; col < D; col += 32) {
         float* const o1 = other + (col & (D / 2 - 1)) * TILE + x;
@@ -1012,17 +1024,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (D == 64 || col == 32) bar_sync(2, SOFTMAX_THREADS);  // half the columns fill the buffer
         }
         if (writes) {
-          if (direct) {  // into the tile's own queries' place, which the products are done with
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              uint32_t b[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                b[e] = none ? 0u : pack_bf16x2(f[8 * j + 2 * e] * inv, f[8 * j + 2 * e + 1] * inv);
-              const uint32_t ch = col / 8 + j;
-              *reinterpret_cast<uint4*>(tile + (ch >> 3) * (TILE * 128) + tile_at + (((ch ^ x) & 7) << 4)) =
-                  make_uint4(b[0], b[1], b[2], b[3]);
-            }
+          if (direct) {
+            stage(f, col, inv, none);
           } else {
             float4* const o = part_o<D>(a, slot_id) + (col / 4) * (2 * TILE) + part_row;
 #pragma unroll
@@ -1031,7 +1034,139 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
       tc_fence_before();
-      if (direct && (dual || t == 0)) {
+      bool whole = direct;  // the rows' outputs are in shared memory
+      if (!direct) {
+        if (writes) part_ml<D>(a, slot_id)[part_row] = make_float2(m, l);
+        __threadfence();
+        bar_sync(1, SOFTMAX_THREADS);
+        if (tid == 0) {
+          const unsigned done = atomicAdd(&a.counters[sg.cta0], 1u);
+          sh.last_part = done + 1 == (unsigned)sg.parts;
+          if (sh.last_part) a.counters[sg.cta0] = 0;
+          __threadfence();
+        }
+        bar_sync(2, SOFTMAX_THREADS);
+        // The last to arrive joins the parts, in their order: many rows a thread each, few rows over all threads.
+        auto slot_of = [&](int q) { return q == 0 ? 2 * sg.cta0 + 1 : 2 * (sg.cta0 + q); };
+        auto joined_ml = [&](int r) {  // a row's maximum and sum
+          float mm = -INFINITY, ll = 0.f;
+#pragma unroll 1
+          for (int q = 0; q < sg.parts; q += 8) {
+            float2 z[8];
+            float top = mm;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              z[i] = q + i < sg.parts ? __ldcg(part_ml<D>(a, slot_of(q + i)) + r) : make_float2(-INFINITY, 0.f);
+              top = fmaxf(top, z[i].x);
+            }
+            const float mb = top == -INFINITY ? 0.f : top;
+            ll *= ex2((mm - mb) * c);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ll = fmaf(z[i].y, ex2((z[i].x - mb) * c), ll);
+            mm = top;
+          }
+          return make_float2(mm, ll);
+        };
+        if (sh.last_part) __threadfence();
+        if (sh.last_part && (dual || sg.ntok * g > TILE / 2)) {
+          whole = true;
+          if (writes) {
+            const float2 z = joined_ml(part_row);
+            m = z.x;
+            l = z.y;
+            const float mb = m == -INFINITY ? 0.f : m, scale = rcp(l);
+#pragma unroll 1
+            for (int col = 0; col < D; col += 32) {
+              float f[32];
+#pragma unroll
+              for (int j = 0; j < 32; ++j) f[j] = 0.f;
+#pragma unroll 1
+              for (int q = 0; q < sg.parts; ++q) {
+                const int sid = slot_of(q);
+                const float4* const o = part_o<D>(a, sid) + (col / 4) * (2 * TILE) + part_row;
+                float4 v[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = __ldcg(o + j * (2 * TILE));
+                const float w = ex2((__ldcg(&part_ml<D>(a, sid)[part_row].x) - mb) * c);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                  f[4 * j] = fmaf(v[j].x, w, f[4 * j]);
+                  f[4 * j + 1] = fmaf(v[j].y, w, f[4 * j + 1]);
+                  f[4 * j + 2] = fmaf(v[j].z, w, f[4 * j + 2]);
+                  f[4 * j + 3] = fmaf(v[j].w, w, f[4 * j + 3]);
+                }
+              }
+              stage(f, col, scale, l == 0.f);
+            }
+          }
+        } else if (sh.last_part) {
+          const int rows = sg.ntok * g;  // of one tile
+          float* const jm = reinterpret_cast<float*>(smem + S::Q0);  // the queries are done with
+          float* const jl = jm + TILE;
+          if (tid < rows) {
+            const float2 z = joined_ml(tid);
+            jm[tid] = z.x == -INFINITY ? 0.f : z.x;
+            jl[tid] = z.y;
+            if (p.lse != nullptr)
+              p.lse[((int64_t)sg.row0 + div_g(tid)) * p.num_q_heads + sg.head * g + (tid - div_g(tid) * g)] =
+                  z.x == -INFINITY ? -INFINITY : z.x * p.scale + ln(z.y);
+          }
+          bar_sync(1, SOFTMAX_THREADS);
+          // then four columns of a row at a time; `pad` rows a group of columns, so that neighbours read neighbours
+          const int pad = (rows + 7) & ~7;
+          constexpr int U = 2;
+#pragma unroll 1
+          for (int i0 = tid; i0 < pad * (D / 4); i0 += U * SOFTMAX_THREADS) {
+            float acc[U][4];
+            int at[U];
+            float mb[U];
+            bool on[U];
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+              const int i = i0 + k * SOFTMAX_THREADS;
+              const int col = i / pad, row2 = i - col * pad;
+              on[k] = col < D / 4 && row2 < rows;
+              at[k] = on[k] ? col * (2 * TILE) + row2 : 0;
+              mb[k] = on[k] ? jm[row2] : 0.f;
+              acc[k][0] = acc[k][1] = acc[k][2] = acc[k][3] = 0.f;
+            }
+#pragma unroll 4
+            for (int q = 0; q < sg.parts; ++q) {
+              const int sid = slot_of(q);
+#pragma unroll
+              for (int k = 0; k < U; ++k) {
+                if (!on[k]) continue;
+                const float4 v = __ldcg(part_o<D>(a, sid) + at[k]);
+                const float f = ex2((__ldcg(&part_ml<D>(a, sid)[at[k] % (2 * TILE)].x) - mb[k]) * c);
+                acc[k][0] = fmaf(v.x, f, acc[k][0]);
+                acc[k][1] = fmaf(v.y, f, acc[k][1]);
+                acc[k][2] = fmaf(v.z, f, acc[k][2]);
+                acc[k][3] = fmaf(v.w, f, acc[k][3]);
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+              if (!on[k]) continue;
+              const int row2 = at[k] % (2 * TILE), col = at[k] / (2 * TILE) * 4;
+              const float ll = jl[row2], iv = rcp(ll);
+              uint16_t* const dst = static_cast<uint16_t*>(p.out) + (int64_t)sg.row0 * p.out_b_stride +
+                                    (int64_t)(sg.head * g) * p.out_h_stride +
+                                    row_offset(row2, p.out_b_stride, p.out_h_stride) + col;
+              const uint32_t b0 = ll == 0.f ? 0u : pack_bf16x2(acc[k][0] * iv, acc[k][1] * iv);
+              const uint32_t b1 = ll == 0.f ? 0u : pack_bf16x2(acc[k][2] * iv, acc[k][3] * iv);
+              if (a.out_wide) {
+                *reinterpret_cast<uint2*>(dst) = make_uint2(b0, b1);
+              } else {
+                dst[0] = (uint16_t)b0;
+                dst[1] = (uint16_t)(b0 >> 16);
+                dst[2] = (uint16_t)b1;
+                dst[3] = (uint16_t)(b1 >> 16);
+              }
+            }
+          }
+        }
+      }
+      if (whole && (dual || t == 0)) {
         if (t == 0)
           bar_sync(3, TILE);
         else
@@ -1063,115 +1198,9 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
         }
       }
-      if (writes) {
-        if (direct) {
-          const Row r = my_row();
-          if (p.lse != nullptr)
-            p.lse[((int64_t)sg.row0 + r.tok) * p.num_q_heads + sg.head * g + (x - div_g(x) * g)] =
-                m == -INFINITY ? -INFINITY : m * p.scale + ln(l);
-        } else {
-          part_ml<D>(a, slot_id)[part_row] = make_float2(m, l);
-        }
-      }
-      if (!direct) {
-        __threadfence();
-        bar_sync(1, SOFTMAX_THREADS);
-        if (tid == 0) {
-          const unsigned done = atomicAdd(&a.counters[sg.cta0], 1u);
-          sh.last_part = done + 1 == (unsigned)sg.parts;
-          if (sh.last_part) a.counters[sg.cta0] = 0;
-          __threadfence();
-        }
-        bar_sync(2, SOFTMAX_THREADS);
-        if (sh.last_part) {
-          // join the parts in their order; first every row's maximum and sum, a thread a row
-          __threadfence();
-          auto slot_of = [&](int q) { return q == 0 ? 2 * sg.cta0 + 1 : 2 * (sg.cta0 + q); };
-          const int rows = dual ? TILE + (sg.ntok - tpt) * g : sg.ntok * g;
-          float* const jm = reinterpret_cast<float*>(smem + S::Q0);  // the queries are done with
-          float* const jl = jm + 2 * TILE;
-          const bool is_row = tid < rows && tid % TILE < tpt * g;
-          if (is_row) {
-            float mm = -INFINITY, ll = 0.f;
-            for (int q = 0; q < sg.parts; q += 8) {
-              float2 z[8];
-              float top = mm;
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                z[i] = q + i < sg.parts ? __ldcg(part_ml<D>(a, slot_of(q + i)) + tid) : make_float2(-INFINITY, 0.f);
-                top = fmaxf(top, z[i].x);
-              }
-              const float mb = top == -INFINITY ? 0.f : top;
-              ll *= ex2((mm - mb) * c);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) ll = fmaf(z[i].y, ex2((z[i].x - mb) * c), ll);
-              mm = top;
-            }
-            jm[tid] = mm == -INFINITY ? 0.f : mm;
-            jl[tid] = ll;
-            if (p.lse != nullptr) {
-              const int tk = tid % TILE / g;
-              const int64_t orow = (int64_t)sg.row0 + tid / TILE * tpt + tk;
-              p.lse[orow * p.num_q_heads + sg.head * g + (tid % TILE - tk * g)] =
-                  mm == -INFINITY ? -INFINITY : mm * p.scale + ln(ll);
-            }
-          }
-          bar_sync(1, SOFTMAX_THREADS);
-          // then four columns of a row at a time; `pad` rows a group of columns, so that neighbours read neighbours
-          const int pad = (rows + 7) & ~7;
-          constexpr int U = 4;
-#pragma unroll 1
-          for (int i0 = tid; i0 < pad * (D / 4); i0 += U * SOFTMAX_THREADS) {
-            float acc[U][4];
-            int at[U];
-            float mb[U];
-            bool on[U];
-#pragma unroll
-            for (int k = 0; k < U; ++k) {
-              const int i = i0 + k * SOFTMAX_THREADS;
-              const int col = i / pad, row2 = i - col * pad;
-              on[k] = col < D / 4 && row2 < rows && row2 % TILE < tpt * g;
-              at[k] = on[k] ? col * (2 * TILE) + row2 : 0;
-              mb[k] = on[k] ? jm[row2] : 0.f;
-              acc[k][0] = acc[k][1] = acc[k][2] = acc[k][3] = 0.f;
-            }
-#pragma unroll 2
-            for (int q = 0; q < sg.parts; ++q) {
-              const int sid = slot_of(q);
-#pragma unroll
-              for (int k = 0; k < U; ++k) {
-                if (!on[k]) continue;
-                const float4 v = __ldcg(part_o<D>(a, sid) + at[k]);
-                const float f = ex2((__ldcg(&part_ml<D>(a, sid)[at[k] % (2 * TILE)].x) - mb[k]) * c);
-                acc[k][0] = fmaf(v.x, f, acc[k][0]);
-                acc[k][1] = fmaf(v.y, f, acc[k][1]);
-                acc[k][2] = fmaf(v.z, f, acc[k][2]);
-                acc[k][3] = fmaf(v.w, f, acc[k][3]);
-              }
-            }
-#pragma unroll
-            for (int k = 0; k < U; ++k) {
-              if (!on[k]) continue;
-              const int row2 = at[k] % (2 * TILE), col = at[k] / (2 * TILE) * 4;
-              const float ll = jl[row2], iv = rcp(ll);
-              const int tk = row2 % TILE / g;
-              const int64_t orow = (int64_t)sg.row0 + row2 / TILE * tpt + tk;
-              const int oh = sg.head * g + (row2 % TILE - tk * g);
-              uint16_t* const dst = static_cast<uint16_t*>(p.out) + orow * p.out_b_stride + (int64_t)oh * p.out_h_stride + col;
-              const uint32_t b0 = ll == 0.f ? 0u : pack_bf16x2(acc[k][0] * iv, acc[k][1] * iv);
-              const uint32_t b1 = ll == 0.f ? 0u : pack_bf16x2(acc[k][2] * iv, acc[k][3] * iv);
-              if (a.out_wide) {
-                *reinterpret_cast<uint2*>(dst) = make_uint2(b0, b1);
-              } else {
-                dst[0] = (uint16_t)b0;
-                dst[1] = (uint16_t)(b0 >> 16);
-                dst[2] = (uint16_t)b1;
-                dst[3] = (uint16_t)(b1 >> 16);
-              }
-            }
-          }
-        }
-      }
+      if (whole && writes && p.lse != nullptr)
+        p.lse[((int64_t)sg.row0 + (dual ? t * tpt : 0) + div_g(x)) * p.num_q_heads + sg.head * g + (x - div_g(x) * g)] =
+            m == -INFINITY ? -INFINITY : m * p.scale + ln(l);
       if (t == 0)
         bar_sync(3, TILE);
       else
