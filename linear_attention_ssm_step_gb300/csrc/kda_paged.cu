@@ -63,6 +63,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) kda_paged_plan_kernel(kda_plan_p
   __shared__ long long warp_rows[PLAN_THREADS / 32], warp_need[PLAN_THREADS / 32];
   __shared__ int taken_all, bad_all;
   if (tid == 0) taken_all = bad_all = 0;
+  next_may_start();
+  earlier_work();
   const int free_now = min(max(*p.free_count, 0), p.free_capacity);
   __syncthreads();
 
@@ -178,20 +180,23 @@ cudaError_t launch_paged_plan(const kda_plan_params& p, cudaStream_t s) {
   const cudaError_t e =
       set_smem_limit_once(kda_paged_plan_kernel, (3 * KDA_MAX_REQUESTS + 2) * sizeof(int32_t), done);
   if (e != cudaSuccess) return e;
-  kda_paged_plan_kernel<<<grid, PLAN_THREADS, smem, s>>>(p);
-  return cudaGetLastError();
+  return launch_early(kda_paged_plan_kernel, dim3((unsigned)grid), PLAN_THREADS, smem, s, p);
 }
 
 // ---------------------------------------------------------------- rotary positions and append
 //
 // One CTA per row: its rotary_dim / 2 sines and cosines are formed once, in
 // shared memory, for all query and key heads of the row (a sincos costs more
-// than the traffic of the pair it turns). The rest is a copy: a thread moves
-// two runs of VEC values, the two halves of VEC pairs when the halves are
-// paired, 2 VEC consecutive values else; VEC = 8 (16-byte accesses) when every
-// row allows it, 1 otherwise.
+// than the traffic of the pair it turns). The rest is a copy, bound by memory:
+// a thread moves two runs of VEC values, the two halves of VEC pairs when the
+// halves are paired, 2 VEC consecutive values else; VEC = 8 (16-byte accesses)
+// when every row allows it, 1 otherwise. What a row waits for (its position,
+// its values) is covered by the other rows of the SM: with one task a thread in
+// flight and 16 CTAs an SM, 8192 rows of 32 + 8 + 8 heads of 128 take 34.9 us
+// (5.8 TB/s of reads and writes, 85 % of a plain copy); three tasks in flight
+// need 56 registers, 9 CTAs an SM and 42.6 us; 256 threads a row 39 us.
 
-constexpr int ROPE_THREADS = 128;
+constexpr int ROPE_THREADS = 128, ROPE_CTAS = 16;  // a full SM: 32 registers a thread
 
 template <int VEC>
 struct alignas(2 * VEC) Run {
@@ -216,95 +221,111 @@ __device__ __forceinline__ void store_run(uint16_t* p, const Run<VEC>& r) {
     *p = r.x[0];
 }
 
+// One task: a run of VEC values at `a` and one at `b` of a head, turned or not.
 template <int VEC>
-__global__ void __launch_bounds__(ROPE_THREADS) kda_rope_append_kernel(kda_rope_params p) {
+struct RopeTask {
+  const uint16_t* src;
+  uint16_t* dst;
+  int a, b, c;    // c: the first pair's run, -1 when nothing turns
+  bool two;       // an odd head_dim ends in a single value (VEC == 1)
+  Run<VEC> ra, rb;
+};
+
+template <int VEC>
+__global__ void __launch_bounds__(ROPE_THREADS, ROPE_CTAS) kda_rope_append_kernel(kda_rope_params p) {
   __shared__ float2 turn[128];  // mscale (cos, sin) of pair i
   const int t = blockIdx.x, tid = threadIdx.x;
-  const int pos = p.positions[t];
-  if (pos < 0) return;
-  const int slot = p.slots[t];
   const int half = p.rotary_dim >> 1, D = p.cache.head_dim;
-  for (int i = tid; i < half; i += ROPE_THREADS) {
+  const int Hq = p.num_q_heads, Hkv = p.cache.num_heads;
+  const int per_head = (D + 2 * VEC - 1) / (2 * VEC), tasks = (Hq + 2 * Hkv) * per_head;
+  next_may_start();
+  earlier_work();
+  const int pos = p.positions[t], slot = p.slots[t];
+  const uint64_t freq = tid < half ? p.freqs[tid] : 0u;
+  const uint16_t* const qi = static_cast<const uint16_t*>(p.q.ptr) + (int64_t)t * p.q.b_stride;
+  const uint16_t* const ki = static_cast<const uint16_t*>(p.k.ptr) + (int64_t)t * p.k.b_stride;
+  const uint16_t* const vi = static_cast<const uint16_t*>(p.v.ptr) + (int64_t)t * p.v.b_stride;
+  // Per head D / (2 VEC) tasks (rounded up): first the pairs, then what passes unchanged.
+  RopeTask<VEC> j;
+  auto load = [&](int i) {
+    const int h = i / per_head, c = i - h * per_head;
+    j.src = h < Hq ? qi + (int64_t)h * p.q.h_stride
+                   : h < Hq + Hkv ? ki + (int64_t)(h - Hq) * p.k.h_stride : vi + (int64_t)(h - Hq - Hkv) * p.v.h_stride;
+    j.c = h < Hq + Hkv && c * VEC < half ? c * VEC : -1;
+    j.a = 2 * c * VEC;
+    j.b = j.a + VEC;
+    if (j.c >= 0 && !p.interleaved) {
+      j.a = j.c;
+      j.b = j.a + half;
+    }
+    j.two = j.b < D;
+    j.ra = load_run<VEC>(j.src + j.a);
+    j.rb = j.ra;
+    if (j.two) j.rb = load_run<VEC>(j.src + j.b);
+  };
+  // The first task's values are asked for before the position is known.
+  if (tid < tasks) load(tid);
+
+  if (pos < 0) return;
+  if (tid < half) {  // half <= 128 = ROPE_THREADS
     // the exact phase in 2^-64 turns; its upper 32 bits as a signed number of half turns
-    const uint64_t phase = (uint64_t)(uint32_t)pos * p.freqs[i];
+    const uint64_t phase = (uint64_t)(uint32_t)pos * freq;
     float sn, cs;
     sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &sn, &cs);
-    turn[i] = make_float2(p.mscale * cs, p.mscale * sn);
+    turn[tid] = make_float2(p.mscale * cs, p.mscale * sn);
   }
-  __syncthreads();
-
-  const long long size = p.cache.page_size, slots = (long long)p.cache.num_pages * size;
+  const long long slots = (long long)p.cache.num_pages * p.cache.page_size;
   const bool append = slot >= 0 && slot < slots;
   if (!append && slot != -1 && tid == 0 && p.error_word) atomicOr(p.error_word, KDA_ERR_PAGES);
   const int64_t page = append ? slot / p.cache.page_size : 0, off = append ? slot % p.cache.page_size : 0;
   uint16_t* const ck = static_cast<uint16_t*>(p.cache.k.ptr) + page * p.cache.k.page_stride + off * p.cache.k.token_stride;
   uint16_t* const cv = static_cast<uint16_t*>(p.cache.v.ptr) + page * p.cache.v.page_stride + off * p.cache.v.token_stride;
-  const uint16_t* const qi = static_cast<const uint16_t*>(p.q.ptr) + (int64_t)t * p.q.b_stride;
-  const uint16_t* const ki = static_cast<const uint16_t*>(p.k.ptr) + (int64_t)t * p.k.b_stride;
-  const uint16_t* const vi = static_cast<const uint16_t*>(p.v.ptr) + (int64_t)t * p.v.b_stride;
   uint16_t* const qo = static_cast<uint16_t*>(p.q_out) + (int64_t)t * p.q_out_b_stride;
+  __syncthreads();
 
-  // Per head D / (2 VEC) tasks (rounded up): first the pairs, then what passes unchanged.
-  const int Hq = p.num_q_heads, Hkv = p.cache.num_heads;
-  const int per_head = (D + 2 * VEC - 1) / (2 * VEC);
-  const int tasks = (Hq + (append ? 2 * Hkv : 0)) * per_head;
-  for (int i = tid; i < tasks; i += ROPE_THREADS) {
-    const int h = i / per_head, c = i - h * per_head;
-    const uint16_t* src;
-    uint16_t* dst;
-    if (h < Hq) {
-      src = qi + (int64_t)h * p.q.h_stride;
-      dst = qo + (int64_t)h * p.q_out_h_stride;
-    } else if (h < Hq + Hkv) {
-      src = ki + (int64_t)(h - Hq) * p.k.h_stride;
-      dst = ck + (int64_t)(h - Hq) * p.cache.k.head_stride;
-    } else {
-      src = vi + (int64_t)(h - Hq - Hkv) * p.v.h_stride;
-      dst = cv + (int64_t)(h - Hq - Hkv) * p.cache.v.head_stride;
-    }
-    const bool turned = h < Hq + Hkv && c * VEC < half;
-    int a = 2 * c * VEC, b = a + VEC;
-    if (turned && !p.interleaved) {
-      a = c * VEC;
-      b = a + half;
-    }
-    const bool two = b < D;  // an odd head_dim ends in a single value (VEC == 1)
-    Run<VEC> ra = load_run<VEC>(src + a), rb = ra;
-    if (two) rb = load_run<VEC>(src + b);
-    if (turned) {
+  auto finish = [&](int i) {
+    const int h = i / per_head;
+    if (h >= Hq && !append) return;
+    j.dst = h < Hq ? qo + (int64_t)h * p.q_out_h_stride
+                   : h < Hq + Hkv ? ck + (int64_t)(h - Hq) * p.cache.k.head_stride
+                                  : cv + (int64_t)(h - Hq - Hkv) * p.cache.v.head_stride;
+    if (j.c >= 0) {
       if (VEC == 8 && p.interleaved) {
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-          const float2 u = turn[(a + j) >> 1], w = turn[(b + j) >> 1];
-          const int j1 = VEC == 8 ? j + 1 : 0, j0 = VEC == 8 ? j : 0;
-          const float xa = bf16_bits_to_float(ra.x[j0]), ya = bf16_bits_to_float(ra.x[j1]);
-          ra.x[j0] = float_to_bf16_bits(xa * u.x - ya * u.y);
-          ra.x[j1] = float_to_bf16_bits(ya * u.x + xa * u.y);
-          const float xb = bf16_bits_to_float(rb.x[j0]), yb = bf16_bits_to_float(rb.x[j1]);
-          rb.x[j0] = float_to_bf16_bits(xb * w.x - yb * w.y);
-          rb.x[j1] = float_to_bf16_bits(yb * w.x + xb * w.y);
+        for (int e = 0; e < 8; e += 2) {
+          const int e0 = VEC == 8 ? e : 0, e1 = VEC == 8 ? e + 1 : 0;
+          const float2 u = turn[(j.a + e) >> 1], w = turn[(j.b + e) >> 1];
+          const float xa = bf16_bits_to_float(j.ra.x[e0]), ya = bf16_bits_to_float(j.ra.x[e1]);
+          j.ra.x[e0] = float_to_bf16_bits(xa * u.x - ya * u.y);
+          j.ra.x[e1] = float_to_bf16_bits(ya * u.x + xa * u.y);
+          const float xb = bf16_bits_to_float(j.rb.x[e0]), yb = bf16_bits_to_float(j.rb.x[e1]);
+          j.rb.x[e0] = float_to_bf16_bits(xb * w.x - yb * w.y);
+          j.rb.x[e1] = float_to_bf16_bits(yb * w.x + xb * w.y);
         }
       } else {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          const float2 u = turn[c * VEC + j];
-          const float x = bf16_bits_to_float(ra.x[j]), y = bf16_bits_to_float(rb.x[j]);
-          ra.x[j] = float_to_bf16_bits(x * u.x - y * u.y);
-          rb.x[j] = float_to_bf16_bits(y * u.x + x * u.y);
+        for (int e = 0; e < VEC; ++e) {
+          const float2 u = turn[j.c + e];
+          const float x = bf16_bits_to_float(j.ra.x[e]), y = bf16_bits_to_float(j.rb.x[e]);
+          j.ra.x[e] = float_to_bf16_bits(x * u.x - y * u.y);
+          j.rb.x[e] = float_to_bf16_bits(y * u.x + x * u.y);
         }
       }
     }
-    store_run<VEC>(dst + a, ra);
-    if (two) store_run<VEC>(dst + b, rb);
+    store_run<VEC>(j.dst + j.a, j.ra);
+    if (j.two) store_run<VEC>(j.dst + j.b, j.rb);
+  };
+  for (int i = tid; i < tasks;) {
+    finish(i);
+    i += ROPE_THREADS;
+    if (i < tasks) load(i);
   }
 }
 
 cudaError_t launch_rope_append(const kda_rope_params& p, bool wide, cudaStream_t s) {
-  if (wide)
-    kda_rope_append_kernel<8><<<p.num_tokens, ROPE_THREADS, 0, s>>>(p);
-  else
-    kda_rope_append_kernel<1><<<p.num_tokens, ROPE_THREADS, 0, s>>>(p);
-  return cudaGetLastError();
+  const dim3 grid((unsigned)p.num_tokens);
+  return wide ? launch_early(kda_rope_append_kernel<8>, grid, ROPE_THREADS, 0, s, p)
+              : launch_early(kda_rope_append_kernel<1>, grid, ROPE_THREADS, 0, s, p);
 }
 
 // ---------------------------------------------------------------- attention on the CUDA cores
@@ -325,6 +346,8 @@ __global__ void __launch_bounds__(ATTN_WARPS * 32) kda_paged_attention_simt_kern
   const uint16_t* const kc = static_cast<const uint16_t*>(p.cache.k.ptr);
   const uint16_t* const vc = static_cast<const uint16_t*>(p.cache.v.ptr);
   const int r = blockIdx.y;
+  next_may_start();
+  earlier_work();
   const AttnRequest q = attn_request(p, r);
   if (blockIdx.x == 0 && threadIdx.x == 0 && q.bad && p.error_word) atomicOr(p.error_word, q.bad);
   const int32_t* const table = p.table + (int64_t)r * p.table_stride;
@@ -395,8 +418,7 @@ cudaError_t launch_paged_attention_simt(const kda_attention_params& p, cudaStrea
   const long long rows = (long long)p.num_tokens * p.num_q_heads;
   long long per = rows / ((long long)ATTN_WARPS * p.num_requests) + 1;
   const dim3 grid((unsigned)(per > 4096 ? 4096 : per), (unsigned)p.num_requests);
-  kda_paged_attention_simt_kernel<<<grid, ATTN_WARPS * 32, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_early(kda_paged_attention_simt_kernel, grid, ATTN_WARPS * 32, 0, s, p);
 }
 
 }  // namespace kda

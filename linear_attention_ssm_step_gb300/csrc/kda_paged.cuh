@@ -6,6 +6,13 @@
 
 namespace kda {
 
+// The kernels of a step follow one another closely (plan, then per layer append and attention), and the small ones are
+// over in a few microseconds, so each is launched while the kernel before it still runs (launch_early) and waits here for
+// it before it touches memory. earlier_work(): everything before in the stream is done and visible. next_may_start(): the
+// next such kernel may be brought in once every CTA of this one has come so far.
+__device__ __forceinline__ void earlier_work() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void next_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // One request's rows and keys after the checks: n rows from row0 on, kv keys,
 // row j at position kv - n + j. A request with bad row bounds has n = 0.
 struct AttnRequest {
@@ -25,6 +32,22 @@ __device__ __forceinline__ AttnRequest attn_request(const kda_attention_params& 
     q.kv = 0;
   }
   return q;
+}
+
+// Launches a kernel that begins with earlier_work(), allowing it to be brought in early.
+template <typename... Params, typename... Args>
+inline cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t s, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
 }
 
 }  // namespace kda

@@ -444,6 +444,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     asm volatile("prefetch.tensormap [%0];" ::"l"(&vmap) : "memory");
   }
 
+  next_may_start();
+  earlier_work();
+
   // ---- this CTA's share of the line of units
   int total = 0;
   unsigned bad = 0;
@@ -1236,8 +1239,7 @@ static cudaError_t launch_tc(const CUtensorMap& km, const CUtensorMap& vm, const
   static std::atomic<bool> done{false};
   const cudaError_t e = set_smem_limit_once(kda_paged_attention_tc_kernel<D>, bytes, done);
   if (e != cudaSuccess) return e;
-  kda_paged_attention_tc_kernel<D><<<ctas, THREADS, bytes, s>>>(km, vm, a);
-  return cudaGetLastError();
+  return launch_early(kda_paged_attention_tc_kernel<D>, dim3((unsigned)ctas), THREADS, bytes, s, km, vm, a);
 }
 
 cudaError_t launch_paged_attention_tc(const kda_attention_params& p, void* workspace, int ctas, cudaStream_t s) {
