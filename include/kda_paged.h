@@ -93,7 +93,7 @@ typedef struct {
   const int32_t* new_len;    /* [num_requests] */
   int32_t* table;            /* [num_requests][table_width], updated in place */
   int64_t table_stride;      /* elements between requests, >= table_width */
-  int32_t table_width;       /* >= 1 */
+  int32_t table_width;       /* >= 1; table_width * page_size <= 2^31 - 256 */
   const int32_t* free_pages; /* [free_capacity] */
   int32_t free_capacity;     /* >= 0 */
   const int32_t* free_count; /* [1] */
@@ -185,7 +185,8 @@ kda_status kda_rope_freqs(uint64_t* freqs, int32_t rotary_dim, double base, int3
  * head_dim 64 or 128 with a page size that is a power of two from 16 on and
  * 16-byte aligned cache rows (pointers, and strides that are multiples of 8)
  * runs on the tensor cores; any other cache (head_dim 1..256) on the CUDA
- * cores, slower.
+ * cores, slower (as do strides of q or out of 2^31 elements or more, and work
+ * past 2^31 tiles of 256 rows by 128 keys).
  *
  * workspace: kda_paged_attention_workspace_bytes(head_dim) bytes of device
  * memory, 16-byte aligned, the caller's own, overlapping no other argument.
@@ -210,7 +211,7 @@ typedef struct {
   const int32_t* kv_len; /* [num_requests] */
   const int32_t* table;  /* [num_requests][table_width] */
   int64_t table_stride;
-  int32_t table_width;   /* >= 1 */
+  int32_t table_width;   /* >= 1; table_width * cache.page_size <= 2^31 - 256 */
   kda_paged_cache cache; /* read */
   uint32_t* error_word;  /* optional */
 } kda_attention_params;

@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(ATTN_WARPS * 32) kda_paged_attention_simt_kern
     __syncwarp();
     for (int c = lane; c < D; c += 32) qs[warp][c] = bf16_bits_to_float(qr[c]);
     __syncwarp();
-    const int lo = p.window > 0 ? max(0, pos - p.window + 1) : 0, hi = pos + 1;  // keys [lo, hi)
+    const int lo = first_key(pos, p.window), hi = pos + 1;  // keys [lo, hi)
     float m = -INFINITY, l = 0.f, acc[ATTN_MAX_D / 32];
 #pragma unroll
     for (int i = 0; i < ATTN_MAX_D / 32; ++i) acc[i] = 0.f;

@@ -34,6 +34,11 @@ __device__ __forceinline__ AttnRequest attn_request(const kda_attention_params& 
   return q;
 }
 
+// The first key a row at position pos sees (window 0: all before it).
+__device__ __forceinline__ int first_key(int pos, int window) {
+  return window > 0 && pos >= window ? pos - window + 1 : 0;
+}
+
 // Launches a kernel that begins with earlier_work(), allowing it to be brought in early.
 template <typename... Params, typename... Args>
 inline cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t s, Args&&... args) {

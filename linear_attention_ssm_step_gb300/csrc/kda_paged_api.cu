@@ -83,8 +83,8 @@ kda_status check_cache(const kda_paged_cache& c) {
 
 kda_status check_table(const int32_t* table, int64_t stride, int32_t width, int32_t page_size, int32_t requests) {
   if (width < 1) return fail(KDA_EINVAL, "table_width = %d is below 1", width);
-  if ((long long)width * page_size > 0x7fffffffLL)
-    return fail(KDA_EUNSUPPORTED, "table_width * page_size = %lld tokens, 2^31 or more", (long long)width * page_size);
+  if ((long long)width * page_size > 0x7fffff00LL)  // positions rounded up to whole units of keys stay in 32 bits
+    return fail(KDA_EUNSUPPORTED, "table_width * page_size = %lld tokens, above 2^31 - 256", (long long)width * page_size);
   if (requests > 1 && stride < width)
     return fail(KDA_EINVAL, "table_stride = %lld is below table_width = %d", (long long)stride, width);
   return check_words("table", table, true);

@@ -97,7 +97,7 @@ struct Span {
 __device__ __forceinline__ Span item_span(int pos, int n, int i, int w, int window) {
   Span s;
   s.hi = max(0, pos + min(n, (i + 1) * w));
-  s.lo = window > 0 ? max(0, pos + i * w - window + 1) : 0;
+  s.lo = first_key(pos + i * w, window);
   if (s.hi == 0) s.lo = 0;
   s.u0 = s.lo / UNIT;
   s.u1 = max(s.u0 + 1, (s.hi + UNIT - 1) / UNIT);  // rows that see no key still need their zeros
@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int x = __shfl_up_sync(0xffffffffu, scan, o);
       if (lane >= o) scan += x;
     }
-    __syncthreads();
+    if (base > 0) __syncthreads();  // the sums of the block before are read
     if (lane == 31) sh.warp_sum[warp] = scan;
     __syncthreads();
     before = scan - mine;
@@ -531,11 +531,17 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int pos = q.kv - q.n, items = (q.n + w - 1) / w;
         if (fresh) {
           // whole heads first, then 32 items at a time
-          const int uh = __shfl_sync(0xffffffffu, head_units(pos, lane == 0 ? q.n : 0, w, window), 0);
+          int uh;
+          if (items == 1) {
+            const Span s = item_span(pos, q.n, 0, w, window);
+            uh = LEAD + s.u1 - s.u0;
+          } else {
+            uh = __shfl_sync(0xffffffffu, head_units(pos, lane == 0 ? q.n : 0, w, window), 0);
+          }
           head = (at - prefix) / uh;
           prefix += uh * head;
           item = 0;
-          for (int base = 0; base < items; base += 32) {
+          for (int base = 0; items > 1 && base < items; base += 32) {
             const int i = base + lane;
             int u = 0;
             if (i < items) {
@@ -868,7 +874,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         r.tok = (sg.dual ? t * tpt : 0) + tk;
         r.valid = tk < tpt && r.tok < sg.ntok;
         r.hi = r.valid ? sg.pos0 + r.tok + 1 : 0x7fffffff;
-        r.lo = r.valid && window > 0 ? max(0, r.hi - window) : 0;
+        r.lo = r.valid ? first_key(r.hi - 1, window) : 0;
         return r;
       };
       bool valid;

@@ -302,6 +302,54 @@ def test_attention_many_requests(dev):
     run_and_check(dev, Attention(new.tolist(), kv.tolist(), 4, 2, 64, 16, seed=12).poison())
 
 
+@pytest.mark.parametrize("Hq,Hkv,D", [(128, 1, 128), (100, 1, 64), (65, 1, 128), (43, 1, 64)])
+def test_attention_many_heads_share(dev, Hq, Hkv, D):
+    """Groups that fill a tile of rows, or leave much of it empty."""
+    run_and_check(dev, Attention([1, 3, 20], [200, 131, 20], Hq, Hkv, D, 16, seed=Hq).poison())
+
+
+@pytest.mark.parametrize("D", [128, 64])
+def test_attention_rows_off_16_bytes(dev, D):
+    """q and out rows that single accesses alone can reach, on the cache of the tensor-core kernel."""
+    a = Attention([3, 150, 1], [77, 350, 600], 6, 2, D, 16, seed=15)
+    a.q = torch.cat([a.q, a.q[:, :1]], dim=1).reshape(-1)[1:1 + a.q.numel()].view(a.q.shape)
+    wide = torch.full((154, 6, D + 3), 7.0, dtype=torch.bfloat16, device=dev)
+    run_and_check(dev, a, out=wide[..., 1:D + 1])
+    assert (wide[..., 0] == 7).all() and (wide[..., D + 1:] == 7).all()
+
+
+@pytest.mark.parametrize("D,Hq,Hkv", [(128, 4, 1), (64, 2, 2)])
+def test_attention_long_chunk(dev, D, Hq, Hkv):
+    """Many items of many units: whole ones, ones cut in two, and their order on the line."""
+    run_and_check(dev, Attention([600, 1, 257], [1700, 3000, 257], Hq, Hkv, D, 64, seed=16).poison())
+
+
+def test_attention_without_lse_and_largest_window(dev):
+    a = Attention([5, 2], [3, 90], 4, 2, 128, 16, seed=17, window=2 ** 31 - 1)
+    out, _ = a.run(dev, kda)
+    args = (to_device(a.q, dev), to_device(a.k, dev), to_device(a.v, dev), ints(a.table, dev), ints(a.cu, dev),
+            ints(a.kv, dev))
+    only = kda.kda_paged_attention(*args, scale=a.scale, window=a.window)
+    assert torch.equal(out, only)
+    a.check(*a.run(dev, kda))
+
+
+@pytest.mark.parametrize("D", [128, 64])
+def test_attention_wait_that_runs_out(dev, D):
+    """Failure detection without a fault: in the build that issues no copy (tests/test_timeout_gpu.py) the bounded waits
+    run out, the call reports KDA_ERR_TIMEOUT and returns, and the context stays usable."""
+    from linear_attention_ssm_step_gb300 import _build
+    wlib = kda.bind_library(_build.build(variant="waittest"))
+    a = Attention([1, 40], [300, 90], 4, 2, D, 16, seed=18)
+    err = err_word(dev)
+    call = kda.prepare_paged_attention(to_device(a.q, dev), to_device(a.k, dev), to_device(a.v, dev), ints(a.table, dev),
+                                       ints(a.cu, dev), ints(a.kv, dev), error_word=err)
+    assert wlib.kda_paged_attention(*call._args) == kda.KDA_OK
+    torch.cuda.synchronize()
+    assert int(err.item()) == kda.KDA_ERR_TIMEOUT
+    run_and_check(dev, a)
+
+
 def test_attention_without_work(dev):
     q = torch.zeros((0, 4, 64), dtype=torch.bfloat16, device=dev)
     c = torch.zeros((2, 16, 2, 64), dtype=torch.bfloat16, device=dev)
@@ -382,3 +430,28 @@ def test_the_three_together(dev):
         # q and k may round to the other bf16 neighbour: one ulp, 2^-7 of a value in [1, 2) mantissa terms at most,
         # of all of the score's terms: 2^-6 S in the scores, twice that in the weights
         assert (np.abs(g - o) <= (2.0 ** -8 + 2.0 ** -5 * S[:, :, None]) * A + 2.0 ** -8 * np.abs(o)).all()
+
+
+def test_hybrid_layers_in_chunks_equal_one_pass(dev):
+    """KDA and attention layers together (hybrid.py): prompts in two chunks and a token each, against all at once.
+    The two differ by roundings to bf16: the KDA state between calls, and what follows from it; every layer adds to a
+    residual of its own size, so half a percent of the largest output per layer is allowed."""
+    from linear_attention_ssm_step_gb300 import hybrid
+    lens, steps = [75, 20, 133], [[50, 20, 100], [24, 0, 32], [1, 0, 1]]
+    gen = torch.Generator(device=dev).manual_seed(3)
+    x = [torch.randn((n, 512), generator=gen, device=dev).to(torch.bfloat16) for n in lens]
+    outs = []
+    for plan in ([lens], steps):
+        model = hybrid.HybridLayers(hidden=512, layers="kka", heads=4, kv_heads=2, requests=3, pages=64, page_size=16,
+                                    max_tokens=200, device=dev, seed=5)
+        done, got = [0, 0, 0], [[], [], []]
+        for new in plan:
+            rows = torch.cat([x[r][done[r]:done[r] + n] for r, n in enumerate(new)])
+            y = model.step(rows, new)
+            at = 0
+            for r, n in enumerate(new):
+                got[r].append(y[at:at + n])
+                at, done[r] = at + n, done[r] + n
+        assert int(model.error_word.item()) == 0
+        outs.append(torch.cat([torch.cat(g) for g in got]).float())
+    assert (outs[0] - outs[1]).abs().max() <= 3 * 0.005 * outs[0].abs().max()

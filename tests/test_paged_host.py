@@ -126,7 +126,7 @@ INVALID, UNSUPPORTED = kda.KDA_EINVAL, kda.KDA_EUNSUPPORTED
     ("num_pages", 1 << 28, UNSUPPORTED, "2^31"),
     ("free_capacity", -1, INVALID, "free_capacity"),
     ("table_width", 0, INVALID, "table_width"),
-    ("table_width", 1 << 28, UNSUPPORTED, "2^31"),
+    ("table_width", 1 << 28, UNSUPPORTED, "2^31 - 256"),
     ("table_stride", 7, INVALID, "table_stride"),
     ("table", None, INVALID, "table is NULL"),
     ("cached", None, INVALID, "cached is NULL"),
