@@ -63,7 +63,6 @@ __global__ void __launch_bounds__(PLAN_THREADS) kda_paged_plan_kernel(kda_plan_p
   __shared__ long long warp_rows[PLAN_THREADS / 32], warp_need[PLAN_THREADS / 32];
   __shared__ int taken_all, bad_all;
   if (tid == 0) taken_all = bad_all = 0;
-  next_may_start();
   earlier_work();
   const int free_now = min(max(*p.free_count, 0), p.free_capacity);
   __syncthreads();
@@ -192,9 +191,9 @@ cudaError_t launch_paged_plan(const kda_plan_params& p, cudaStream_t s) {
 // halves are paired, 2 VEC consecutive values else; VEC = 8 (16-byte accesses)
 // when every row allows it, 1 otherwise. What a row waits for (its position,
 // its values) is covered by the other rows of the SM: with one task a thread in
-// flight and 16 CTAs an SM, 8192 rows of 32 + 8 + 8 heads of 128 take 34.9 us
-// (5.8 TB/s of reads and writes, 85 % of a plain copy); three tasks in flight
-// need 56 registers, 9 CTAs an SM and 42.6 us; 256 threads a row 39 us.
+// flight and 16 CTAs an SM, 8192 rows of 32 + 8 + 8 heads of 128 take 32.3 us
+// (6.2 TB/s of reads and writes, 92 % of a plain copy); three tasks in flight
+// need 56 registers, 9 CTAs an SM and 8 us more; 256 threads a row 4 us more.
 
 constexpr int ROPE_THREADS = 128, ROPE_CTAS = 16;  // a full SM: 32 registers a thread
 
@@ -238,7 +237,6 @@ __global__ void __launch_bounds__(ROPE_THREADS, ROPE_CTAS) kda_rope_append_kerne
   const int half = p.rotary_dim >> 1, D = p.cache.head_dim;
   const int Hq = p.num_q_heads, Hkv = p.cache.num_heads;
   const int per_head = (D + 2 * VEC - 1) / (2 * VEC), tasks = (Hq + 2 * Hkv) * per_head;
-  next_may_start();
   earlier_work();
   const int pos = p.positions[t], slot = p.slots[t];
   const uint64_t freq = tid < half ? p.freqs[tid] : 0u;
@@ -346,7 +344,6 @@ __global__ void __launch_bounds__(ATTN_WARPS * 32) kda_paged_attention_simt_kern
   const uint16_t* const kc = static_cast<const uint16_t*>(p.cache.k.ptr);
   const uint16_t* const vc = static_cast<const uint16_t*>(p.cache.v.ptr);
   const int r = blockIdx.y;
-  next_may_start();
   earlier_work();
   const AttnRequest q = attn_request(p, r);
   if (blockIdx.x == 0 && threadIdx.x == 0 && q.bad && p.error_word) atomicOr(p.error_word, q.bad);

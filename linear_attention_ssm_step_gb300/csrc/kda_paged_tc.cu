@@ -444,7 +444,6 @@ __global__ void __launch_bounds__(THREADS, 1)
     asm volatile("prefetch.tensormap [%0];" ::"l"(&vmap) : "memory");
   }
 
-  next_may_start();
   earlier_work();
 
   // ---- this CTA's share of the line of units
