@@ -22,14 +22,25 @@
 // finishes last joins them in the order of the parts: the same bits whichever
 // comes last.
 //
-// A CTA is twelve warps: two softmax groups of four (a thread per row), a warp
-// each that loads keys and values (one tensor-map copy per page and 64
-// columns), that issues either product, and that walks the line. With two row
-// tiles, group t owns tile t; a single tile (decode, verify) takes the units in
-// turn with the groups, each with its own O, joined at the end, so that in
-// either case one group's exponentials run while the other's products do.
-// S and P share tensor-memory columns: P (bf16) overwrites the S it came from
-// and enters the second product from there.
+// A CTA is twelve warps: two softmax groups of four (a thread per row), and one
+// warp each that loads keys and values (one tensor-map copy per page and 64
+// columns), that issues the products, that walks the line, and that asks the
+// next runs' queries into L2. With two row tiles, group t owns tile t; a single
+// tile (decode, verify) takes the units in turn with the groups, each with its
+// own O, joined at the end, so that in either case one group's exponentials run
+// while the other's products do. S and P share tensor-memory columns: P (bf16)
+// overwrites the S it came from and enters the second product from there. The
+// next S into the same columns is issued right behind that product: the products
+// of a CTA are issued by one warp and executed in the order of their issue.
+//
+// What bounds it. Few rows: memory (64 decode requests of 2048..8192 cached
+// tokens, 8 key-value heads of 128: 200 us, 6.2 TB/s, 92 % of a plain copy).
+// Chunks: the chain score product - registers - maximum - exponentials - weights
+// - value product of a tile, 2800 cycles a pair of units where the tensor core
+// needs 2048 (two chunks of 2048 tokens over 4096..16384 cached, 32 query heads:
+// 565..605 us, 1.46..1.56 PFLOP/s). Small calls: latency (one decode request of
+// 1000 tokens 11.7 us). Once-a-run code is kept short and in loops that are not
+// unrolled: it is fetched anew each run.
 #include <math.h>
 
 #include "kda_paged.cuh"
@@ -720,6 +731,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
     } else if (warp == PRODUCT_WARP) {
+      // ---- the products: the values of a tile, then its next scores, tile after tile. A product takes 64 cycles of the
+      // tensor core (head_dim 128) and its issue waits for room in a short queue, so little may stand between two of them:
+      // the warp stays together and its operands in uniform registers, and a run of products is one statement (formed one by
+      // one, with an election each, they took 85 cycles).
       const uint32_t base = smem_addr(smem), tm = uniform(tmem);
       constexpr uint32_t IDESC_S = idesc_bf16_f32(TILE, UNIT);
       constexpr uint32_t IDESC_O = idesc_bf16_f32(TILE, D) | B_MN_MAJOR;
