@@ -66,16 +66,19 @@ class HybridLayers:
 
     def step(self, x, new_len):
         """x: bf16 [sum(new_len), hidden], the packed rows of all requests (request r's new_len[r] rows after those of
-        the requests before it). Returns the layers' output rows; every request's state and cache move on."""
+        the requests before it). Returns the layers' output rows; every request's state and cache move on, but for
+        requests that the plan turns down (error_word says why): they stay as they were, and their rows mean nothing."""
         T, H, D = x.shape[0], self.heads, HEAD_DIM
-        plan = kda.kda_paged_plan(self.cached, torch.tensor(new_len, dtype=torch.int32, device=self.device),
-                                  self.block_table, self.free_pages, self.free_count, self.page_size, self.pages, T,
-                                  error_word=self.error_word)
+        new_len = torch.tensor(new_len, dtype=torch.int32, device=self.device)
+        plan = kda.kda_paged_plan(self.cached, new_len, self.block_table, self.free_pages, self.free_count,
+                                  self.page_size, self.pages, T, error_word=self.error_word)
+        admitted = plan.kv_len == self.cached + new_len  # the kv_len of a request turned down is 0
+        slots = torch.where(admitted, self.slots, -1)
         for kind, w, memory in zip(self.layers, self.weights, self.memory):
             y = self._norm(x) @ w["in"]
             if kind == "k":
                 q, k, v, g = (y[:, i * H * D:(i + 1) * H * D].view(T, H, D) for i in range(4))
-                out = kda.kda_prefill(memory, self.slots, plan.cu_new, q, k, v, g, y[:, 4 * H * D:], w["A_log"],
+                out = kda.kda_prefill(memory, slots, plan.cu_new, q, k, v, g, y[:, 4 * H * D:], w["A_log"],
                                       w["dt_bias"], error_word=self.error_word)
             else:
                 q, k, v = y.view(T, -1, D).split((H, self.kv_heads, self.kv_heads), dim=1)
@@ -85,7 +88,7 @@ class HybridLayers:
                 out = kda.kda_paged_attention(q, k_cache, v_cache, self.block_table, plan.cu_new, plan.kv_len,
                                               workspace=self.workspace, error_word=self.error_word)
             x = x + out.reshape(T, H * D) @ w["out"]
-        self.cached, self.free_count = plan.kv_len, plan.free_count
+        self.cached, self.free_count = torch.where(admitted, plan.kv_len, self.cached), plan.free_count
         return x
 
 

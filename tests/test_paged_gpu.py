@@ -455,3 +455,27 @@ def test_hybrid_layers_in_chunks_equal_one_pass(dev):
         assert int(model.error_word.item()) == 0
         outs.append(torch.cat([torch.cat(g) for g in got]).float())
     assert (outs[0] - outs[1]).abs().max() <= 3 * 0.005 * outs[0].abs().max()
+
+
+def test_hybrid_layers_leave_a_request_turned_down_as_it_was(dev):
+    """A step whose pages run out for one request: its state, cache and length stay, and it goes on later as if that
+    step had not been asked of it (the same bits: the later step has the same shapes)."""
+    from linear_attention_ssm_step_gb300 import hybrid
+    gen = torch.Generator(device=dev).manual_seed(4)
+    x = [torch.randn((n, 256), generator=gen, device=dev).to(torch.bfloat16) for n in (31, 34)]
+    outs = []
+    for asked in (14, 0):
+        model = hybrid.HybridLayers(hidden=256, layers="ka", heads=2, kv_heads=1, requests=2, pages=4, page_size=16,
+                                    max_tokens=64, device=dev, seed=6)
+        model.step(torch.cat([x[0][:30], x[1][:20]]), [30, 20])
+        assert int(model.error_word.item()) == 0
+        own = model.block_table[1, :2].long()
+        state, cache, table = model.memory[0][1].clone(), model.memory[1][own].clone(), model.block_table.clone()
+        model.step(torch.cat([x[0][30:], x[1][20:20 + asked]]), [1, asked])  # 34 tokens would take a fifth page
+        assert int(model.error_word.item()) == (kda.KDA_ERR_PAGES if asked else 0)
+        assert model.cached.tolist() == [31, 20] and int(model.free_count.item()) == 0
+        assert torch.equal(model.memory[0][1], state) and torch.equal(model.memory[1][own], cache)
+        assert torch.equal(model.block_table, table)
+        outs.append(model.step(x[1][20:32], [0, 12]))
+        assert model.cached.tolist() == [31, 32]
+    assert torch.equal(outs[0], outs[1])
