@@ -171,8 +171,8 @@ kda_status kda_rope_freqs(uint64_t* freqs, int32_t rotary_dim, double base, int3
  * Scores, maxima, sums and outputs are kept in fp32; the weights enter the
  * product with v as bf16 (their sum does not); out is rounded to bf16 once.
  *
- * Values of tokens at or past kv_len, and keys, are never multiplied into a
- * result, whatever they hold. A cached value below kv_len that is infinite or
+ * Keys and values of tokens at or past kv_len do not enter any result, whatever
+ * they hold, nor do keys a row does not see enter that row's. A cached value below kv_len that is infinite or
  * NaN makes NaN of the rows that see it, and may of other rows of its request.
  *
  * Pages are found through table[r][token / page_size]; entries of pages no row

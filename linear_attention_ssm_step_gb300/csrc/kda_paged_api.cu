@@ -251,7 +251,9 @@ size_t kda_paged_attention_workspace_bytes(int32_t head_dim) {
   if (head_dim < 1 || head_dim > 256) return 0;
   const int ctas = attention_ctas();
   if (ctas == 0) return 0;
-  return KDA_ATTENTION_WORKSPACE_ZEROED + kda::paged_attention_parts_bytes(head_dim, ctas);
+  // only the tensor-core kernel, which takes these head sizes, leaves parts
+  const size_t parts = head_dim == 64 || head_dim == 128 ? kda::paged_attention_parts_bytes(head_dim, ctas) : 0;
+  return KDA_ATTENTION_WORKSPACE_ZEROED + parts;
 }
 
 kda_status kda_paged_attention(const kda_attention_params* p, void* workspace, size_t workspace_bytes, void* stream) {
