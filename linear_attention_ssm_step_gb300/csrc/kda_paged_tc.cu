@@ -93,7 +93,7 @@ struct Shared {
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
   uint64_t v_tail, q_full[2], s_full[2], p_full[2][2], o_done[2], seg_full[RING], seg_empty[RING], drain;
   Segment seg[RING];
-  float m1[TILE], l1[TILE];  // the second group's m and l when both groups share a tile
+  float m1[2][TILE], l1[2][TILE];  // the groups' m and l when both share a tile
   int warp_sum[THREADS / 32];
   AttnRequest start;  // the request in which this CTA's share begins, and its first unit
   int start_prefix;
@@ -994,21 +994,20 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int x = me.x;
       if (alive && units > 0) alive = warp_wait(&sh.o_done[t], runs++ & 1);
       if (units > 0) tc_fence_after();
-      float fade0 = 1.f;  // what the O of this thread's tensor memory is scaled by
-      float fade1 = 0.f;
-      if (!dual && t == 1) {
-        sh.m1[x] = m;
-        sh.l1[x] = l;
+      float fade = 1.f, fade_other = 0.f;  // what this thread's O is scaled by where the groups share a tile, and the other's
+      if (!dual) {
+        sh.m1[t][x] = m;
+        sh.l1[t][x] = l;
       }
       if (bar_any(1, SOFTMAX_THREADS, !alive)) {
         alive = false;
         break;
       }
-      if (!dual && t == 0) {
-        const float mo = sh.m1[x], mm = fmaxf(m, mo), mb = mm == -INFINITY ? 0.f : mm;
-        fade0 = ex2((m - mb) * c);
-        fade1 = ex2((mo - mb) * c);
-        l = l * fade0 + sh.l1[x] * fade1;
+      if (!dual) {
+        const float mo = sh.m1[1 - t][x], mm = fmaxf(m, mo), mb = mm == -INFINITY ? 0.f : mm;
+        fade = ex2((m - mb) * c);
+        fade_other = ex2((mo - mb) * c);
+        l = l * fade + sh.l1[1 - t][x] * fade_other;
         m = mm;
       }
       const bool direct = sg.parts == 1;
@@ -1018,8 +1017,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       uint8_t* const tile = smem + (dual && t ? S::Q1 : S::Q0);
       const bool none = l == 0.f;  // no key: zeros
       const float inv = rcp(l);
-      float* const other = reinterpret_cast<float*>(smem + S::Q1);  // the second group's O, half the columns at a time
-      const bool two = !dual && sg.u1 - sg.u0 > 1;  // the second group has one
+      // Where both groups have an O of one tile, each hands the other half of its columns (in the queries' place, which the
+      // products are done with) and adds up the other half: columns [from, to) are this thread's.
+      const bool two = !dual && sg.u1 - sg.u0 > 1;
+      const int from = two ? t * (D / 2) : 0, to = two ? from + D / 2 : dual || t == 0 ? D : 0;
       // 32 columns of this thread's row, scaled, into the tile's own queries' place, which the products are done with.
       auto stage = [&](const float (&f)[32], int col, float scale, bool zero) {
 #pragma unroll
@@ -1033,32 +1034,42 @@ __global__ void __launch_bounds__(THREADS, 1)
               make_uint4(b[0], b[1], b[2], b[3]);
         }
       };
-      // 32 columns at a time, in a loop that is not unrolled: this runs once a run, and its instructions come from afar
+      // 32 columns at a time, in loops that are not unrolled: this runs once a run, and its instructions come from afar
+      if (two) {
+        float* const give = reinterpret_cast<float*>(smem + (t ? S::Q1 : S::Q0)) + x;
+        const float* const taken = reinterpret_cast<const float*>(smem + (t ? S::Q0 : S::Q1)) + x;
 #pragma unroll 1
-      for (int col = 0; col < D; col += 32) {
-        float* const o1 = other + (col & (D / 2 - 1)) * TILE + x;
-        float f[32];
-        if (warp_valid && (dual || t == 0 || two)) tmem_ld32(o_addr + col, f);
-        if (two) {
-          if (t == 1 && warp_valid) {
+        for (int col = 0; warp_valid && col < D / 2; col += 32) {
+          float f[32];
+          tmem_ld32(o_addr + (D / 2 - from) + col, f);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) o1[j * TILE] = f[j];
-          }
-          bar_sync(2, SOFTMAX_THREADS);
-          if (t == 0 && warp_valid) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) f[j] = f[j] * fade0 + o1[j * TILE] * fade1;
-          }
-          if (D == 64 || col == 32) bar_sync(2, SOFTMAX_THREADS);  // half the columns fill the buffer
+          for (int j = 0; j < 32; ++j) give[(col + j) * TILE] = f[j];
         }
-        if (writes) {
-          if (direct) {
-            stage(f, col, inv, none);
-          } else {
-            float4* const o = part_o<D>(a, slot_id) + (col / 4) * (2 * TILE) + part_row;
+        bar_sync(2, SOFTMAX_THREADS);
+#pragma unroll 1
+        for (int col = 0; warp_valid && col < D / 2; col += 32) {
+          float f[32];
+          uint32_t b[32];
+          tmem_ld32(o_addr + from + col, f);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) o[j * (2 * TILE)] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
-          }
+          for (int j = 0; j < 32; ++j) b[j] = __float_as_uint(f[j] * fade + taken[(col + j) * TILE] * fade_other);
+          st16(o_addr + from + col, b);
+          st16(o_addr + from + col + 16, b + 16);
+          tmem_st_wait();
+        }
+        if (direct) bar_sync(2, SOFTMAX_THREADS);  // the outputs go where the other group read
+      }
+#pragma unroll 1
+      for (int col = from; col < to; col += 32) {
+        float f[32];
+        if (warp_valid) tmem_ld32(o_addr + col, f);
+        if (!valid) continue;
+        if (direct) {
+          stage(f, col, inv, none);
+        } else {
+          float4* const o = part_o<D>(a, slot_id) + (col / 4) * (2 * TILE) + part_row;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) o[j * (2 * TILE)] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
         }
       }
       tc_fence_before();
@@ -1096,104 +1107,103 @@ __global__ void __launch_bounds__(THREADS, 1)
           return make_float2(mm, ll);
         };
         if (sh.last_part) __threadfence();
-        if (sh.last_part && (dual || sg.ntok * g > TILE / 2)) {
+        if (sh.last_part && (dual || sg.ntok * g > TILE / 2)) {  // half the columns a group where they share a tile
           whole = true;
-          if (writes) {
+          if (valid) {
             const float2 z = joined_ml(part_row);
             m = z.x;
             l = z.y;
             const float mb = m == -INFINITY ? 0.f : m, scale = rcp(l);
+            const int join_to = dual ? D : (t + 1) * (D / 2);
 #pragma unroll 1
-            for (int col = 0; col < D; col += 32) {
+            for (int col = dual ? 0 : t * (D / 2); col < join_to; col += 32) {
               float f[32];
 #pragma unroll
               for (int j = 0; j < 32; ++j) f[j] = 0.f;
 #pragma unroll 1
-              for (int q = 0; q < sg.parts; ++q) {
-                const int sid = slot_of(q);
-                const float4* const o = part_o<D>(a, sid) + (col / 4) * (2 * TILE) + part_row;
-                float4 v[8];
+              for (int q = 0; q < sg.parts; q += 2) {  // two parts at a time: mostly there are no more
+                float4 v[2][8];
+                float w[2];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = __ldcg(o + j * (2 * TILE));
-                const float w = ex2((__ldcg(&part_ml<D>(a, sid)[part_row].x) - mb) * c);
+                for (int i = 0; i < 2; ++i) {
+                  const bool on = q + i < sg.parts;
+                  const int sid = slot_of(on ? q + i : q);
+                  const float4* const o = part_o<D>(a, sid) + (col / 4) * (2 * TILE) + part_row;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                  f[4 * j] = fmaf(v[j].x, w, f[4 * j]);
-                  f[4 * j + 1] = fmaf(v[j].y, w, f[4 * j + 1]);
-                  f[4 * j + 2] = fmaf(v[j].z, w, f[4 * j + 2]);
-                  f[4 * j + 3] = fmaf(v[j].w, w, f[4 * j + 3]);
+                  for (int j = 0; j < 8; ++j) v[i][j] = on ? __ldcg(o + j * (2 * TILE)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                  w[i] = ex2((__ldcg(&part_ml<D>(a, sid)[part_row].x) - mb) * c);
                 }
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                  for (int j = 0; j < 8; ++j) {
+                    f[4 * j] = fmaf(v[i][j].x, w[i], f[4 * j]);
+                    f[4 * j + 1] = fmaf(v[i][j].y, w[i], f[4 * j + 1]);
+                    f[4 * j + 2] = fmaf(v[i][j].z, w[i], f[4 * j + 2]);
+                    f[4 * j + 3] = fmaf(v[i][j].w, w[i], f[4 * j + 3]);
+                  }
               }
               stage(f, col, scale, l == 0.f);
             }
           }
         } else if (sh.last_part) {
-          const int rows = sg.ntok * g;  // of one tile
-          float* const jm = reinterpret_cast<float*>(smem + S::Q0);  // the queries are done with
-          float* const jl = jm + TILE;
-          if (tid < rows) {
-            const float2 z = joined_ml(tid);
-            jm[tid] = z.x == -INFINITY ? 0.f : z.x;
-            jl[tid] = z.y;
-            if (p.lse != nullptr)
-              p.lse[((int64_t)sg.row0 + div_g(tid)) * p.num_q_heads + sg.head * g + (tid - div_g(tid) * g)] =
-                  z.x == -INFINITY ? -INFINITY : z.x * p.scale + ln(z.y);
-          }
-          bar_sync(1, SOFTMAX_THREADS);
-          // then four columns of a row at a time; `pad` rows a group of columns, so that neighbours read neighbours
-          const int pad = (rows + 7) & ~7;
-          constexpr int U = 2;
+          // Four columns of a row a thread, `pad` rows a group of columns, so that neighbours read neighbours; a thread finds
+          // its row's maximum and sum itself, from the same trip to memory as the columns.
+          const int rows = sg.ntok * g, pad = (rows + 7) & ~7;  // of one tile
 #pragma unroll 1
-          for (int i0 = tid; i0 < pad * (D / 4); i0 += U * SOFTMAX_THREADS) {
-            float acc[U][4];
-            int at[U];
-            float mb[U];
-            bool on[U];
+          for (int i0 = tid; i0 < pad * (D / 4); i0 += SOFTMAX_THREADS) {
+            const int group = i0 / pad, row2 = i0 - group * pad;
+            if (row2 >= rows) continue;
+            const int at = group * (2 * TILE) + row2;
+            float mm = -INFINITY, ll = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+            for (int q = 0; q < sg.parts; q += 8) {
+              float2 z[8];
+              float4 v[8];
 #pragma unroll
-            for (int k = 0; k < U; ++k) {
-              const int i = i0 + k * SOFTMAX_THREADS;
-              const int col = i / pad, row2 = i - col * pad;
-              on[k] = col < D / 4 && row2 < rows;
-              at[k] = on[k] ? col * (2 * TILE) + row2 : 0;
-              mb[k] = on[k] ? jm[row2] : 0.f;
-              acc[k][0] = acc[k][1] = acc[k][2] = acc[k][3] = 0.f;
-            }
-#pragma unroll 4
-            for (int q = 0; q < sg.parts; ++q) {
-              const int sid = slot_of(q);
-#pragma unroll
-              for (int k = 0; k < U; ++k) {
-                if (!on[k]) continue;
-                const float4 v = __ldcg(part_o<D>(a, sid) + at[k]);
-                const float f = ex2((__ldcg(&part_ml<D>(a, sid)[at[k] % (2 * TILE)].x) - mb[k]) * c);
-                acc[k][0] = fmaf(v.x, f, acc[k][0]);
-                acc[k][1] = fmaf(v.y, f, acc[k][1]);
-                acc[k][2] = fmaf(v.z, f, acc[k][2]);
-                acc[k][3] = fmaf(v.w, f, acc[k][3]);
+              for (int i = 0; i < 8; ++i) {
+                const bool on = q + i < sg.parts;
+                const int sid = slot_of(on ? q + i : q);
+                z[i] = on ? __ldcg(part_ml<D>(a, sid) + row2) : make_float2(-INFINITY, 0.f);
+                v[i] = on ? __ldcg(part_o<D>(a, sid) + at) : make_float4(0.f, 0.f, 0.f, 0.f);
               }
-            }
+              float top = mm;
 #pragma unroll
-            for (int k = 0; k < U; ++k) {
-              if (!on[k]) continue;
-              const int row2 = at[k] % (2 * TILE), col = at[k] / (2 * TILE) * 4;
-              const float ll = jl[row2], iv = rcp(ll);
-              uint16_t* const dst = static_cast<uint16_t*>(p.out) + (int64_t)sg.row0 * p.out_b_stride +
-                                    (int64_t)(sg.head * g) * p.out_h_stride +
-                                    row_offset(row2, p.out_b_stride, p.out_h_stride) + col;
-              const uint32_t b0 = ll == 0.f ? 0u : pack_bf16x2(acc[k][0] * iv, acc[k][1] * iv);
-              const uint32_t b1 = ll == 0.f ? 0u : pack_bf16x2(acc[k][2] * iv, acc[k][3] * iv);
-              if (a.out_wide) {
-                *reinterpret_cast<uint2*>(dst) = make_uint2(b0, b1);
-              } else {
-                dst[0] = (uint16_t)b0;
-                dst[1] = (uint16_t)(b0 >> 16);
-                dst[2] = (uint16_t)b1;
-                dst[3] = (uint16_t)(b1 >> 16);
+              for (int i = 0; i < 8; ++i) top = fmaxf(top, z[i].x);
+              const float mb = top == -INFINITY ? 0.f : top, f = ex2((mm - mb) * c);
+              ll *= f;
+              acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float w = ex2((z[i].x - mb) * c);
+                ll = fmaf(z[i].y, w, ll);
+                acc.x = fmaf(v[i].x, w, acc.x);
+                acc.y = fmaf(v[i].y, w, acc.y);
+                acc.z = fmaf(v[i].z, w, acc.z);
+                acc.w = fmaf(v[i].w, w, acc.w);
               }
+              mm = top;
             }
+            const float iv = rcp(ll);
+            const int64_t row0 = (int64_t)sg.row0 + div_g(row2);
+            const int h = sg.head * g + (row2 - div_g(row2) * g);
+            uint16_t* const dst = static_cast<uint16_t*>(p.out) + row0 * p.out_b_stride + (int64_t)h * p.out_h_stride + group * 4;
+            const uint32_t b0 = ll == 0.f ? 0u : pack_bf16x2(acc.x * iv, acc.y * iv);
+            const uint32_t b1 = ll == 0.f ? 0u : pack_bf16x2(acc.z * iv, acc.w * iv);
+            if (a.out_wide) {
+              *reinterpret_cast<uint2*>(dst) = make_uint2(b0, b1);
+            } else {
+              dst[0] = (uint16_t)b0;
+              dst[1] = (uint16_t)(b0 >> 16);
+              dst[2] = (uint16_t)b1;
+              dst[3] = (uint16_t)(b1 >> 16);
+            }
+            if (group == 0 && p.lse != nullptr) p.lse[row0 * p.num_q_heads + h] = mm * p.scale + ln(ll);
           }
         }
       }
+      if (whole && !dual) bar_sync(1, SOFTMAX_THREADS);
       if (whole && (dual || t == 0)) {
         if (t == 0)
           bar_sync(3, TILE);
@@ -1228,7 +1238,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       if (whole && writes && p.lse != nullptr)
         p.lse[((int64_t)sg.row0 + (dual ? t * tpt : 0) + div_g(x)) * p.num_q_heads + sg.head * g + (x - div_g(x) * g)] =
-            m == -INFINITY ? -INFINITY : m * p.scale + ln(l);
+            m * p.scale + ln(l);  // no key: -inf; only NaN scores: NaN
       if (t == 0)
         bar_sync(3, TILE);
       else

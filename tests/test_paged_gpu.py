@@ -294,6 +294,33 @@ def test_attention_many_splits_and_repeats(dev, D):
         assert torch.equal(o2.view(torch.int16), out.view(torch.int16)) and torch.equal(l2, lse)
 
 
+@pytest.mark.parametrize("D", [128, 64, 48])
+def test_attention_nan_rows(dev, D):
+    """A query, and a key, of NaN: the rows that see one are NaN, value and log-sum; the others are as without it."""
+    a = Attention([1, 150, 3], [300, 400, 260], 8, 2, D, 16, seed=12)
+    b = Attention([1, 150, 3], [300, 400, 260], 8, 2, D, 16, seed=12)
+    b.q[0, 5], b.q[20] = float("nan"), float("nan")
+    key = 351  # of request 1: seen by its rows from 351 - 250 on
+    b.k[int(b.table[1, key // 16]), key % 16, 1] = float("nan")
+    (o, z), (on, zn) = run_and_check(dev, a), b.run(dev, kda)
+    bad = torch.zeros((154, 8), dtype=torch.bool, device=dev)
+    bad[0, 5], bad[20] = True, True
+    bad[1 + 101:151, 4:] = True
+    assert torch.isnan(on[bad]).all() and torch.isnan(zn[bad]).all()
+    assert torch.equal(on[~bad], o[~bad]) and torch.equal(zn[~bad], z[~bad])
+
+
+@pytest.mark.parametrize("D", [128, 64])
+@pytest.mark.parametrize("R,new,g,kv", [(160, 1, 4, 700), (120, 8, 16, 500), (3, 8, 16, 3000), (2, 3, 16, 5000),
+                                        (150, 2, 3, 140), (40, 5, 12, 1100)])
+def test_attention_tiles_of_one_request(dev, D, R, new, g, kv):
+    """Few and many rows in a tile, held whole by one block or cut between several."""
+    rng = np.random.default_rng(R + g)
+    lens = rng.integers(max(new, kv // 3), kv + 1, R)
+    a = Attention([new] * R, lens.tolist(), 2 * g, 2, D, 32, seed=R + g).poison()
+    run_and_check(dev, a)
+
+
 def test_attention_many_requests(dev):
     rng = np.random.default_rng(11)
     R = 900
