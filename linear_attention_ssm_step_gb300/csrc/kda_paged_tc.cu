@@ -34,13 +34,13 @@
 // of a CTA are issued by one warp and executed in the order of their issue.
 //
 // What bounds it. Few rows: memory (64 decode requests of 2048..8192 cached
-// tokens, 8 key-value heads of 128: 200 us, 6.2 TB/s, 92 % of a plain copy).
+// tokens, 8 key-value heads of 128: 192..197 us, 6.4 TB/s, 94 % of a plain copy).
 // Chunks: the chain score product - registers - maximum - exponentials - weights
-// - value product of a tile, 2800 cycles a pair of units where the tensor core
+// - value product of a tile, 2600 cycles a pair of units where the tensor core
 // needs 2048 (two chunks of 2048 tokens over 4096..16384 cached, 32 query heads:
-// 565..605 us, 1.46..1.56 PFLOP/s). Small calls: latency (one decode request of
-// 1000 tokens 11.7 us). Once-a-run code is kept short and in loops that are not
-// unrolled: it is fetched anew each run.
+// 530 us alone, 1.66 PFLOP/s, and 560..585 us in a loop, under the power cap).
+// Small calls: latency (one decode request of 1000 tokens 10 us). Once-a-run code
+// is kept short and in loops that are not unrolled: it is fetched anew each run.
 #include <math.h>
 
 #include "kda_paged.cuh"
@@ -61,7 +61,8 @@ constexpr int PRODUCT_WARP = 8, LOAD_WARP = 9, WALK_WARP = 10, AHEAD_WARP = 11;
 constexpr int FIRST = 96;   // keys of a unit whose weights are handed over first, while the others' are formed
 constexpr int RING = 4;  // segments the walking warp may be ahead
 // What an item costs beside its units (its queries, its end), in units: each item takes LEAD + its units of the line. A
-// first chunk of 4096 tokens, whose items have 1 to 32 units: 168 us at 2, 144 at 4, 148 at 7.
+// first chunk of 4096 tokens, whose items have 1 to 32 units: 122 us at 3, 118 at 4, 119.5 at 5 (two tiles); 32 verify
+// requests: 56.7 us at 1, 55.7 at 2, 54.6 at 4, 56.4 at 6 (one tile).
 constexpr int LEAD = 4;
 // Registers a thread after the split: 256 x 208 + 128 x 88 = 384 x 168, what the block launches with.
 constexpr int SOFTMAX_REGS = 208, OTHER_REGS = 88;
