@@ -411,6 +411,39 @@ def test_attention_graph_and_side_stream(dev):
         assert torch.equal(out, ref)
 
 
+@pytest.mark.parametrize("D", [128, 64, 96])
+def test_pages_past_2_to_the_31_elements(dev, D):
+    """Append and attention in the last pages of a cache of more than 2^31 elements: the same bits as in a small one."""
+    Hq, Hkv, page = 16, 8, 64
+    a = Attention([1, 140, 5], [600, 300, 64], Hq, Hkv, D, page, seed=15)
+    T, few = 146, a.k.shape[0]
+    many = 2 ** 31 // (page * Hkv * D) + few + 8
+    first = many - few  # the small cache's page 0 there
+    gen = torch.Generator().manual_seed(16)
+    q, k, v = (torch.randn((T, h, D), generator=gen).to(torch.bfloat16).to(dev) for h in (Hq, Hkv, Hkv))
+    pos = np.concatenate([np.arange(L - n, L) for n, L in zip(a.new, a.kv)])
+    owner = np.repeat(np.arange(3), a.new)
+    slots = a.table[owner, pos // page] * page + pos % page
+    freqs = kda.rope_freqs(D, device=dev)
+    got = []
+    for base, pages in ((0, few), (first, many)):
+        kc, vc = (torch.empty((pages, page, Hkv, D), dtype=torch.bfloat16, device=dev) for _ in range(2))
+        kc[base:].copy_(a.k)
+        vc[base:].copy_(a.v)
+        err = err_word(dev)
+        qr = kda.kda_rope_append(q, k, v, ints(pos, dev), ints(slots + base * page, dev), freqs, kc, vc, error_word=err)
+        table = np.where(a.table < 0, a.table, a.table + base)
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+        out = kda.kda_paged_attention(qr, kc, vc, ints(table, dev), ints(a.cu, dev), ints(a.kv, dev), lse=lse,
+                                      error_word=err)
+        assert int(err.item()) == 0
+        got.append([x.clone() for x in (qr, out, lse, kc[base:], vc[base:])])
+        del kc, vc
+    assert not torch.equal(got[0][3], a.k.to(dev)), "the rows were appended"
+    for x, y in zip(*got):
+        assert torch.equal(x, y) and torch.isfinite(x.float()).all()
+
+
 def test_the_three_together(dev):
     """A prompt in two chunks, then decode: each token's attention equals attention over the whole
     sequence, laid out plainly."""
