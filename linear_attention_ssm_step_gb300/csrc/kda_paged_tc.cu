@@ -1004,12 +1004,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         alive = false;
         break;
       }
-      if (!dual) {
-        const float mo = sh.m1[1 - t][x], mm = fmaxf(m, mo), mb = mm == -INFINITY ? 0.f : mm;
-        fade = ex2((m - mb) * c);
-        fade_other = ex2((mo - mb) * c);
-        l = l * fade + sh.l1[1 - t][x] * fade_other;
-        m = mm;
+      if (!dual) {  // the same bits of m and l in both groups
+        const float m0 = sh.m1[0][x], m1 = sh.m1[1][x];
+        m = fmaxf(m0, m1);
+        const float mb = m == -INFINITY ? 0.f : m, fade0 = ex2((m0 - mb) * c), fade1 = ex2((m1 - mb) * c);
+        l = sh.l1[0][x] * fade0 + sh.l1[1][x] * fade1;
+        fade = t ? fade1 : fade0;
+        fade_other = t ? fade0 : fade1;
       }
       const bool direct = sg.parts == 1;
       const bool writes = (dual || t == 0) && valid;

@@ -321,6 +321,36 @@ def test_attention_tiles_of_one_request(dev, D, R, new, g, kv):
     run_and_check(dev, a)
 
 
+@pytest.mark.parametrize("D,Hq,Hkv,new,kv", [
+    (128, 32, 8, [300, 1, 700], [300, 3000, 1900]),           # chunks: items of two tiles cut in two
+    (64, 16, 4, [100, 37, 1, 60] * 6, [1200, 900, 2500, 64] * 6),
+    (128, 12, 4, [8] * 32, list(range(1000, 5000, 125))),     # few rows
+    (128, 32, 2, [5] * 9, list(range(700, 3400, 300))),       # one tile, many rows
+    (64, 8, 1, [2], [30000]),                                 # more parts than a batch of the join
+])
+def test_attention_same_bits_whatever_the_order_of_arrival(dev, D, Hq, Hkv, new, kv):
+    """Parts of cut items are joined by whichever block ends last: with the GPU to itself, and with other work beside
+    that makes blocks end in other orders, the same bits."""
+    a = Attention(new, kv, Hq, Hkv, D, 16, seed=17)
+    ws = kda.paged_attention_workspace(D, dev)
+    out, lse = run_and_check(dev, a, workspace=ws)
+    args = (to_device(a.q, dev), to_device(a.k, dev), to_device(a.v, dev), ints(a.table, dev), ints(a.cu, dev),
+            ints(a.kv, dev))
+    outs = [(torch.empty_like(out), torch.empty_like(lse)) for _ in range(24)]
+    noise = torch.empty(1 << 26, device=dev)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for i, (o, z) in enumerate(outs):
+        if i % 3:
+            with torch.cuda.stream(side):
+                noise.add_(1.0)
+        kda.kda_paged_attention(*args, out=o, lse=z, scale=a.scale, workspace=ws)
+    torch.cuda.synchronize()
+    for o, z in outs:
+        assert torch.equal(o, out) and torch.equal(z, lse)
+    assert (ws[:kda.KDA_ATTENTION_WORKSPACE_ZEROED] == 0).all()
+
+
 def test_attention_many_requests(dev):
     rng = np.random.default_rng(11)
     R = 900
