@@ -470,6 +470,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   int mine = 0, before = 0;  // the units of this thread's request in the latest block, and those before it
   const int R = p.num_requests;
   const bool one_block = R <= THREADS;
+  bool summed = false;  // warp_sum holds an earlier block's sums (of this pass or of the one before)
   auto block_units = [&](int base) {
     const int r = base + tid;
     mine_r = AttnRequest{0, 0, 0, 0u};
@@ -482,7 +483,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int x = __shfl_up_sync(0xffffffffu, scan, o);
       if (lane >= o) scan += x;
     }
-    if (base > 0) __syncthreads();  // the sums of the block before are read
+    if (summed) __syncthreads();  // every warp has read the sums of the block before
+    summed = true;
     if (lane == 31) sh.warp_sum[warp] = scan;
     __syncthreads();
     before = scan - mine;

@@ -1,0 +1,66 @@
+"""The paged-attention calls on the GPU at their limits: many requests, rows and
+bounds that go wrong, values that are not finite, other streams. Bounds and
+their derivation: paged_cases.py."""
+
+import numpy as np
+import pytest
+import torch
+
+from linear_attention_ssm_step_gb300 import kda
+from paged_cases import Attention, ints, to_device
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    import __graft_entry__
+    __graft_entry__.build()
+    return torch.device("cuda:0")
+
+
+def err_word(dev):
+    return torch.zeros(1, dtype=torch.int32, device=dev)
+
+
+def on_device(a, dev):
+    """The tensors of an attention problem, in the order of the call's arguments."""
+    return (to_device(a.q, dev), to_device(a.k, dev), to_device(a.v, dev), ints(a.table, dev), ints(a.cu, dev),
+            ints(a.kv, dev))
+
+
+# ---------------------------------------------------------------- many requests
+
+@pytest.mark.parametrize("R", [383, 384, 385, 767, 768, 769, 1536, 4096])
+def test_attention_requests_in_blocks_of_the_sum(dev, R):
+    """Above 384 requests each CTA sums them in blocks, twice: once for the whole and once to find its share. Ragged
+    lengths, so that the warps of a CTA reach the second sum at different times, and many calls, with other work
+    beside them: every call's rows are right and the same bits."""
+    rng = np.random.default_rng(R)
+    new = rng.integers(0, 3, R)
+    kv = new + rng.integers(0, 30, R)
+    for r, extra in ((0, 900), (R // 2, 2500), (R - 1, 400)):
+        kv[r] += extra
+    new[R // 3] += 300
+    kv[R // 3] += 700
+    a = Attention(new.tolist(), kv.tolist(), 4, 2, 64, 16, seed=R).poison()
+    ws = kda.paged_attention_workspace(64, dev)
+    err = err_word(dev)
+    out, lse = a.run(dev, kda, workspace=ws, error_word=err)
+    a.check(out, lse)
+    args = on_device(a, dev)
+    outs = [(torch.empty_like(out), torch.empty_like(lse)) for _ in range(40)]
+    noise = torch.empty(1 << 25, device=dev)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for i, (o, z) in enumerate(outs):
+        if i % 3:
+            with torch.cuda.stream(side):
+                noise.add_(1.0)
+        kda.kda_paged_attention(*args, out=o, lse=z, scale=a.scale, workspace=ws, error_word=err)
+    torch.cuda.synchronize()
+    for o, z in outs:
+        assert torch.equal(o, out) and torch.equal(z, lse)
+    assert int(err.item()) == 0 and (ws[:kda.KDA_ATTENTION_WORKSPACE_ZEROED] == 0).all()
