@@ -180,7 +180,9 @@ kda_status kda_rope_freqs(uint64_t* freqs, int32_t rotary_dim, double base, int3
  * of zero, with KDA_ERR_PAGES. Bounds cu_new out of order or past num_tokens
  * skip the request (KDA_ERR_SEQLENS); a kv_len negative or over table_width *
  * page_size counts as 0 (KDA_ERR_LENGTHS). Rows no request covers are not
- * written; overlapping ranges are undefined.
+ * written; rows that several requests cover are undefined, and where the
+ * requests together hold more than num_tokens rows, every row is
+ * (KDA_ERR_SEQLENS).
  *
  * head_dim 64 or 128 with a page size that is a power of two from 16 on and
  * 16-byte aligned cache rows (pointers, and strides that are multiples of 8)

@@ -527,7 +527,15 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (cta >= ctas) return;  // the whole CTA: nothing allocated yet
   if (warp == PRODUCT_WARP) tmem_alloc(&sh.tmem, 512);
   tc_fence_before();
-  __syncthreads();
+  if (__syncthreads_or(bad & KDA_ERR_SEQLENS)) {
+    // Ranges can share rows only where some bounds are out of order. Together they may then hold more rows than there are,
+    // for which the sums above are not made (32 bits): nothing is done.
+    long long rows = 0;
+    for (int r = lane; r < R; r += 32) rows += attn_request(p, r).n;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) rows += __shfl_xor_sync(0xffffffffu, rows, o);
+    if (rows > p.num_tokens) end = begin;
+  }
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
   const uint32_t S_COL = tmem, O_COL = tmem + 2 * TILE;
@@ -1283,7 +1291,9 @@ static cudaError_t launch_tc(const CUtensorMap& km, const CUtensorMap& vm, const
 
 cudaError_t launch_paged_attention_tc(const kda_attention_params& p, void* workspace, int ctas, cudaStream_t s) {
   if ((p.q.b_stride | p.q.h_stride | p.out_b_stride | p.out_h_stride) >> 31) return cudaErrorNotSupported;
-  // the line of units is counted in 32 bits: at most so many items of so many units a key-value head
+  // the line of units is counted in 32 bits: at most so many items of so many units a key-value head (for ranges that
+  // share no rows; the kernel turns away others that hold more than num_tokens)
+  if (p.num_tokens > 0x7fffffff - 2 * TILE) return cudaErrorNotSupported;
   const long long tokens = 2 * (TILE / (p.num_q_heads / p.cache.num_heads));
   long long keys = (long long)p.table_width * p.cache.page_size;
   if (p.window > 0 && p.window + tokens < keys) keys = p.window + tokens;

@@ -64,3 +64,32 @@ def test_attention_requests_in_blocks_of_the_sum(dev, R):
     for o, z in outs:
         assert torch.equal(o, out) and torch.equal(z, lse)
     assert int(err.item()) == 0 and (ws[:kda.KDA_ATTENTION_WORKSPACE_ZEROED] == 0).all()
+
+
+# ---------------------------------------------------------------- bounds and rows
+
+@pytest.mark.parametrize("D", [128, 64])
+def test_attention_ranges_that_hold_too_many_rows(dev, D):
+    """cu_new that jumps back gives the same rows to many requests: 2048 requests of 65536 rows over 65536 keys have
+    more units than 32 bits count. The call ends, reports the bounds, and leaves its workspace ready."""
+    T, R, Hq, page, pages = 65536, 4096, 64 * 64 // D, 256, 300
+    heads = Hq  # 32 or 64 key-value heads
+    units = 0
+    for i in range(0, T, 256):  # the items of a request, 256 rows each: keys up to the last row's, four units of lead
+        units += 4 + (i + 256) // 128
+    assert R // 2 * units * heads > 2 ** 31
+    gen = torch.Generator(device=dev).manual_seed(1)
+    q = torch.randn((T, Hq, D), generator=gen, device=dev, dtype=torch.float32).to(torch.bfloat16)
+    k = torch.zeros((pages, page, heads, D), dtype=torch.bfloat16, device=dev)
+    table = torch.arange(T // page, dtype=torch.int32, device=dev).expand(R, -1).contiguous()
+    cu = torch.tensor([0, T] * (R // 2) + [0], dtype=torch.int32, device=dev)
+    kv = torch.full((R,), T, dtype=torch.int32, device=dev)
+    ws = kda.paged_attention_workspace(D, dev)
+    err = err_word(dev)
+    kda.kda_paged_attention(q, k, k.clone(), table, cu, kv, workspace=ws, error_word=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == kda.KDA_ERR_SEQLENS
+    a = Attention([3, 90], [40, 300], 4, 2, D, 16, seed=3)
+    err.zero_()
+    a.check(*a.run(dev, kda, workspace=ws, error_word=err))
+    assert int(err.item()) == 0
