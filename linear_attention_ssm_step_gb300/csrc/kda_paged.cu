@@ -132,21 +132,24 @@ __global__ void __launch_bounds__(PLAN_THREADS) kda_paged_plan_kernel(kda_plan_p
     *p.free_count_out = free_now - taken;
     if (bad_all && p.error_word) atomicOr(p.error_word, (unsigned)bad_all);
   }
+  // rows and pages are counted without a sign: below 2^31, and a step of the whole grid beyond that must not wrap
+  const unsigned first = blockIdx.x * PLAN_THREADS + tid, stride = gridDim.x * PLAN_THREADS;
+  const unsigned num_tokens = (unsigned)p.num_tokens;
   if (R == 0) {
-    for (int t = blockIdx.x * PLAN_THREADS + tid; t < p.num_tokens; t += gridDim.x * PLAN_THREADS)
-      p.positions[t] = p.slots[t] = -1;
+    for (unsigned t = first; t < num_tokens; t += stride) p.positions[t] = p.slots[t] = -1;
     return;
   }
 
   const int P = p.page_size;
   // new pages into the table: every page index below `taken` belongs to an admitted request
-  for (int i = blockIdx.x * PLAN_THREADS + tid; i < taken; i += gridDim.x * PLAN_THREADS) {
-    const int r = last_at_most(s.pages, R, i);
+  for (unsigned u = first; u < (unsigned)taken; u += stride) {
+    const int i = (int)u, r = last_at_most(s.pages, R, i);
     const int have = (int)(((long long)s.kept[r] + P - 1) / P);
     p.table[(int64_t)r * p.table_stride + have + (i - s.pages[r])] = p.free_pages[free_now - 1 - i];
   }
   bool bad_page = false;
-  for (int t = blockIdx.x * PLAN_THREADS + tid; t < p.num_tokens; t += gridDim.x * PLAN_THREADS) {
+  for (unsigned u = first; u < num_tokens; u += stride) {
+    const int t = (int)u;
     int pos = -1, slot = -1;
     if (t < s.cu[R]) {
       const int r = last_at_most(s.cu, R, t);
@@ -172,7 +175,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) kda_paged_plan_kernel(kda_plan_p
 
 cudaError_t launch_paged_plan(const kda_plan_params& p, cudaStream_t s) {
   const int rows = p.num_tokens > p.num_requests ? p.num_tokens : p.num_requests;
-  int grid = (rows + PLAN_THREADS - 1) / PLAN_THREADS;
+  int grid = rows / PLAN_THREADS + (rows % PLAN_THREADS != 0);
   grid = grid < 1 ? 1 : grid > 152 ? 152 : grid;
   const size_t smem = (size_t)(3 * p.num_requests + 2) * sizeof(int32_t);
   static std::atomic<bool> done{false};

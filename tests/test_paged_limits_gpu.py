@@ -93,3 +93,35 @@ def test_attention_ranges_that_hold_too_many_rows(dev, D):
     err.zero_()
     a.check(*a.run(dev, kda, workspace=ws, error_word=err))
     assert int(err.item()) == 0
+
+
+@pytest.mark.parametrize("requests", [0, 3])
+def test_plan_of_the_most_rows(dev, requests):
+    """num_tokens of 2^31 - 1: the rows past the requests' get -1 up to the last one, and nothing is written beside
+    the arrays (a row number that wrapped would be a store in front of them)."""
+    T, page, pages, guard = 2 ** 31 - 1, 16, 40, 1 << 18
+    words = torch.full((2, guard + T + guard + 1), 7, dtype=torch.int32, device=dev)
+    positions, slots = words[0, guard:guard + T], words[1, guard:guard + T]
+    new, cached = [5, 0, 30][:requests], [20, 3, 16][:requests]
+    table = torch.full((requests, 4), -1, dtype=torch.int32, device=dev)
+    for r, row in enumerate([[1, 2], [3], [4]][:requests]):
+        table[r, :len(row)] = ints(row, dev)
+    def new_ints(n):
+        return torch.empty(n, dtype=torch.int32, device=dev)
+
+    out = kda.PagedPlan(new_ints(requests + 1), new_ints(requests), positions, slots, new_ints(1))
+    err = err_word(dev)
+    kda.kda_paged_plan(ints(cached, dev), ints(new, dev), table, ints(np.arange(10, 20), dev), ints([10], dev), page,
+                       pages, T, out=out, error_word=err)
+    assert int(err.item()) == 0
+    n = sum(new)
+    if requests:
+        assert positions[:n].tolist() == list(range(20, 25)) + list(range(16, 46))
+        assert slots[:5].tolist() == list(range(2 * page + 4, 2 * page + 9))
+        assert slots[5:21].tolist() == list(range(19 * page, 20 * page))
+        assert slots[21:n].tolist() == list(range(18 * page, 18 * page + 14))
+    for x in (positions, slots):
+        for at in range(n, T, 1 << 27):
+            assert (x[at:min(at + (1 << 27), T)] == -1).all()
+    for side in (words[:, :guard], words[:, guard + T:]):
+        assert (side == 7).all()
