@@ -226,6 +226,20 @@ def _stream_handle(stream, device):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _empty(shape, dtype, device, stream):
+    """What a call allocates for itself (its outputs, a workspace), from the pool of the call's stream: memory of the
+    current stream's pool may still be in use by that stream's earlier work. The current stream, which may use it
+    later, is noted, so that the memory is not handed out again while either stream has work with it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if stream.cuda_stream != current.cuda_stream:
+        t.record_stream(current)
+    return t
+
+
 def _params(state, state_indices, q, k, v, g_raw, beta_logit, A_log, dt_bias, out, T,
             lower_bound, scale, error_word, config_override, gate_mode, state_dtype=torch.bfloat16,
             n_indices=None):
@@ -644,7 +658,7 @@ def prepare_paged_plan(cached, new_len, block_table, free_pages, free_count, pag
     p.free_pages, p.free_capacity = _ints(free_pages, "free_pages", (free_pages.numel(),)), free_pages.numel()
     p.free_count = _ints(free_count, "free_count", (1,))
     if out is None:
-        new = lambda n: torch.empty(n, dtype=torch.int32, device=cached.device)  # noqa: E731
+        new = lambda n: _empty(n, torch.int32, cached.device, stream)  # noqa: E731
         out = PagedPlan(new(R + 1), new(R), new(num_tokens), new(num_tokens), new(1))
     p.cu_new, p.kv_len = _ints(out.cu_new, "out.cu_new", (R + 1,)), _ints(out.kv_len, "out.kv_len", (R,))
     p.positions = _ints(out.positions, "out.positions", (num_tokens,))
@@ -689,7 +703,7 @@ def prepare_rope_append(q, k, v, positions, slots, freqs, k_cache, v_cache, q_ou
     p.num_tokens, p.num_q_heads = T, Hq
     p.k, p.v = _rows(k, "k", T, Hkv, D), _rows(v, "v", T, Hkv, D)
     if q_out is None:
-        q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+        q_out = _empty((T, Hq, D), torch.bfloat16, q.device, stream)
     o = _rows(q_out, "q_out", T, Hq, D)
     p.q_out, p.q_out_b_stride, p.q_out_h_stride = o.ptr, o.b_stride, o.h_stride
     p.positions, p.slots = _ints(positions, "positions", (T,)), _ints(slots, "slots", (T,))
@@ -721,11 +735,14 @@ def paged_attention_workspace_bytes(head_dim):
     return int(load_library().kda_paged_attention_workspace_bytes(head_dim))
 
 
-def paged_attention_workspace(head_dim, device):
-    """A device workspace for kda_paged_attention calls on one stream, zeroed as its first use needs."""
+def paged_attention_workspace(head_dim, device, stream=None):
+    """A device workspace for kda_paged_attention calls on one stream (the current one when None), zeroed there as its
+    first use needs. Calls on a stream other than that one must be ordered behind the zeroing."""
     device = torch.device(device)
     with torch.cuda.device(device):
-        return torch.zeros(max(16, paged_attention_workspace_bytes(head_dim)), dtype=torch.uint8, device=device)
+        ws = _empty(max(16, paged_attention_workspace_bytes(head_dim)), torch.uint8, device, stream)
+        with torch.cuda.stream(stream):  # no change when None
+            return ws.zero_()
 
 
 def prepare_paged_attention(q, k_cache, v_cache, block_table, cu_new, kv_len, out=None, lse=None, scale=None,
@@ -740,7 +757,7 @@ def prepare_paged_attention(q, k_cache, v_cache, block_table, cu_new, kv_len, ou
     p.num_requests, p.num_tokens, p.num_q_heads, p.window = R, T, Hq, window
     p.scale = D ** -0.5 if scale is None else scale
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+        out = _empty((T, Hq, D), torch.bfloat16, q.device, stream)
     o = _rows(out, "out", T, Hq, D)
     p.out, p.out_b_stride, p.out_h_stride = o.ptr, o.b_stride, o.h_stride
     if lse is not None:
@@ -752,7 +769,7 @@ def prepare_paged_attention(q, k_cache, v_cache, block_table, cu_new, kv_len, ou
     p.table, p.table_stride, p.table_width = _table(block_table, R)
     p.error_word = _error_word(error_word)
     if workspace is None:
-        workspace = paged_attention_workspace(D, q.device)
+        workspace = paged_attention_workspace(D, q.device, stream)
     _need(workspace, "workspace", torch.uint8)
     if not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous byte tensor")
@@ -769,7 +786,7 @@ def kda_paged_attention(q, k_cache, v_cache, block_table, cu_new, kv_len, out=No
     with any strides, holding the new tokens' keys and values too; block_table:
     int32 [R, W]; kv_len: int32 [R]; lse: optional fp32 [T, Hq], written;
     scale: D ** -0.5 when None; window: keys a row sees at most (0: all);
-    workspace: a paged_attention_workspace kept between calls (allocated when
-    None). Returns out bf16 [T, Hq, D]."""
+    workspace: a paged_attention_workspace kept between calls (allocated and
+    zeroed on the call's stream when None). Returns out bf16 [T, Hq, D]."""
     return prepare_paged_attention(q, k_cache, v_cache, block_table, cu_new, kv_len, out, lse, scale, window,
                                    workspace, error_word, stream)()

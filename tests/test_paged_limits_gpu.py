@@ -125,3 +125,59 @@ def test_plan_of_the_most_rows(dev, requests):
             assert (x[at:min(at + (1 << 27), T)] == -1).all()
     for side in (words[:, :guard], words[:, guard + T:]):
         assert (side == 7).all()
+
+
+# ---------------------------------------------------------------- streams
+
+def test_calls_on_another_stream_allocate_there(dev):
+    """stream= without outputs or a workspace: what the call allocates belongs to that stream. The current stream is
+    kept busy with writes into memory that it gave back to its pool, which a call on the other stream must not get,
+    and a zeroing of the workspace that waited for them would come after the kernel."""
+    a = Attention([1, 3], [3000, 5000], 8, 2, 128, 16, seed=21)
+    args = on_device(a, dev)
+    ref, _ = a.run(dev, kda)
+    a.check(*a.run(dev, kda))
+    T, Hq, D = a.q.shape
+    freqs = kda.rope_freqs(D, device=dev)
+    pos, slots = ints(np.arange(T), dev), ints(np.full(T, -1), dev)
+    turned = kda.kda_rope_append(args[0], args[0][:, :2], args[0][:, :2], pos, slots, freqs, args[1], args[2])
+    plan_in = (ints([5, 0], dev), ints([3, 1], dev), ints([[1, 2], [3, 4]], dev), ints(np.arange(8), dev), ints([8], dev))
+    planned = kda.kda_paged_plan(*plan_in, 4, 16, 4)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    bytes_ = kda.paged_attention_workspace_bytes(D)
+    for _ in range(5):
+        big = torch.full((bytes_,), 7, dtype=torch.uint8, device=dev)
+        small = [torch.full((T * Hq * D,), 7.0, dtype=torch.bfloat16, device=dev) for _ in range(4)]
+        few = [torch.full((n,), 7, dtype=torch.int32, device=dev) for n in (3, 2, 4, 4, 1) * 2]
+        torch.cuda._sleep(20_000_000)  # about 10 ms, then the writes
+        for t in [big] + small + few:
+            t.fill_(9)
+        del big, small, few, t
+        out = kda.kda_paged_attention(*args, scale=a.scale, stream=side)
+        q_out = kda.kda_rope_append(args[0], args[0][:, :2], args[0][:, :2], pos, slots, freqs, args[1], args[2],
+                                    stream=side)
+        plan = kda.kda_paged_plan(*plan_in, 4, 16, 4, stream=side)
+        call = kda.prepare_paged_attention(*args, scale=a.scale, stream=side)
+        prepared = call()
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref) and torch.equal(prepared, ref) and torch.equal(q_out, turned)
+        assert all(torch.equal(x, y) for x, y in zip(plan, planned))
+
+
+def test_memory_of_a_call_on_another_stream_is_not_reused_early(dev):
+    """An unprepared call drops its workspace when it returns, while its kernel has yet to run: the next allocations on
+    the current stream must not get that memory."""
+    a = Attention([1, 3], [3000, 5000], 8, 2, 128, 16, seed=22)
+    args = on_device(a, dev)
+    ref, _ = a.run(dev, kda)
+    side = torch.cuda.Stream()
+    bytes_ = kda.paged_attention_workspace_bytes(a.D)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)
+        out = kda.kda_paged_attention(*args, scale=a.scale, stream=side)
+        over = [torch.full((bytes_,), 9, dtype=torch.uint8, device=dev) for _ in range(3)]
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref) and len(over) == 3
