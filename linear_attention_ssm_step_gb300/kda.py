@@ -736,13 +736,14 @@ def paged_attention_workspace_bytes(head_dim):
 
 
 def paged_attention_workspace(head_dim, device, stream=None):
-    """A device workspace for kda_paged_attention calls on one stream (the current one when None), zeroed there as its
-    first use needs. Calls on a stream other than that one must be ordered behind the zeroing."""
+    """A device workspace for kda_paged_attention calls on one stream (the current one when None), with the part that
+    its first use needs zeroed there. Calls on a stream other than that one must be ordered behind the zeroing."""
     device = torch.device(device)
     with torch.cuda.device(device):
         ws = _empty(max(16, paged_attention_workspace_bytes(head_dim)), torch.uint8, device, stream)
         with torch.cuda.stream(stream):  # no change when None
-            return ws.zero_()
+            ws[:KDA_ATTENTION_WORKSPACE_ZEROED].zero_()
+        return ws
 
 
 def prepare_paged_attention(q, k_cache, v_cache, block_table, cu_new, kv_len, out=None, lse=None, scale=None,

@@ -181,3 +181,22 @@ def test_memory_of_a_call_on_another_stream_is_not_reused_early(dev):
         over = [torch.full((bytes_,), 9, dtype=torch.uint8, device=dev) for _ in range(3)]
         torch.cuda.synchronize()
         assert torch.equal(out, ref) and len(over) == 3
+
+
+# ---------------------------------------------------------------- workspace
+
+@pytest.mark.parametrize("D", [128, 64, 96])
+def test_workspace_needs_zeros_in_its_first_part_alone(dev, D, monkeypatch):
+    """Cut items (two chunks), many parts (one token over a long cache): what lies past the zeroed part is not read
+    before it is written, and the helper clears that part alone (its cost is one small fill, whatever the head size)."""
+    zeroed = kda.KDA_ATTENTION_WORKSPACE_ZEROED
+    a = Attention([300, 1, 8], [700, 20000, 900], 8, 2, D, 16, seed=23).poison()
+    ws = kda.paged_attention_workspace(D, dev)
+    assert (ws[:zeroed] == 0).all()
+    ws[zeroed:].fill_(0xff)  # NaN as fp32
+    err = err_word(dev)
+    a.check(*a.run(dev, kda, workspace=ws, error_word=err))
+    assert int(err.item()) == 0 and (ws[:zeroed] == 0).all()
+    monkeypatch.setattr(kda, "_empty", lambda n, dtype, device, stream: torch.full((n,), 0xff, dtype=dtype, device=device))
+    fresh = kda.paged_attention_workspace(D, dev)
+    assert (fresh[:zeroed] == 0).all() and (fresh[zeroed:] == 0xff).all()
