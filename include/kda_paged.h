@@ -172,8 +172,12 @@ kda_status kda_rope_freqs(uint64_t* freqs, int32_t rotary_dim, double base, int3
  * product with v as bf16 (their sum does not); out is rounded to bf16 once.
  *
  * Keys and values of tokens at or past kv_len do not enter any result, whatever
- * they hold, nor do keys a row does not see enter that row's. A cached value below kv_len that is infinite or
- * NaN makes NaN of the rows that see it, and may of other rows of its request.
+ * they hold, nor do keys a row does not see enter that row's scores. Infinite
+ * and NaN numbers that a row does see act as the formulas say: a score of -inf
+ * is a weight of 0; where all the scores are -inf, out is NaN (0 / 0) and lse
+ * -inf; a score of +inf or NaN makes out and lse NaN. An infinite or NaN number
+ * of a value below kv_len makes infinite or NaN its dimension of out in the
+ * rows that see it, and may make it NaN in other rows of the request.
  *
  * Pages are found through table[r][token / page_size]; entries of pages no row
  * sees are not read. A page outside [0, num_pages) counts as keys and values

@@ -1027,7 +1027,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int slot_id = sg.part == 0 ? 2 * cta + 1 : 2 * cta;
       const int part_row = (dual ? t * TILE : 0) + x;
       uint8_t* const tile = smem + (dual && t ? S::Q1 : S::Q0);
-      const bool none = l == 0.f;  // no key: zeros
+      const bool none = my_row().hi <= 0;  // sees no key: zeros (l is 0 too where every key's score is -inf, which gives 0 / 0)
       const float inv = rcp(l);
       // Where both groups have an O of one tile, each hands the other half of its columns (in the queries' place, which the
       // products are done with) and adds up the other half: columns [from, to) are this thread's.
@@ -1155,7 +1155,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     f[4 * j + 3] = fmaf(v[i][j].w, w[i], f[4 * j + 3]);
                   }
               }
-              stage(f, col, scale, l == 0.f);
+              stage(f, col, scale, none);
             }
           }
         } else if (sh.last_part) {
@@ -1201,8 +1201,9 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int64_t row0 = (int64_t)sg.row0 + div_g(row2);
             const int h = sg.head * g + (row2 - div_g(row2) * g);
             uint16_t* const dst = static_cast<uint16_t*>(p.out) + row0 * p.out_b_stride + (int64_t)h * p.out_h_stride + group * 4;
-            const uint32_t b0 = ll == 0.f ? 0u : pack_bf16x2(acc.x * iv, acc.y * iv);
-            const uint32_t b1 = ll == 0.f ? 0u : pack_bf16x2(acc.z * iv, acc.w * iv);
+            const bool none2 = sg.pos0 + div_g(row2) < 0;
+            const uint32_t b0 = none2 ? 0u : pack_bf16x2(acc.x * iv, acc.y * iv);
+            const uint32_t b1 = none2 ? 0u : pack_bf16x2(acc.z * iv, acc.w * iv);
             if (a.out_wide) {
               *reinterpret_cast<uint2*>(dst) = make_uint2(b0, b1);
             } else {
@@ -1250,7 +1251,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       if (whole && writes && p.lse != nullptr)
         p.lse[((int64_t)sg.row0 + (dual ? t * tpt : 0) + div_g(x)) * p.num_q_heads + sg.head * g + (x - div_g(x) * g)] =
-            m * p.scale + ln(l);  // no key: -inf; only NaN scores: NaN
+            m * p.scale + ln(l);  // no key, or scores of -inf alone: -inf; a score of +inf or NaN: NaN
       if (t == 0)
         bar_sync(3, TILE);
       else

@@ -200,3 +200,92 @@ def test_workspace_needs_zeros_in_its_first_part_alone(dev, D, monkeypatch):
     monkeypatch.setattr(kda, "_empty", lambda n, dtype, device, stream: torch.full((n,), 0xff, dtype=dtype, device=device))
     fresh = kda.paged_attention_workspace(D, dev)
     assert (fresh[:zeroed] == 0).all() and (fresh[zeroed:] == 0xff).all()
+
+
+# ---------------------------------------------------------------- numbers that are not finite
+
+NOT_FINITE = [(128, 16), (64, 16), (96, 16), (33, 5)]  # tensor cores, tensor cores, CUDA cores wide and narrow
+
+
+def key_at(a, r, key):
+    return int(a.table[r, key // a.page]), key % a.page
+
+
+@pytest.mark.parametrize("D,page", NOT_FINITE)
+def test_attention_key_of_minus_infinity(dev, D, page):
+    """One key with -inf in it: where its score is -inf it has weight 0, the same bits as a key whose score is so low
+    that its weight is 0 in fp32; where it is +inf, or -inf times 0, the row is NaN. Rows that do not see it are as
+    without it."""
+    rows = ([1, 150, 3], [300, 400, 260], 8, 2, D, page)
+    key, low = 351, -2.0 ** 13  # of request 1, head 1; 2^13 D^-0.5 >= 512 below the others
+    a, b = Attention(*rows, seed=24), Attention(*rows, seed=24)
+    for x in (a, b):
+        x.q[..., 0] = 1.0
+        x.q[30, :, 0], x.q[140, :, 0] = 0.0, -1.0
+    b.q[140, :, 0] = 1.0
+    at, off = key_at(a, 1, key)
+    a.k[at, off, 1, 0], b.k[at, off, 1, 0] = float("-inf"), low
+    (o, z), (ob, zb) = a.run(dev, kda), b.run(dev, kda)
+    b.check(ob, zb)
+    bad = torch.zeros((154, 8), dtype=torch.bool, device=dev)
+    bad[140, 4:] = True  # row 30 stands before the key, row 140 behind it
+    same = ~bad
+    same[140] = False
+    assert torch.equal(o[same], ob[same]) and torch.equal(z[same], zb[same])
+    assert torch.isnan(o[bad]).all() and torch.isnan(z[bad]).all()
+    assert torch.isfinite(o[140, :4].float()).all() and torch.isfinite(z[140, :4]).all()
+    a.q[140, :, 0] = 0.0
+    o, z = a.run(dev, kda)
+    assert torch.isnan(o[bad]).all() and torch.isnan(z[bad]).all()
+    assert torch.equal(o[same], ob[same]) and torch.equal(z[same], zb[same])
+
+
+@pytest.mark.parametrize("D,page", NOT_FINITE)
+@pytest.mark.parametrize("new,kv,window", [
+    ([1, 5, 1], [1, 5, 0], 0),         # one unit of keys, whole
+    ([2], [20000], 0),                 # many parts of few rows
+    ([300, 7, 9], [700, 500, 4], 0),   # parts of many rows; rows that see no key
+    ([40, 1], [300, 200], 1),          # a row's own key alone
+    ([60] * 3, [2000, 1500, 1800], 100),
+])
+def test_attention_scores_of_minus_infinity_alone(dev, D, page, new, kv, window):
+    """Every key that a row sees has a score of -inf: out is 0 / 0, NaN, and lse -inf, from keys of -inf and from
+    queries of +inf alike; a row that sees no key keeps its zeros."""
+    for infinite in ("k", "q"):
+        a = Attention(new, kv, 8, 2, D, page, window=window, seed=25)
+        a.q[..., 0], a.k[..., 0] = (1.0, float("-inf")) if infinite == "k" else (float("inf"), -1.0)
+        err = err_word(dev)
+        o, z = a.run(dev, kda, error_word=err)
+        pos = torch.tensor(np.concatenate([np.arange(L - n, L) for n, L in zip(new, kv)]), device=dev)
+        assert int(err.item()) == 0 and torch.isneginf(z).all()
+        assert torch.isnan(o[pos >= 0]).all() and (o[pos < 0] == 0).all()
+
+
+@pytest.mark.parametrize("D,page", NOT_FINITE)
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+def test_attention_value_that_is_not_finite(dev, D, page, value):
+    """It stays in its dimension of the rows of its request and head."""
+    rows = ([1, 150, 3], [300, 400, 260], 8, 2, D, page)
+    a, b = Attention(*rows, seed=26), Attention(*rows, seed=26)
+    at, off = key_at(a, 1, 260)
+    a.v[at, off, 1, 3] = value
+    (o, z), (ob, zb) = a.run(dev, kda), b.run(dev, kda)
+    b.check(ob, zb)
+    assert torch.equal(z, zb)
+    assert not torch.isfinite(o[1 + 10:151, 4:, 3].float()).any()  # row 10 of the request stands at key 260
+    o[1:151, 4:, 3] = ob[1:151, 4:, 3]
+    assert torch.equal(o, ob)
+
+
+@pytest.mark.parametrize("D,page", NOT_FINITE)
+def test_attention_query_of_infinity(dev, D, page):
+    """Scores of both signs: +inf among them, so NaN, in that row and head alone."""
+    rows = ([1, 150, 3], [300, 400, 260], 8, 2, D, page)
+    a, b = Attention(*rows, seed=27), Attention(*rows, seed=27)
+    a.q[0, 5, 2], a.q[20, 1, 2] = float("inf"), float("-inf")
+    (o, z), (ob, zb) = a.run(dev, kda), b.run(dev, kda)
+    b.check(ob, zb)
+    for r, h in ((0, 5), (20, 1)):
+        assert torch.isnan(o[r, h]).all() and torch.isnan(z[r, h])
+        o[r, h], z[r, h] = ob[r, h], zb[r, h]
+    assert torch.equal(o, ob) and torch.equal(z, zb)
