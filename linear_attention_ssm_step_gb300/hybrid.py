@@ -72,7 +72,8 @@ class HybridLayers:
         new_len = torch.tensor(new_len, dtype=torch.int32, device=self.device)
         plan = kda.kda_paged_plan(self.cached, new_len, self.block_table, self.free_pages, self.free_count,
                                   self.page_size, self.pages, T, error_word=self.error_word)
-        admitted = plan.kv_len == self.cached + new_len  # the kv_len of a request turned down is 0
+        # the kv_len of a request turned down is 0 (as is the sum for a negative length that takes all of the cached away)
+        admitted = (new_len >= 0) & (plan.kv_len == self.cached + new_len)
         slots = torch.where(admitted, self.slots, -1)
         for kind, w, memory in zip(self.layers, self.weights, self.memory):
             y = self._norm(x) @ w["in"]

@@ -289,3 +289,27 @@ def test_attention_query_of_infinity(dev, D, page):
         assert torch.isnan(o[r, h]).all() and torch.isnan(z[r, h])
         o[r, h], z[r, h] = ob[r, h], zb[r, h]
     assert torch.equal(o, ob) and torch.equal(z, zb)
+
+
+# ---------------------------------------------------------------- hybrid layers
+
+def test_hybrid_layers_turn_down_a_negative_length(dev):
+    """-n tokens for a request of n cached ones: turned down, so its state, cache and length stay, and it goes on as
+    if that step had asked nothing of it (the same bits: the later step has the same shapes)."""
+    from linear_attention_ssm_step_gb300 import hybrid
+    gen = torch.Generator(device=dev).manual_seed(7)
+    x = [torch.randn((n, 256), generator=gen, device=dev).to(torch.bfloat16) for n in (31, 32)]
+    outs = []
+    for asked in (-20, 0):
+        model = hybrid.HybridLayers(hidden=256, layers="ka", heads=2, kv_heads=1, requests=2, pages=8, page_size=16,
+                                    max_tokens=64, device=dev, seed=6)
+        model.step(torch.cat([x[0][:30], x[1][:20]]), [30, 20])
+        own = model.block_table[1, :2].long()
+        state, cache = model.memory[0][1].clone(), model.memory[1][own].clone()
+        model.step(x[0][30:], [1, asked])
+        assert int(model.error_word.item()) == (kda.KDA_ERR_LENGTHS if asked else 0)
+        assert model.cached.tolist() == [31, 20]
+        assert torch.equal(model.memory[0][1], state) and torch.equal(model.memory[1][own], cache)
+        outs.append(model.step(x[1][20:], [0, 12]))
+        assert model.cached.tolist() == [31, 32]
+    assert torch.equal(outs[0], outs[1])
