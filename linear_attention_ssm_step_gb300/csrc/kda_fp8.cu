@@ -398,7 +398,7 @@ template <int TV, bool BULK>
 static cudaError_t launch_vf8(const kda_params& p, const kda_fp8_pool& f, int T, cudaStream_t s) {
   auto kern = kda_verify_fp8_kernel<TV, BULK>;
   const size_t smem = fp8_verify_smem_bytes(TV, KDA_MAX_T);  // sized for any T, so one attribute call suffices
-  static std::atomic<bool> smem_set{false};
+  static DeviceFlags smem_set;
   cudaError_t e = set_smem_limit_once(kern, smem, smem_set);
   if (e != cudaSuccess) return e;
   const int tiles = KD / TV;

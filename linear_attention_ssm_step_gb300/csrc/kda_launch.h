@@ -5,22 +5,49 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cstdint>
 
 #include "kda.h"
 #include "kda_fp8.h"
 
 namespace kda {
 
-// Raise a kernel's dynamic shared-memory limit on its first launch only, so
-// that later calls (including calls made during CUDA-graph capture) make no
-// attribute call. `done` must be a flag owned by that one kernel (a static
-// local of the per-kernel launcher). A failed attempt is retried next launch.
-template <typename Kernel>
-cudaError_t set_smem_limit_once(Kernel kern, size_t bytes, std::atomic<bool>& done) {
-  if (done.load(std::memory_order_acquire)) return cudaSuccess;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (e == cudaSuccess) done.store(true, std::memory_order_release);
+// The devices of this process on which something has been done, a bit each: a kernel's attributes hold for the device
+// that is current when they are set.
+struct DeviceFlags {
+  std::atomic<uint64_t> bits{0};
+};
+
+// Calls `set` on the first use on the current device only (every time beyond 64 devices), so that later calls (including
+// calls made during CUDA-graph capture) make no attribute call. `done` must be owned by that one kernel and attribute (a
+// static local of the per-kernel launcher). A failed attempt is retried next launch.
+template <typename Set>
+cudaError_t once_per_device(DeviceFlags& done, Set set) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev >= 0 && dev < 64 ? uint64_t{1} << dev : 0;
+  if (done.bits.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = set();
+  if (e == cudaSuccess) done.bits.fetch_or(bit, std::memory_order_release);
   return e;
+}
+
+// Raise a kernel's dynamic shared-memory limit.
+template <typename Kernel>
+cudaError_t set_smem_limit_once(Kernel kern, size_t bytes, DeviceFlags& done) {
+  return once_per_device(done, [&] {
+    return cudaFuncSetAttribute(reinterpret_cast<const void*>(kern), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  });
+}
+
+// All of L1 as shared memory for a kernel, so that several of its CTAs fit an SM.
+template <typename Kernel>
+cudaError_t set_carveout_once(Kernel kern, DeviceFlags& done) {
+  return once_per_device(done, [&] {
+    return cudaFuncSetAttribute(reinterpret_cast<const void*>(kern), cudaFuncAttributePreferredSharedMemoryCarveout,
+                                (int)cudaSharedmemCarveoutMaxShared);
+  });
 }
 
 // T-token step (T = 1 is decode). tile_v in {16, 32, 64, 128}; bulk selects

@@ -178,7 +178,7 @@ cudaError_t launch_paged_plan(const kda_plan_params& p, cudaStream_t s) {
   int grid = rows / PLAN_THREADS + (rows % PLAN_THREADS != 0);
   grid = grid < 1 ? 1 : grid > 152 ? 152 : grid;
   const size_t smem = (size_t)(3 * p.num_requests + 2) * sizeof(int32_t);
-  static std::atomic<bool> done{false};
+  static DeviceFlags done;
   const cudaError_t e =
       set_smem_limit_once(kda_paged_plan_kernel, (3 * KDA_MAX_REQUESTS + 2) * sizeof(int32_t), done);
   if (e != cudaSuccess) return e;

@@ -1284,7 +1284,7 @@ template <int D>
 static cudaError_t launch_tc(const CUtensorMap& km, const CUtensorMap& vm, const AttnArgs& a, int ctas, cudaStream_t s) {
   constexpr size_t bytes = Shape<D>::END + sizeof(Shared);
   static_assert(bytes <= 232448, "shared memory of one CTA");
-  static std::atomic<bool> done{false};
+  static DeviceFlags done;
   const cudaError_t e = set_smem_limit_once(kda_paged_attention_tc_kernel<D>, bytes, done);
   if (e != cudaSuccess) return e;
   return launch_early(kda_paged_attention_tc_kernel<D>, dim3((unsigned)ctas), THREADS, bytes, s, km, vm, a);

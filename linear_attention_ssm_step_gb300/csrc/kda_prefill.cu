@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(32 * NW) kda_prefill_kernel(const kda_params p
 template <int TV, int NW>
 static cudaError_t launch_pf(const kda_params& p, const int32_t* cu, int num_seqs, bool bulk, cudaStream_t stream) {
   auto kern = bulk ? kda_prefill_kernel<TV, true, NW> : kda_prefill_kernel<TV, false, NW>;
-  static std::atomic<bool> smem_set_bulk{false}, smem_set_plain{false};
+  static DeviceFlags smem_set_bulk, smem_set_plain;
   cudaError_t e = set_smem_limit_once(kern, prefill_smem_bytes(TV), bulk ? smem_set_bulk : smem_set_plain);
   if (e != cudaSuccess) return e;
   kda_params q = p;  // token t of a chunk is activation row c0 + t

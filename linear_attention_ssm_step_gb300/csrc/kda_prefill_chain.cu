@@ -1015,7 +1015,7 @@ static cudaError_t launch_fused(const CUtensorMap& map, const kda_params& q, con
                                 unsigned char* ws, long long images, uint32_t* flags, int sms, cudaStream_t s) {
   auto kern = kda_prefill_fused_kernel<TMA>;
   const size_t smem = std::max(cn_smem_bytes(), (size_t)FU_TABLE + 4u * FU_MAX_SEQS * 4u + 1024u);
-  static std::atomic<bool> smem_set{false};  // one flag per instantiation
+  static DeviceFlags smem_set;  // one flag per instantiation
   cudaError_t e = set_smem_limit_once(kern, smem, smem_set);
   if (e != cudaSuccess) return e;
   int per_sm = 0;
@@ -1072,7 +1072,7 @@ static cudaError_t launch_chain(const CUtensorMap& map, const kda_params& q, con
                                 const unsigned char* ws, long long images, int sms, cudaStream_t s) {
   auto kern = kda_prefill_chain_kernel<TMA>;
   const size_t smem = cn_smem_bytes();
-  static std::atomic<bool> smem_set{false};  // one flag per instantiation
+  static DeviceFlags smem_set;  // one flag per instantiation
   cudaError_t e = set_smem_limit_once(kern, smem, smem_set);
   if (e != cudaSuccess) return e;
   const long long items = (long long)num_seqs * q.H;
@@ -1111,7 +1111,7 @@ cudaError_t launch_prefill_chain(const kda_params& p, const int32_t* cu, int num
     const bool vec = prefill_rows_aligned16(q);
     auto kern = vec ? kda_prefill_prepare_kernel<true> : kda_prefill_prepare_kernel<false>;
     const size_t smem = pp_smem_bytes(vec);
-    static std::atomic<bool> smem_set_vec{false}, smem_set_plain{false};
+    static DeviceFlags smem_set_vec, smem_set_plain;
     if ((e = set_smem_limit_once(kern, smem, vec ? smem_set_vec : smem_set_plain)) != cudaSuccess) return e;
     const long long per = (long long)num_seqs * p.H;
     const long long want = 8LL * sms;

@@ -597,16 +597,11 @@ static cudaError_t launch_pftc(const CUtensorMap& map, const TokenMaps& tm, cons
                                int num_seqs, cudaStream_t s) {
   auto kern = kda_prefill_tc_kernel<TMA, TOK>;
   const size_t smem = pc_smem_bytes();
-  static std::atomic<bool> smem_set{false};  // one flag per instantiation
+  static DeviceFlags smem_set;  // one flag per instantiation
   cudaError_t e = set_smem_limit_once(kern, smem, smem_set);
   if (e != cudaSuccess) return e;
-  static std::atomic<bool> carveout_set{false};  // all of L1 as shared memory: two CTAs per SM
-  if (!carveout_set.load(std::memory_order_acquire)) {
-    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                  (int)cudaSharedmemCarveoutMaxShared)) != cudaSuccess)
-      return e;
-    carveout_set.store(true, std::memory_order_release);
-  }
+  static DeviceFlags carveout_set;  // all of L1 as shared memory: two CTAs per SM
+  if ((e = set_carveout_once(kern, carveout_set)) != cudaSuccess) return e;
   // Persistent grid: as many CTAs as fit at once (shared memory, registers and
   // the SM's 512 tensor-memory columns), at most one per (sequence, head).
   int dev = 0, sms = 0, smem_sm = 0, reserved = 0, regs_sm = 0, blocks_sm = 0;

@@ -853,16 +853,11 @@ template <bool TMA, int TT, bool CIRC, bool F8 = false>
 static cudaError_t launch_ring_one(const CUtensorMap& map, const kda_params& p, int T, const kda_ring_params& r,
                                    cudaStream_t s, const kda_fp8_pool& f8 = kda_fp8_pool{}) {
   auto kern = kda_ring_kernel<TMA, TT, CIRC, F8>;
-  static std::atomic<bool> smem_set{false};  // one flag per instantiation
+  static DeviceFlags smem_set;  // one flag per instantiation
   cudaError_t e = set_smem_limit_once(kern, ring_smem_bytes(TT, 64, 64), smem_set);
   if (e != cudaSuccess) return e;
-  static std::atomic<bool> carveout_set{false};  // all of L1 as shared memory: several CTAs per SM
-  if (!carveout_set.load(std::memory_order_acquire)) {
-    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                  (int)cudaSharedmemCarveoutMaxShared)) != cudaSuccess)
-      return e;
-    carveout_set.store(true, std::memory_order_release);
-  }
+  static DeviceFlags carveout_set;  // all of L1 as shared memory: several CTAs per SM
+  if ((e = set_carveout_once(kern, carveout_set)) != cudaSuccess) return e;
   // Persistent grid: as many CTAs as fit on the device at once (shared
   // memory, registers, and tensor-memory columns: 512 per SM), at most one
   // per item. The occupancy calculator is not used: it reports one CTA per

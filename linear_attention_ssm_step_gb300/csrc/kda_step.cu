@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(32 * NW, MULTI ? (NW == 8 ? 2 : 1) : 6)
 template <int TV, bool BULK, bool MULTI, int NW, int TT>
 static cudaError_t launch_one(const kda_params& p, int T, cudaStream_t stream) {
   auto kern = kda_step_kernel<TV, BULK, MULTI, NW, TT>;
-  static std::atomic<bool> smem_set{false};  // one flag per instantiation
+  static DeviceFlags smem_set;  // one flag per instantiation
   cudaError_t e = set_smem_limit_once(kern, step_smem_bytes(TV, KDA_MAX_T), smem_set);
   if (e != cudaSuccess) return e;
   const int tiles = KD / TV;

@@ -398,16 +398,11 @@ template <bool TMA, int TT, bool TOK>
 static cudaError_t launch_vtc(const CUtensorMap& map, const VerifyTokenMaps& tm, const kda_params& p, int T,
                               cudaStream_t s) {
   auto kern = kda_verify_tc_kernel<TMA, TT, TOK>;
-  static std::atomic<bool> smem_set{false};  // one flag per instantiation
+  static DeviceFlags smem_set;  // one flag per instantiation
   cudaError_t e = set_smem_limit_once(kern, verify_tc_smem_bytes(TT), smem_set);
   if (e != cudaSuccess) return e;
-  static std::atomic<bool> carveout_set{false};  // all of L1 as shared memory: four CTAs per SM
-  if (!carveout_set.load(std::memory_order_acquire)) {
-    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                  (int)cudaSharedmemCarveoutMaxShared)) != cudaSuccess)
-      return e;
-    carveout_set.store(true, std::memory_order_release);
-  }
+  static DeviceFlags carveout_set;  // all of L1 as shared memory: four CTAs per SM
+  if ((e = set_carveout_once(kern, carveout_set)) != cudaSuccess) return e;
   kern<<<(unsigned)((long long)p.B * p.H), VT_THREADS, verify_tc_smem_bytes(TT), s>>>(map, tm, p, T);
   return cudaGetLastError();
 }
