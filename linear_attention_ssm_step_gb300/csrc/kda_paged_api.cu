@@ -48,12 +48,15 @@ kda_status check_words(const char* name, const void* p, bool needed) {
   return KDA_OK;
 }
 
-// A bf16 tensor whose strides must be in [0, 2^40) so that no extent overflows.
-kda_status check_rows(const char* name, const void* p, int64_t b_stride, int64_t h_stride) {
+// A bf16 tensor of n rows (below 2^31, of at most 2^17 heads). Strides in [0, 2^40) and a span of rows of at most 2^60
+// elements, so that no extent overflows.
+kda_status check_rows(const char* name, const void* p, int64_t n, int64_t b_stride, int64_t h_stride) {
   if (p == nullptr) return fail(KDA_EINVAL, "%s is NULL", name);
   if (!aligned(p, 2)) return fail(KDA_EINVAL, "%s is not 2-byte aligned", name);
   if (b_stride < 0 || h_stride < 0) return fail(KDA_EINVAL, "%s has a negative stride", name);
   if (b_stride >> 40 || h_stride >> 40) return fail(KDA_EUNSUPPORTED, "%s has a stride of 2^40 or more", name);
+  if (n > 1 && b_stride > (int64_t{1} << 60) / (n - 1))
+    return fail(KDA_EUNSUPPORTED, "%s has rows that span more than 2^60 elements", name);
   return KDA_OK;
 }
 
@@ -87,6 +90,7 @@ kda_status check_table(const int32_t* table, int64_t stride, int32_t width, int3
     return fail(KDA_EUNSUPPORTED, "table_width * page_size = %lld tokens, above 2^31 - 256", (long long)width * page_size);
   if (requests > 1 && stride < width)
     return fail(KDA_EINVAL, "table_stride = %lld is below table_width = %d", (long long)stride, width);
+  if (requests > 1 && stride >> 40) return fail(KDA_EUNSUPPORTED, "table_stride = %lld, 2^40 or more", (long long)stride);
   return check_words("table", table, true);
 }
 
@@ -184,10 +188,10 @@ kda_status kda_rope_append(const kda_rope_params* p, void* stream) {
     return fail(KDA_EINVAL, "rotary_dim = %d is not an even number in 0..%d", p->rotary_dim, D);
   if (!isfinite(p->mscale)) return fail(KDA_EINVAL, "mscale is not finite");
   if (p->num_tokens == 0) return ok();
-  if ((s = check_rows("q", p->q.ptr, p->q.b_stride, p->q.h_stride)) != KDA_OK) return s;
-  if ((s = check_rows("k", p->k.ptr, p->k.b_stride, p->k.h_stride)) != KDA_OK) return s;
-  if ((s = check_rows("v", p->v.ptr, p->v.b_stride, p->v.h_stride)) != KDA_OK) return s;
-  if ((s = check_rows("q_out", p->q_out, p->q_out_b_stride, p->q_out_h_stride)) != KDA_OK) return s;
+  if ((s = check_rows("q", p->q.ptr, p->num_tokens, p->q.b_stride, p->q.h_stride)) != KDA_OK) return s;
+  if ((s = check_rows("k", p->k.ptr, p->num_tokens, p->k.b_stride, p->k.h_stride)) != KDA_OK) return s;
+  if ((s = check_rows("v", p->v.ptr, p->num_tokens, p->v.b_stride, p->v.h_stride)) != KDA_OK) return s;
+  if ((s = check_rows("q_out", p->q_out, p->num_tokens, p->q_out_b_stride, p->q_out_h_stride)) != KDA_OK) return s;
   if ((s = check_words("positions", p->positions, true)) != KDA_OK) return s;
   if ((s = check_words("slots", p->slots, true)) != KDA_OK) return s;
   if ((s = check_words("error_word", p->error_word, false)) != KDA_OK) return s;
@@ -274,8 +278,8 @@ kda_status kda_paged_attention(const kda_attention_params* p, void* workspace, s
   if (!isfinite(p->scale) || !(p->scale > 0.f)) return fail(KDA_EINVAL, "scale is not a finite number above 0");
   if (p->num_requests == 0 || p->num_tokens == 0) return ok();
   if ((s = check_table(p->table, p->table_stride, p->table_width, p->cache.page_size, p->num_requests)) != KDA_OK) return s;
-  if ((s = check_rows("q", p->q.ptr, p->q.b_stride, p->q.h_stride)) != KDA_OK) return s;
-  if ((s = check_rows("out", p->out, p->out_b_stride, p->out_h_stride)) != KDA_OK) return s;
+  if ((s = check_rows("q", p->q.ptr, p->num_tokens, p->q.b_stride, p->q.h_stride)) != KDA_OK) return s;
+  if ((s = check_rows("out", p->out, p->num_tokens, p->out_b_stride, p->out_h_stride)) != KDA_OK) return s;
   if ((s = check_words("cu_new", p->cu_new, true)) != KDA_OK) return s;
   if ((s = check_words("kv_len", p->kv_len, true)) != KDA_OK) return s;
   if ((s = check_words("lse", p->lse, false)) != KDA_OK) return s;
