@@ -19,6 +19,10 @@
  * allocated or synchronized, kernels on `stream` only, host-side validation
  * before any launch, kda_last_error(), error words that kernels OR bits into,
  * strides in elements, bf16 tensors with the last dimension contiguous.
+ * Where arguments must not overlap, rows of heads (q, k, v and q_out, q and
+ * out) may lie beside one another in the rows, or in the heads, of one buffer
+ * of a common stride; any others are taken to overlap where their ranges from
+ * the first byte to the last do.
  * Every call is deterministic and can be captured in a CUDA graph.
  */
 #ifndef KDA_GB300_KDA_PAGED_H

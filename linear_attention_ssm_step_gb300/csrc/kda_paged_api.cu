@@ -4,6 +4,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <numeric>
+
 #include "kda_error.h"
 #include "kda_paged.h"
 #include "kda_paged_launch.h"
@@ -46,6 +48,37 @@ kda_status check_words(const char* name, const void* p, bool needed) {
   if (needed && p == nullptr) return fail(KDA_EINVAL, "%s is NULL", name);
   if (!aligned(p, 4)) return fail(KDA_EINVAL, "%s is not 4-byte aligned", name);
   return KDA_OK;
+}
+
+// Rows of heads, in bytes: row i, head j at lo + i b + j h, dim bytes long. A stride that no second entry uses is 0.
+struct Rows {
+  uint64_t lo, b, h, head_span, dim;  // head_span: from a row's first byte to behind its last
+  Extent e;
+};
+
+Rows rows_of(const void* p, int64_t n, int64_t b_stride, int64_t heads, int64_t h_stride, int64_t dim) {
+  Rows r;
+  r.lo = reinterpret_cast<uintptr_t>(p);
+  r.b = n > 1 ? (uint64_t)b_stride * 2 : 0;
+  r.h = heads > 1 ? (uint64_t)h_stride * 2 : 0;
+  r.dim = (uint64_t)dim * 2;
+  r.head_span = (uint64_t)(heads - 1) * r.h + r.dim;
+  r.e = rows_extent(p, n, b_stride, heads, h_stride, dim);
+  return r;
+}
+
+// Whether two tensors may share a byte. They do not where their ranges are apart, and not where they lie beside one another
+// in a common period: modulo a divisor of the strides, every row (every head of every row) of a tensor falls on one
+// interval, and the two intervals are apart (columns of the rows of one buffer, or of its heads).
+bool overlaps(const Rows& x, const Rows& y) {
+  if (!overlaps(x.e, y.e)) return false;
+  const uint64_t rows = std::gcd(x.b, y.b), heads = std::gcd(rows, std::gcd(x.h, y.h));
+  auto apart = [&](uint64_t period, uint64_t x_span, uint64_t y_span) {
+    if (period == 0) return false;
+    const uint64_t to_y = (y.lo % period + period - x.lo % period) % period;
+    return to_y >= x_span && period - to_y >= y_span;
+  };
+  return !apart(rows, x.head_span, y.head_span) && !apart(heads, x.dim, y.dim);
 }
 
 // A bf16 tensor of n rows (below 2^31, of at most 2^17 heads). Strides in [0, 2^40) and a span of rows of at most 2^60
@@ -198,10 +231,10 @@ kda_status kda_rope_append(const kda_rope_params* p, void* stream) {
   if (p->rotary_dim > 0 && (p->freqs == nullptr || !aligned(p->freqs, 8)))
     return fail(KDA_EINVAL, "freqs is NULL or not 8-byte aligned");
   const int64_t T = p->num_tokens;
-  const Extent q = rows_extent(p->q.ptr, T, p->q.b_stride, p->num_q_heads, p->q.h_stride, D);
-  const Extent k = rows_extent(p->k.ptr, T, p->k.b_stride, Hkv, p->k.h_stride, D);
-  const Extent v = rows_extent(p->v.ptr, T, p->v.b_stride, Hkv, p->v.h_stride, D);
-  const Extent o = rows_extent(p->q_out, T, p->q_out_b_stride, p->num_q_heads, p->q_out_h_stride, D);
+  const Rows q = rows_of(p->q.ptr, T, p->q.b_stride, p->num_q_heads, p->q.h_stride, D);
+  const Rows k = rows_of(p->k.ptr, T, p->k.b_stride, Hkv, p->k.h_stride, D);
+  const Rows v = rows_of(p->v.ptr, T, p->v.b_stride, Hkv, p->v.h_stride, D);
+  const Rows o = rows_of(p->q_out, T, p->q_out_b_stride, p->num_q_heads, p->q_out_h_stride, D);
   const Extent ck = pages_extent(p->cache.k, p->cache), cv = pages_extent(p->cache.v, p->cache);
   const bool in_place = p->q_out == p->q.ptr;
   if (in_place && ((p->q_out_b_stride != p->q.b_stride && T > 1) ||
@@ -210,7 +243,7 @@ kda_status kda_rope_append(const kda_rope_params* p, void* stream) {
   if (!in_place && (overlaps(o, q) || overlaps(o, k) || overlaps(o, v)))
     return fail(KDA_EINVAL, "q_out overlaps q, k or v");
   for (const Extent& c : {ck, cv})
-    if (overlaps(c, q) || overlaps(c, k) || overlaps(c, v) || overlaps(c, o))
+    if (overlaps(c, q.e) || overlaps(c, k.e) || overlaps(c, v.e) || overlaps(c, o.e))
       return fail(KDA_EINVAL, "the cache overlaps q, k, v or q_out");
   const bool wide = D % 16 == 0 && p->rotary_dim % 16 == 0 && wide_rows(p->q.ptr, p->q.b_stride, p->q.h_stride) &&
                     wide_rows(p->k.ptr, p->k.b_stride, p->k.h_stride) &&
@@ -285,19 +318,22 @@ kda_status kda_paged_attention(const kda_attention_params* p, void* workspace, s
   if ((s = check_words("lse", p->lse, false)) != KDA_OK) return s;
   if ((s = check_words("error_word", p->error_word, false)) != KDA_OK) return s;
   const size_t rows = (size_t)p->num_tokens * p->num_q_heads, R = (size_t)p->num_requests;
-  const Extent o = rows_extent(p->out, p->num_tokens, p->out_b_stride, p->num_q_heads, p->out_h_stride, D);
+  const Rows q = rows_of(p->q.ptr, p->num_tokens, p->q.b_stride, p->num_q_heads, p->q.h_stride, D);
+  const Rows out = rows_of(p->out, p->num_tokens, p->out_b_stride, p->num_q_heads, p->out_h_stride, D);
+  const Extent& o = out.e;
   const Extent l = bytes_extent(p->lse, p->lse ? rows * 4 : 0);
   const struct {
     const char* name;
     Extent e;
-  } inputs[] = {{"q", rows_extent(p->q.ptr, p->num_tokens, p->q.b_stride, p->num_q_heads, p->q.h_stride, D)},
+  } inputs[] = {{"q", q.e},
                 {"cache.k", pages_extent(p->cache.k, p->cache)},
                 {"cache.v", pages_extent(p->cache.v, p->cache)},
                 {"table", bytes_extent(p->table, (size_t)((R - 1) * p->table_stride + p->table_width) * 4)},
                 {"cu_new", bytes_extent(p->cu_new, (R + 1) * 4)},
                 {"kv_len", bytes_extent(p->kv_len, R * 4)}};
+  if (overlaps(out, q)) return fail(KDA_EINVAL, "out overlaps q");
   for (const auto& in : inputs) {
-    if (overlaps(o, in.e)) return fail(KDA_EINVAL, "out overlaps %s", in.name);
+    if (&in != inputs && overlaps(o, in.e)) return fail(KDA_EINVAL, "out overlaps %s", in.name);
     if (overlaps(l, in.e)) return fail(KDA_EINVAL, "lse overlaps %s", in.name);
   }
   if (overlaps(o, l)) return fail(KDA_EINVAL, "out overlaps lse");

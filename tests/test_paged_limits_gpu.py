@@ -313,3 +313,26 @@ def test_hybrid_layers_turn_down_a_negative_length(dev):
         outs.append(model.step(x[1][20:], [0, 12]))
         assert model.cached.tolist() == [31, 32]
     assert torch.equal(outs[0], outs[1])
+
+
+# ---------------------------------------------------------------- rows beside one another
+
+@pytest.mark.parametrize("D", [128, 64, 96])
+@pytest.mark.parametrize("by_heads", [False, True])
+def test_outputs_beside_their_queries(dev, D, by_heads):
+    """q and the outputs in the rows (or in the heads) of one buffer: the bits of outputs of their own, and q as it was."""
+    a = Attention([1, 150, 5], [300, 400, 260], 8, 2, D, 16, seed=28).poison()
+    args = on_device(a, dev)
+    ref, lse = a.run(dev, kda)
+    a.check(ref, lse)
+    T, H = 156, 8
+    both = torch.full((T, H, 2, D) if by_heads else (T, 2, H, D), 7.0, dtype=torch.bfloat16, device=dev)
+    q, out = (both[:, :, 0], both[:, :, 1]) if by_heads else (both[:, 0], both[:, 1])
+    q.copy_(args[0])
+    kda.kda_paged_attention(q, *args[1:], out=out, scale=a.scale)
+    assert torch.equal(out, ref) and torch.equal(q, args[0])
+    freqs, pos, slots = kda.rope_freqs(D, device=dev), ints(np.arange(T), dev), ints(np.full(T, -1), dev)
+    k = args[0][:, :2].clone()
+    want = kda.kda_rope_append(args[0], k, k, pos, slots, freqs, args[1], args[2])
+    kda.kda_rope_append(q, k, k, pos, slots, freqs, args[1], args[2], q_out=out)
+    assert torch.equal(out, want) and torch.equal(q, args[0])

@@ -6,7 +6,7 @@ import ctypes
 import pytest
 
 from linear_attention_ssm_step_gb300 import _build, kda
-from test_paged_host import UNSUPPORTED, fake_attention, fake_plan, fake_rope, no_gpu, put
+from test_paged_host import INVALID, UNSUPPORTED, fake_attention, fake_plan, fake_rope, no_gpu, put
 
 pytestmark = no_gpu
 
@@ -65,3 +65,72 @@ def test_table_stride_past_40_bits(lib, make):
     p.num_requests, p.table_stride = 1, 1 << 61  # a stride that is not used
     if isinstance(p, kda.KdaPlanParams):
         assert status(lib, p) == kda.KDA_ELAUNCH
+
+
+# ---------------------------------------------------------------- rows beside one another
+
+def set_rows(p, name, ptr, b, h):
+    if name in ("out", "q_out"):
+        setattr(p, name, ptr)
+        setattr(p, name + "_b_stride", b)
+        setattr(p, name + "_h_stride", h)
+    else:
+        setattr(p, name, kda.KdaView(ptr, b, 0, h))
+
+
+FREE = kda.KDA_ELAUNCH  # past the checks: there is no device
+
+
+@pytest.mark.parametrize("place,want", [
+    ("columns", FREE),       # [T, q | out]: columns of one buffer's rows
+    ("swapped", FREE),       # [T, out | q]
+    ("heads", FREE),         # [T, H, q | out]: columns of its heads
+    ("gap", FREE),           # columns with others between
+    ("shifted", INVALID),    # out begins in q's last head
+    ("wraps", INVALID),      # out ends in the next row's q
+    ("other", INVALID),      # a row stride of its own: no common period
+])
+@pytest.mark.parametrize("make", [fake_attention, fake_rope])
+def test_rows_beside_one_another(lib, make, place, want):
+    p = make()
+    out = "out" if make is fake_attention else "q_out"
+    H, D = p.num_q_heads, p.cache.head_dim
+    base, row = 1 << 40, H * D
+    q, o, b, h, ob = {"columns": (0, row, 2 * row, D, 2 * row), "swapped": (row, 0, 2 * row, D, 2 * row),
+                      "heads": (0, D, 2 * row, 2 * D, 2 * row), "gap": (0, 2 * row, 4 * row, D, 4 * row),
+                      "shifted": (0, row - 8, 2 * row, D, 2 * row), "wraps": (0, row + 8, 2 * row, D, 2 * row),
+                      "other": (0, row, 2 * row, D, 3 * row)}[place]
+    set_rows(p, "q", base + 2 * q, b, h)
+    set_rows(p, out, base + 2 * o, ob, h)
+    assert status(lib, p) == want
+    if want == INVALID:
+        assert "overlaps q" in kda.kda_last_error()
+
+
+def test_rows_that_share_an_element_are_always_refused(lib):
+    """Against the sets of elements themselves, over many layouts (strides that repeat rows, heads across rows, rows
+    between rows, odd offsets); and columns that share none are let through often enough to matter."""
+    import random
+    rng = random.Random(5)
+    let_through = 0
+    for _ in range(4000):
+        p = fake_attention()
+        T, Hkv, g, D = rng.choice([1, 2, 5]), rng.choice([1, 2]), rng.choice([1, 2]), rng.choice([1, 3, 8])
+        H = Hkv * g
+        p.num_tokens, p.num_q_heads, p.cache.num_heads, p.cache.head_dim = T, H, Hkv, D
+        period = rng.choice([H * D, 2 * H * D, 2 * H * D + 1, 4 * D])
+        lay = []
+        for _ in range(2):
+            h = rng.choice([D, 2 * D, 2 * D, period, rng.randrange(0, 3 * D + 1)])
+            b = rng.choice([period, period, 2 * H * D, rng.randrange(0, 2 * period + 1)])
+            lay.append((rng.choice([0, D, H * D, rng.randrange(0, 3 * H * D + 1)]), b, h))
+        sets = [{at + t * b + i * h + c for t in range(T) for i in range(H) for c in range(D)} for at, b, h in lay]
+        set_rows(p, "q", (1 << 40) + 2 * lay[0][0], *lay[0][1:])
+        set_rows(p, "out", (1 << 40) + 2 * lay[1][0], *lay[1][1:])
+        got = status(lib, p)
+        assert got in (FREE, INVALID)
+        apart = not (sets[0] & sets[1])
+        assert apart or got == INVALID, (T, H, D, lay)
+        if apart and max(min(s) for s in sets) < min(max(s) for s in sets):  # the ranges are not apart
+            let_through += got == FREE
+    assert let_through > 50
