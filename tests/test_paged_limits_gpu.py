@@ -6,8 +6,9 @@ import numpy as np
 import pytest
 import torch
 
+import paged_sequences as ps
 from linear_attention_ssm_step_gb300 import kda
-from paged_cases import Attention, ints, to_device
+from paged_cases import Attention, ints, rope_bound, to_device
 
 pytestmark = pytest.mark.gpu
 
@@ -336,3 +337,58 @@ def test_outputs_beside_their_queries(dev, D, by_heads):
     want = kda.kda_rope_append(args[0], k, k, pos, slots, freqs, args[1], args[2])
     kda.kda_rope_append(q, k, k, pos, slots, freqs, args[1], args[2], q_out=out)
     assert torch.equal(out, want) and torch.equal(q, args[0])
+
+
+# ---------------------------------------------------------------- the three together
+
+@pytest.mark.parametrize("D,page", [(128, 16), (64, 32), (96, 8)])
+def test_every_token_of_the_three_together(dev, D, page):
+    """Prompts in two chunks, then decode. Each position's key and value are where the block table says, turned (within
+    the append's own bound) and as they were; and each row's attention is that of the whole sequence over the numbers
+    that the GPU holds, within the attention's own bound (which test_paged_limits_host.py shows to be below what a
+    token lost or misplaced changes)."""
+    Hq, Hkv, pages = 8, 2, 48
+    qkv = ps.sequences(Hq, Hkv, D, seed=14)
+    gen = torch.Generator().manual_seed(15)
+    kc = torch.full((pages, page, Hkv, D), float("nan"), dtype=torch.bfloat16, device=dev)
+    vc = kc.clone()
+    table = torch.full((3, 200 // page), -1, dtype=torch.int32, device=dev)
+    free = torch.randperm(pages, generator=gen).to(torch.int32).to(dev)
+    count, cached = ints([pages], dev), torch.zeros(3, dtype=torch.int32, device=dev)
+    freqs = kda.rope_freqs(D // 2, 10000.0, kda.KDA_ROPE_LINEAR, 2.0, device=dev)
+    turns = [int(x) % (1 << 64) for x in freqs.cpu().tolist()]
+    err = err_word(dev)
+    done, got = [0, 0, 0], [[[], [], []] for _ in range(3)]
+    for new in ps.STEPS:
+        rows = torch.cat([qkv[r][done[r]:done[r] + n] for r, n in enumerate(new)]).to(dev)
+        plan = kda.kda_paged_plan(cached, ints(new, dev), table, free, count, page, pages, rows.shape[0], error_word=err)
+        q, k, v = rows[:, :Hq], rows[:, Hq:Hq + Hkv], rows[:, Hq + Hkv:]
+        qo = kda.kda_rope_append(q, k, v, plan.positions, plan.slots, freqs, kc, vc, error_word=err)
+        lse = torch.empty((rows.shape[0], Hq), dtype=torch.float32, device=dev)
+        out = kda.kda_paged_attention(qo, kc, vc, table, plan.cu_new, plan.kv_len, lse=lse, error_word=err)
+        at = 0
+        for r, n in enumerate(new):
+            for x, y in zip(got[r], (qo, out, lse)):
+                x.append(y[at:at + n].double().cpu())
+            at, done[r] = at + n, done[r] + n
+        cached, count = plan.kv_len, plan.free_count
+    assert int(err.item()) == 0 and done == ps.LENGTHS
+    half = D // 4
+
+    def partner(x):
+        y = np.zeros_like(x)
+        y[..., :half], y[..., half:2 * half] = x[..., half:2 * half], x[..., :half]
+        return y
+
+    for r, n in enumerate(ps.LENGTHS):
+        q, out, lse = (torch.cat(x).numpy() for x in got[r])
+        at = torch.arange(n, device=dev)
+        where = table[r][at // page].long(), at % page
+        k, v = kc[where].double().cpu().numpy(), vc[where].double().cpu().numpy()
+        x = qkv[r].double().numpy()
+        assert np.array_equal(v, x[:, Hq + Hkv:])
+        q_ref, k_ref = ps.turned(qkv[r], Hq, Hkv, turns)
+        for g, ref, start in ((q, q_ref, x[:, :Hq]), (k, k_ref, x[:, Hq:Hq + Hkv])):
+            assert (np.abs(g - ref) <= rope_bound(ref, start, partner(start), 1.0)).all()
+        o, z, tol, ztol = ps.attend(q, k, v)
+        assert (np.abs(out - o) <= tol).all() and (np.abs(lse - z) <= ztol).all()

@@ -1,14 +1,15 @@
 """The paged-attention calls on the host, without a GPU: sizes and strides at
-their limits, arguments that share a buffer."""
+their limits, arguments that share a buffer, what the bounds of the tests tell
+apart."""
 
 import ctypes
 
+import numpy as np
 import pytest
 
+import paged_sequences as ps
 from linear_attention_ssm_step_gb300 import _build, kda
 from test_paged_host import INVALID, UNSUPPORTED, fake_attention, fake_plan, fake_rope, no_gpu, put
-
-pytestmark = no_gpu
 
 
 @pytest.fixture(scope="module")
@@ -28,6 +29,7 @@ def status(lib, p):
 
 # ---------------------------------------------------------------- sizes
 
+@no_gpu
 @pytest.mark.parametrize("tensor", ["q", "k", "v", "q_out"])
 def test_rope_rows_whose_span_passes_64_bits(lib, tensor):
     """2^31 - 1 rows 2^39 elements apart: the span, 2^70, must not wrap in the check of what overlaps what."""
@@ -38,6 +40,7 @@ def test_rope_rows_whose_span_passes_64_bits(lib, tensor):
     assert f"{tensor} has rows that span" in kda.kda_last_error()
 
 
+@no_gpu
 @pytest.mark.parametrize("tensor", ["q", "out"])
 def test_attention_rows_whose_span_passes_64_bits(lib, tensor):
     p = fake_attention()
@@ -47,6 +50,7 @@ def test_attention_rows_whose_span_passes_64_bits(lib, tensor):
     assert f"{tensor} has rows that span" in kda.kda_last_error()
 
 
+@no_gpu
 def test_a_span_that_wraps_to_nothing_hides_no_overlap(lib):
     """2^31 - 1 rows of 2^33 elements (2^64 of them, less two rows): wrapped, an extent that ends before it begins, and
     in which q_out, although it stands there, does not lie."""
@@ -56,6 +60,7 @@ def test_a_span_that_wraps_to_nothing_hides_no_overlap(lib):
     assert status(lib, p) == UNSUPPORTED
 
 
+@no_gpu
 @pytest.mark.parametrize("make", [fake_plan, fake_attention])
 def test_table_stride_past_40_bits(lib, make):
     p = make()
@@ -90,6 +95,7 @@ FREE = kda.KDA_ELAUNCH  # past the checks: there is no device
     ("wraps", INVALID),      # out ends in the next row's q
     ("other", INVALID),      # a row stride of its own: no common period
 ])
+@no_gpu
 @pytest.mark.parametrize("make", [fake_attention, fake_rope])
 def test_rows_beside_one_another(lib, make, place, want):
     p = make()
@@ -107,6 +113,7 @@ def test_rows_beside_one_another(lib, make, place, want):
         assert "overlaps q" in kda.kda_last_error()
 
 
+@no_gpu
 def test_rows_that_share_an_element_are_always_refused(lib):
     """Against the sets of elements themselves, over many layouts (strides that repeat rows, heads across rows, rows
     between rows, odd offsets); and columns that share none are let through often enough to matter."""
@@ -134,3 +141,26 @@ def test_rows_that_share_an_element_are_always_refused(lib):
         if apart and max(min(s) for s in sets) < min(max(s) for s in sets):  # the ranges are not apart
             let_through += got == FREE
     assert let_through > 50
+
+
+# ---------------------------------------------------------------- what the bounds tell apart
+
+@pytest.mark.parametrize("D", [128, 64, 96])
+def test_a_lost_or_misplaced_token_exceeds_the_bounds(D):
+    """The sequences of the test of the three calls together: at the decode rows, whose newest key is the row's own,
+    leaving that key out, or taking every key and value from the slot before, breaks the attention's bound."""
+    Hq, Hkv = 8, 2
+    turns = [int(2.0 ** 64 * 10000.0 ** (-4.0 * i / D) / 2 / (2 * np.pi)) for i in range(D // 4)]
+    qkv = ps.sequences(Hq, Hkv, D, seed=14)
+    for r, pos in ps.DECODE_ROWS:
+        q, k = (ps.bf16(x) for x in ps.turned(qkv[r], Hq, Hkv, turns))
+        v = qkv[r].double().numpy()[:, Hq + Hkv:]
+        out, lse, tol, lse_tol = (x[pos] for x in ps.attend(q, k, v))
+        lost = ps.oracle.paged_attention(q[pos:pos + 1], k[None], v[None], np.zeros((1, 1), int), [0, 1], [pos], D ** -0.5, 0)
+        kb, vb = (np.concatenate([x[:1], x[:-1]]) for x in (k, v))
+        back = ps.oracle.paged_attention(q[pos:pos + 1], kb[None], vb[None], np.zeros((1, 1), int), [0, 1], [pos + 1],
+                                         D ** -0.5, 0)
+        for wrong in (lost, back):
+            # in some head: one in which the newest key has little weight cannot tell by its output
+            assert (np.abs(wrong[0][0] - out) > tol).any()
+            assert (np.abs(wrong[1][0] - lse) > lse_tol).any()
