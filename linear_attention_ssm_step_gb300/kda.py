@@ -302,7 +302,7 @@ def kda_decode(state, state_indices, q, k, v, g_raw, beta_logit, A_log, dt_bias,
     returns out bf16 [B, H, 128]. With gate_mode=KDA_GATE_PRECOMPUTED, g_raw holds
     log-space g, beta_logit holds beta, and A_log / dt_bias may be None."""
     if out is None:
-        out = torch.empty((q.shape[0], q.shape[1], 128), dtype=torch.bfloat16, device=q.device)
+        out = _empty((q.shape[0], q.shape[1], 128), torch.bfloat16, q.device, stream)
     p = _params(state, state_indices, q, k, v, g_raw, beta_logit, A_log, dt_bias, out, None,
                 lower_bound, scale, error_word, config_override, gate_mode)
     _check(load_library().kda_decode(ctypes.byref(p), _stream_handle(stream, q.device)))
@@ -331,7 +331,7 @@ def prepare_decode(state, state_indices, q, k, v, g_raw, beta_logit, A_log, dt_b
                    stream=None):
     """kda_decode bound to these tensors (see PreparedCall); same arguments."""
     if out is None:
-        out = torch.empty((q.shape[0], q.shape[1], 128), dtype=torch.bfloat16, device=q.device)
+        out = _empty((q.shape[0], q.shape[1], 128), torch.bfloat16, q.device, stream)
     p = _params(state, state_indices, q, k, v, g_raw, beta_logit, A_log, dt_bias, out, None,
                 lower_bound, scale, error_word, config_override, gate_mode)
     keep = (p, state, state_indices, q, k, v, g_raw, beta_logit, A_log, dt_bias, error_word)
@@ -345,7 +345,7 @@ def kda_decode_fp8(codes, scales, state_indices, q, k, v, g_raw, beta_logit, A_l
     [N, H, 128, 128] (E4M3) and scales fp32 [N, H, 128] (powers of two), both
     updated in place for active rows; other arguments as kda_decode."""
     if out is None:
-        out = torch.empty((q.shape[0], q.shape[1], 128), dtype=torch.bfloat16, device=q.device)
+        out = _empty((q.shape[0], q.shape[1], 128), torch.bfloat16, q.device, stream)
     p = _params(codes, state_indices, q, k, v, g_raw, beta_logit, A_log, dt_bias, out, None,
                 lower_bound, scale, error_word, config_override, gate_mode, state_dtype=torch.uint8)
     f = _fp8_pool(codes, scales)
@@ -361,7 +361,7 @@ def kda_verify_fp8(codes, scales, state_indices, q, k, v, g_raw, beta_logit, A_l
     ([B, T, H, 128]); equal to T kda_decode_fp8 calls, bit for bit."""
     B, T, H = q.shape[0], q.shape[1], q.shape[2]
     if out is None:
-        out = torch.empty((B, T, H, 128), dtype=torch.bfloat16, device=q.device)
+        out = _empty((B, T, H, 128), torch.bfloat16, q.device, stream)
     p = _params(codes, state_indices, q, k, v, g_raw, beta_logit, A_log, dt_bias, out, T,
                 lower_bound, scale, error_word, config_override, gate_mode, state_dtype=torch.uint8)
     f = _fp8_pool(codes, scales)
@@ -379,7 +379,7 @@ def kda_verify_ring_fp8(codes, scales, state_indices, q, k, v, g_raw, beta_logit
     kda_verify_ring's."""
     B, T, H = q.shape[0], q.shape[1], q.shape[2]
     if out is None:
-        out = torch.empty((B, T, H, 128), dtype=torch.bfloat16, device=q.device)
+        out = _empty((B, T, H, 128), torch.bfloat16, q.device, stream)
     p = _params(codes, state_indices, q, k, v, g_raw, beta_logit, A_log, dt_bias, out, T,
                 lower_bound, scale, error_word, config_override, gate_mode, state_dtype=torch.uint8)
     r = _ring_params(codes, H, k_cache, u_cache, g_cache, hist_len, flush_min, restart_hist_on_flush, cache_base)
@@ -401,7 +401,7 @@ def prepare_decode_fp8(codes, scales, state_indices, q, k, v, g_raw, beta_logit,
                        stream=None):
     """kda_decode_fp8 bound to these tensors (see PreparedCall); same arguments."""
     if out is None:
-        out = torch.empty((q.shape[0], q.shape[1], 128), dtype=torch.bfloat16, device=q.device)
+        out = _empty((q.shape[0], q.shape[1], 128), torch.bfloat16, q.device, stream)
     p = _params(codes, state_indices, q, k, v, g_raw, beta_logit, A_log, dt_bias, out, None,
                 lower_bound, scale, error_word, config_override, gate_mode, state_dtype=torch.uint8)
     f = _fp8_pool(codes, scales)
@@ -417,7 +417,7 @@ def kda_verify(state, state_indices, q, k, v, g_raw, beta_logit, A_log, dt_bias,
     returns out bf16 [B, T, H, 128]."""
     B, T, H = q.shape[0], q.shape[1], q.shape[2]
     if out is None:
-        out = torch.empty((B, T, H, 128), dtype=torch.bfloat16, device=q.device)
+        out = _empty((B, T, H, 128), torch.bfloat16, q.device, stream)
     p = _params(state, state_indices, q, k, v, g_raw, beta_logit, A_log, dt_bias, out, T,
                 lower_bound, scale, error_word, config_override, gate_mode)
     _check(load_library().kda_verify(ctypes.byref(p), T, _stream_handle(stream, q.device)))
@@ -430,7 +430,7 @@ def prepare_verify(state, state_indices, q, k, v, g_raw, beta_logit, A_log, dt_b
     """kda_verify bound to these tensors (see PreparedCall); same arguments."""
     B, T, H = q.shape[0], q.shape[1], q.shape[2]
     if out is None:
-        out = torch.empty((B, T, H, 128), dtype=torch.bfloat16, device=q.device)
+        out = _empty((B, T, H, 128), torch.bfloat16, q.device, stream)
     p = _params(state, state_indices, q, k, v, g_raw, beta_logit, A_log, dt_bias, out, T,
                 lower_bound, scale, error_word, config_override, gate_mode)
     keep = (p, state, state_indices, q, k, v, g_raw, beta_logit, A_log, dt_bias, error_word)
@@ -448,7 +448,7 @@ def kda_verify_ring(state, state_indices, q, k, v, g_raw, beta_logit, A_log, dt_
     bf16 [B, T, H, 128]."""
     B, T, H = q.shape[0], q.shape[1], q.shape[2]
     if out is None:
-        out = torch.empty((B, T, H, 128), dtype=torch.bfloat16, device=q.device)
+        out = _empty((B, T, H, 128), torch.bfloat16, q.device, stream)
     p = _params(state, state_indices, q, k, v, g_raw, beta_logit, A_log, dt_bias, out, T,
                 lower_bound, scale, error_word, config_override, gate_mode)
     r = _ring_params(state, H, k_cache, u_cache, g_cache, hist_len, flush_min, restart_hist_on_flush, cache_base)
@@ -464,7 +464,7 @@ def prepare_verify_ring(state, state_indices, q, k, v, g_raw, beta_logit, A_log,
     """kda_verify_ring bound to these tensors (see PreparedCall); same arguments."""
     B, T, H = q.shape[0], q.shape[1], q.shape[2]
     if out is None:
-        out = torch.empty((B, T, H, 128), dtype=torch.bfloat16, device=q.device)
+        out = _empty((B, T, H, 128), torch.bfloat16, q.device, stream)
     p = _params(state, state_indices, q, k, v, g_raw, beta_logit, A_log, dt_bias, out, T,
                 lower_bound, scale, error_word, config_override, gate_mode)
     r = _ring_params(state, H, k_cache, u_cache, g_cache, hist_len, flush_min, restart_hist_on_flush, cache_base)
@@ -512,7 +512,7 @@ def kda_prefill(state, state_indices, cu_seqlens, q, k, v, g_raw, beta_logit, A_
     of at least prefill_workspace_bytes(L, S, H) (kda_prefill_ws, which may
     then choose the two-stage configuration 5)."""
     if out is None:
-        out = torch.empty((q.shape[0], q.shape[1], 128), dtype=torch.bfloat16, device=q.device)
+        out = _empty((q.shape[0], q.shape[1], 128), torch.bfloat16, q.device, stream)
     fn, args, _ = _prefill_call(state, state_indices, cu_seqlens, q, k, v, g_raw, beta_logit, A_log, dt_bias,
                                 out, lower_bound, scale, error_word, config_override, gate_mode, stream, workspace)
     _check(fn(*args))
@@ -547,7 +547,7 @@ def prepare_prefill(state, state_indices, cu_seqlens, q, k, v, g_raw, beta_logit
     """kda_prefill bound to these tensors (see PreparedCall); same arguments. The
     sequence count is fixed by cu_seqlens' length; its contents may change."""
     if out is None:
-        out = torch.empty((q.shape[0], q.shape[1], 128), dtype=torch.bfloat16, device=q.device)
+        out = _empty((q.shape[0], q.shape[1], 128), torch.bfloat16, q.device, stream)
     fn, args, keep = _prefill_call(state, state_indices, cu_seqlens, q, k, v, g_raw, beta_logit, A_log, dt_bias,
                                    out, lower_bound, scale, error_word, config_override, gate_mode, stream,
                                    workspace)
