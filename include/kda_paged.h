@@ -88,6 +88,16 @@ typedef struct {
  * get -1 too. A page number outside [0, num_pages), in the table or the free
  * list, gives slot -1 and KDA_ERR_PAGES. *free_count outside [0,
  * free_capacity] is taken as the nearer bound.
+ *
+ * Pages come back through the caller: the plan counts tokens, so a page past
+ * ceil(cached / page_size) is no longer the request's, and its table entry is
+ * written again when the request grows. After a step a request holds the
+ * first ceil(kv_len / page_size) entries of its row. Where fewer tokens are
+ * kept (drafts that a verify step rejects: cached < kv_len), the entries from
+ * ceil(cached / page_size) on go back to the end of the free list, and their
+ * number onto *free_count, before the next plan; all of them do when a
+ * request ends. free_pages needs the room: free_capacity of num_pages always
+ * has it.
  */
 typedef struct {
   int32_t num_requests; /* 0..KDA_MAX_REQUESTS */

@@ -678,7 +678,9 @@ def kda_paged_plan(cached, new_len, block_table, free_pages, free_count, page_si
     free_count[0] are free (taken from the end); num_tokens: rows of positions
     and slots (at least the sum of new_len; rows beyond it get -1). Returns
     PagedPlan(cu_new [R + 1], kv_len [R], positions, slots [num_tokens],
-    free_count [1]), all int32; pass the returned free_count to the next call."""
+    free_count [1]), all int32; pass the returned free_count to the next call.
+    Pages of tokens that are not kept (rejected drafts, requests that end) are
+    put back at the end of the free list by the caller, before the next call."""
     return prepare_paged_plan(cached, new_len, block_table, free_pages, free_count, page_size, num_pages, num_tokens,
                               out, error_word, stream)()
 

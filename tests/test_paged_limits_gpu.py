@@ -392,3 +392,51 @@ def test_every_token_of_the_three_together(dev, D, page):
             assert (np.abs(g - ref) <= rope_bound(ref, start, partner(start), 1.0)).all()
         o, z, tol, ztol = ps.attend(q, k, v)
         assert (np.abs(out - o) <= tol).all() and (np.abs(lse - z) <= ztol).all()
+
+
+def test_pages_of_rejected_drafts_come_back(dev):
+    """Verify steps of eight drafts of which some are rejected, and a request that ends: the caller puts the pages that
+    are no longer needed back at the end of the free list, as the header says. No page is lost or owned twice, and the
+    attention over what was kept is right."""
+    Hq, Hkv, D, page, pages, R = 4, 2, 64, 4, 60, 3
+    rng = np.random.default_rng(29)
+    gen = torch.Generator().manual_seed(29)
+    kc, vc = (torch.full((pages, page, Hkv, D), float("nan"), dtype=torch.bfloat16, device=dev) for _ in range(2))
+    table = torch.full((R, 30), -1, dtype=torch.int32, device=dev)
+    free = ints(rng.permutation(pages), dev)
+    count, cached = ints([pages], dev), ints([0] * R, dev)
+    freqs, err = torch.zeros(0, dtype=torch.int64, device=dev), err_word(dev)  # nothing turned: the keys as they are
+    kept = [torch.zeros((0, 2, Hkv, D), dtype=torch.bfloat16) for _ in range(R)]  # keys and values of the kept tokens
+
+    def give_back(r, tokens, count):
+        held, still = -(-int(cached[r]) // page), -(-tokens // page)
+        n = int(count.item())
+        free[n:n + held - still] = table[r, still:held]
+        cached[r] = tokens
+        return count + (held - still)
+
+    for step in range(12):
+        new = [17, 5, 1] if step == 0 else [8] * R
+        rows = torch.randn((sum(new), Hq + 2 * Hkv, D), generator=gen).to(torch.bfloat16)
+        q, k, v = (x.to(dev) for x in (rows[:, :Hq], rows[:, Hq:Hq + Hkv], rows[:, Hq + Hkv:]))
+        plan = kda.kda_paged_plan(cached, ints(new, dev), table, free, count, page, pages, sum(new), error_word=err)
+        kda.kda_rope_append(q, k, v, plan.positions, plan.slots, freqs, kc, vc, error_word=err)
+        out = kda.kda_paged_attention(q, kc, vc, table, plan.cu_new, plan.kv_len, error_word=err)
+        cached, count = plan.kv_len.clone(), plan.free_count.clone()
+        at = 0
+        for r, n in enumerate(new):
+            mine = rows[at:at + n]
+            seen = torch.cat([kept[r], torch.stack([mine[:, Hq:Hq + Hkv], mine[:, Hq + Hkv:]], 1)])
+            ref = np.zeros((len(seen), Hq, D))
+            ref[len(seen) - n:] = mine[:, :Hq].double().numpy()
+            o, _, tol, _ = ps.attend(ref, seen[:, 0].double().numpy(), seen[:, 1].double().numpy())
+            got = out[at:at + n].double().cpu().numpy()
+            assert (np.abs(got - o[-n:]) <= tol[-n:]).all()
+            accepted = n if step == 0 else int(rng.integers(1, 9))
+            tokens = 0 if step == 6 and r == 1 else len(seen) - n + accepted  # request 1 ends, and its row is used again
+            kept[r] = seen[:tokens]
+            count = give_back(r, tokens, count)
+            at += n
+        owned = [int(p) for r in range(R) for p in table[r, :-(-int(cached[r]) // page)]]
+        assert sorted(owned + free[:int(count.item())].tolist()) == list(range(pages))
+    assert int(err.item()) == 0
