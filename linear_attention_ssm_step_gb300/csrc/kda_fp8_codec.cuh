@@ -30,6 +30,17 @@ __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(f32x2 v) {
   return r;
 }
 
+// Four codes of a word, and one, as fp32 values.
+__device__ __forceinline__ void e4m3x4_to_floats(uint32_t four, float* f) {
+  upk2(e4m3x2_to_f32x2(four), f[0], f[1]);
+  upk2(e4m3x2_to_f32x2(four >> 16), f[2], f[3]);
+}
+__device__ __forceinline__ float e4m3_to_float(uint32_t code) {
+  float lo, hi;
+  upk2(e4m3x2_to_f32x2(code & 0xffu), lo, hi);
+  return lo;
+}
+
 // 2^e as an fp32 value, exactly, for -149 <= e <= 127.
 __device__ __forceinline__ float pow2f(int e) {
   return e >= -126 ? __uint_as_float((uint32_t)(e + 127) << 23) : __uint_as_float(1u << (e + 149));

@@ -1,8 +1,12 @@
 // kda_paged.cu - the page plan of a step, rotary positions with the append to
 // the paged cache, and paged attention on the CUDA cores (include/kda_paged.h).
+#include <type_traits>
+
 #include "kda_device.cuh"
+#include "kda_fp8_codec.cuh"
 #include "kda_paged.cuh"
 #include "kda_paged_launch.h"
+#include "kda_rope.cuh"
 
 namespace kda {
 
@@ -201,39 +205,6 @@ cudaError_t launch_paged_plan(const kda_plan_params& p, cudaStream_t s) {
 constexpr int ROPE_THREADS = 128, ROPE_CTAS = 16;  // a full SM: 32 registers a thread
 
 template <int VEC>
-struct alignas(2 * VEC) Run {
-  uint16_t x[VEC];
-};
-
-template <int VEC>
-__device__ __forceinline__ Run<VEC> load_run(const uint16_t* p) {
-  Run<VEC> r;
-  if constexpr (VEC == 8)
-    *reinterpret_cast<uint4*>(r.x) = *reinterpret_cast<const uint4*>(p);
-  else
-    r.x[0] = *p;
-  return r;
-}
-
-template <int VEC>
-__device__ __forceinline__ void store_run(uint16_t* p, const Run<VEC>& r) {
-  if constexpr (VEC == 8)
-    *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(r.x);
-  else
-    *p = r.x[0];
-}
-
-// One task: a run of VEC values at `a` and one at `b` of a head, turned or not.
-template <int VEC>
-struct RopeTask {
-  const uint16_t* src;
-  uint16_t* dst;
-  int a, b, c;    // c: the first pair's run, -1 when nothing turns
-  bool two;       // an odd head_dim ends in a single value (VEC == 1)
-  Run<VEC> ra, rb;
-};
-
-template <int VEC>
 __global__ void __launch_bounds__(ROPE_THREADS, ROPE_CTAS) kda_rope_append_kernel(kda_rope_params p) {
   __shared__ float2 turn[128];  // mscale (cos, sin) of pair i
   const int t = blockIdx.x, tid = threadIdx.x;
@@ -290,29 +261,7 @@ __global__ void __launch_bounds__(ROPE_THREADS, ROPE_CTAS) kda_rope_append_kerne
     j.dst = h < Hq ? qo + (int64_t)h * p.q_out_h_stride
                    : h < Hq + Hkv ? ck + (int64_t)(h - Hq) * p.cache.k.head_stride
                                   : cv + (int64_t)(h - Hq - Hkv) * p.cache.v.head_stride;
-    if (j.c >= 0) {
-      if (VEC == 8 && p.interleaved) {
-#pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-          const int e0 = VEC == 8 ? e : 0, e1 = VEC == 8 ? e + 1 : 0;
-          const float2 u = turn[(j.a + e) >> 1], w = turn[(j.b + e) >> 1];
-          const float xa = bf16_bits_to_float(j.ra.x[e0]), ya = bf16_bits_to_float(j.ra.x[e1]);
-          j.ra.x[e0] = float_to_bf16_bits(xa * u.x - ya * u.y);
-          j.ra.x[e1] = float_to_bf16_bits(ya * u.x + xa * u.y);
-          const float xb = bf16_bits_to_float(j.rb.x[e0]), yb = bf16_bits_to_float(j.rb.x[e1]);
-          j.rb.x[e0] = float_to_bf16_bits(xb * w.x - yb * w.y);
-          j.rb.x[e1] = float_to_bf16_bits(yb * w.x + xb * w.y);
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const float2 u = turn[j.c + e];
-          const float x = bf16_bits_to_float(j.ra.x[e]), y = bf16_bits_to_float(j.rb.x[e]);
-          j.ra.x[e] = float_to_bf16_bits(x * u.x - y * u.y);
-          j.rb.x[e] = float_to_bf16_bits(y * u.x + x * u.y);
-        }
-      }
-    }
+    if (j.c >= 0) turn_task<VEC>(j, turn, p.interleaved);
     store_run<VEC>(j.dst + j.a, j.ra);
     if (j.two) store_run<VEC>(j.dst + j.b, j.rb);
   };
@@ -338,7 +287,8 @@ cudaError_t launch_rope_append(const kda_rope_params& p, bool wide, cudaStream_t
 // the head's dimensions and add the 32 value rows, each weight broadcast from
 // its lane. The warps' sums are joined in their order at the end. WIDE: rows on
 // 16 bytes (and head_dim a multiple of 8), so that a lane reads 8 values of a
-// key, and 2 of a value row, at a time.
+// key, and 2 of a value row, at a time. FP8: a cache in 8 bits, its codes in the
+// places of the values; a key's score and weight are scaled by its block's.
 //
 // Bound by the issue of its loads and products: every query head of a group
 // reads the keys again (from L2 or L1). 32 requests of 4000 tokens, 32 query
@@ -349,14 +299,22 @@ cudaError_t launch_rope_append(const kda_rope_params& p, bool wide, cudaStream_t
 constexpr int ATTN_WARPS = 8;
 constexpr int ATTN_MAX_D = 256;
 
-template <bool WIDE>
-__global__ void __launch_bounds__(ATTN_WARPS * 32) kda_paged_attention_simt_kernel(kda_attention_params p) {
+template <bool WIDE, bool FP8>
+__global__ void __launch_bounds__(ATTN_WARPS * 32)
+    kda_paged_attention_simt_kernel(kda_attention_params p, kda_paged_scales sc) {
+  using Elem = std::conditional_t<FP8, uint8_t, uint16_t>;
+  auto value = [](Elem x) {
+    if constexpr (FP8)
+      return e4m3_to_float(x);
+    else
+      return bf16_bits_to_float(x);
+  };
   __shared__ __align__(16) float qs[ATTN_MAX_D];
   __shared__ float part_o[ATTN_WARPS][ATTN_MAX_D], part_m[ATTN_WARPS], part_l[ATTN_WARPS];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int D = p.cache.head_dim, P = p.cache.page_size, g = p.num_q_heads / p.cache.num_heads;
-  const uint16_t* const kc = static_cast<const uint16_t*>(p.cache.k.ptr);
-  const uint16_t* const vc = static_cast<const uint16_t*>(p.cache.v.ptr);
+  const Elem* const kc = static_cast<const Elem*>(p.cache.k.ptr);
+  const Elem* const vc = static_cast<const Elem*>(p.cache.v.ptr);
   const int r = blockIdx.y;
   earlier_work();
   const AttnRequest q = attn_request(p, r);
@@ -379,7 +337,7 @@ __global__ void __launch_bounds__(ATTN_WARPS * 32) kda_paged_attention_simt_kern
     for (int i = 0; i < ATTN_MAX_D / 32; ++i) acc[i] = 0.f;
     for (long long k0 = (long long)lo + warp * 32; k0 < hi; k0 += ATTN_WARPS * 32) {
       const int key = (int)k0 + lane;
-      float s = -INFINITY;
+      float s = -INFINITY, vscale = 1.f;
       int page = -1, place = 0;
       if (key < hi) {
         page = table[key / P];
@@ -390,9 +348,26 @@ __global__ void __launch_bounds__(ATTN_WARPS * 32) kda_paged_attention_simt_kern
         }
         s = 0.f;
         if (page >= 0) {
-          const uint16_t* const kr = kc + page * p.cache.k.page_stride + (int64_t)place * p.cache.k.token_stride +
-                                     (int64_t)hk * p.cache.k.head_stride;
-          if (WIDE) {
+          const Elem* const kr = kc + page * p.cache.k.page_stride + (int64_t)place * p.cache.k.token_stride +
+                                 (int64_t)hk * p.cache.k.head_stride;
+          if constexpr (WIDE && FP8) {
+#pragma unroll 4
+            for (int c = 0; c < D; c += 8) {
+              const uint2 x = *reinterpret_cast<const uint2*>(kr + c);
+              const float4 q0 = *reinterpret_cast<const float4*>(qs + c), q1 = *reinterpret_cast<const float4*>(qs + c + 4);
+              float f[8];
+              e4m3x4_to_floats(x.x, f);
+              e4m3x4_to_floats(x.y, f + 4);
+              s = fmaf(q0.x, f[0], s);
+              s = fmaf(q0.y, f[1], s);
+              s = fmaf(q0.z, f[2], s);
+              s = fmaf(q0.w, f[3], s);
+              s = fmaf(q1.x, f[4], s);
+              s = fmaf(q1.y, f[5], s);
+              s = fmaf(q1.z, f[6], s);
+              s = fmaf(q1.w, f[7], s);
+            }
+          } else if constexpr (WIDE) {
 #pragma unroll 4
             for (int c = 0; c < D; c += 8) {
               const uint4 x = *reinterpret_cast<const uint4*>(kr + c);
@@ -407,7 +382,11 @@ __global__ void __launch_bounds__(ATTN_WARPS * 32) kda_paged_attention_simt_kern
               s = fmaf(q1.w, __uint_as_float(x.w & 0xffff0000u), s);
             }
           } else {
-            for (int c = 0; c < D; ++c) s = fmaf(qs[c], bf16_bits_to_float(kr[c]), s);
+            for (int c = 0; c < D; ++c) s = fmaf(qs[c], value(kr[c]), s);
+          }
+          if constexpr (FP8) {
+            s *= block_scale(sc.k, page, place, hk);
+            vscale = block_scale(sc.v, page, place, hk);
           }
         }
         s *= p.scale;
@@ -424,23 +403,30 @@ __global__ void __launch_bounds__(ATTN_WARPS * 32) kda_paged_attention_simt_kern
       const int count = (int)min(32LL, hi - k0);
 #pragma unroll 4
       for (int u = 0; u < count; ++u) {
-        const float wu = __shfl_sync(0xffffffffu, w, u);
+        const float wu = __shfl_sync(0xffffffffu, FP8 ? w * vscale : w, u);
         const int pu = __shfl_sync(0xffffffffu, page, u), at = __shfl_sync(0xffffffffu, place, u);
         if (pu < 0) continue;  // the same for the whole warp
-        const uint16_t* const vr = vc + pu * p.cache.v.page_stride + (int64_t)at * p.cache.v.token_stride +
-                                   (int64_t)hk * p.cache.v.head_stride;
+        const Elem* const vr = vc + pu * p.cache.v.page_stride + (int64_t)at * p.cache.v.token_stride +
+                               (int64_t)hk * p.cache.v.head_stride;
         if (WIDE) {
 #pragma unroll
           for (int i = 0; i < ATTN_MAX_D / 32; i += 2)
             if (dim(i) < D) {
-              const uint32_t x = *reinterpret_cast<const uint32_t*>(vr + dim(i));
-              acc[i] = fmaf(wu, __uint_as_float(x << 16), acc[i]);
-              acc[i + 1] = fmaf(wu, __uint_as_float(x & 0xffff0000u), acc[i + 1]);
+              float v0, v1;
+              if constexpr (FP8) {
+                upk2(e4m3x2_to_f32x2(*reinterpret_cast<const uint16_t*>(vr + dim(i))), v0, v1);
+              } else {
+                const uint32_t x = *reinterpret_cast<const uint32_t*>(vr + dim(i));
+                v0 = __uint_as_float(x << 16);
+                v1 = __uint_as_float(x & 0xffff0000u);
+              }
+              acc[i] = fmaf(wu, v0, acc[i]);
+              acc[i + 1] = fmaf(wu, v1, acc[i + 1]);
             }
         } else {
 #pragma unroll
           for (int i = 0; i < ATTN_MAX_D / 32; ++i)
-            if (dim(i) < D) acc[i] = fmaf(wu, bf16_bits_to_float(vr[dim(i)]), acc[i]);
+            if (dim(i) < D) acc[i] = fmaf(wu, value(vr[dim(i)]), acc[i]);
         }
       }
     }
@@ -471,17 +457,21 @@ __global__ void __launch_bounds__(ATTN_WARPS * 32) kda_paged_attention_simt_kern
   if (bad_page && p.error_word) atomicOr(p.error_word, KDA_ERR_PAGES);
 }
 
-cudaError_t launch_paged_attention_simt(const kda_attention_params& p, cudaStream_t s) {
+cudaError_t launch_paged_attention_simt(const kda_attention_params& p, const kda_paged_scales* scales, cudaStream_t s) {
   const long long rows = (long long)p.num_tokens * p.num_q_heads;
   const long long per = rows / p.num_requests + 1;
   const dim3 grid((unsigned)(per > 4096 ? 4096 : per), (unsigned)p.num_requests);
-  auto rows16 = [](const kda_pages& g) {
-    return (reinterpret_cast<uintptr_t>(g.ptr) & 15) == 0 && g.page_stride % 8 == 0 && g.token_stride % 8 == 0 &&
-           g.head_stride % 8 == 0;
+  auto rows8 = [&](const kda_pages& g) {  // 8 elements at a time
+    return (reinterpret_cast<uintptr_t>(g.ptr) & (scales ? 7 : 15)) == 0 && g.page_stride % 8 == 0 &&
+           g.token_stride % 8 == 0 && g.head_stride % 8 == 0;
   };
-  const bool wide = p.cache.head_dim % 8 == 0 && rows16(p.cache.k) && rows16(p.cache.v);
-  return launch_early(wide ? kda_paged_attention_simt_kernel<true> : kda_paged_attention_simt_kernel<false>, grid,
-                      ATTN_WARPS * 32, 0, s, p);
+  const bool wide = p.cache.head_dim % 8 == 0 && rows8(p.cache.k) && rows8(p.cache.v);
+  const int threads = ATTN_WARPS * 32;
+  if (scales != nullptr)
+    return launch_early(wide ? kda_paged_attention_simt_kernel<true, true> : kda_paged_attention_simt_kernel<false, true>,
+                        grid, threads, 0, s, p, *scales);
+  return launch_early(wide ? kda_paged_attention_simt_kernel<true, false> : kda_paged_attention_simt_kernel<false, false>,
+                      grid, threads, 0, s, p, kda_paged_scales{});
 }
 
 }  // namespace kda

@@ -2,7 +2,7 @@
 #pragma once
 
 #include "kda_device.cuh"
-#include "kda_paged.h"
+#include "kda_paged_fp8.h"
 
 namespace kda {
 
@@ -20,9 +20,10 @@ struct AttnRequest {
   unsigned bad;  // KDA_ERR_* bits
 };
 
-__device__ __forceinline__ AttnRequest attn_request(const kda_attention_params& p, int r) {
-  AttnRequest q{p.cu_new[r], 0, p.kv_len[r], 0u};
-  const int end = p.cu_new[r + 1];
+template <typename Params>  // kda_attention_params, or others with the same names
+__device__ __forceinline__ AttnRequest paged_request(const Params& p, const int32_t* cu, int r) {
+  AttnRequest q{cu[r], 0, p.kv_len[r], 0u};
+  const int end = cu[r + 1];
   if (q.row0 < 0 || end < q.row0 || end > p.num_tokens)
     q.bad |= KDA_ERR_SEQLENS;
   else
@@ -32,6 +33,15 @@ __device__ __forceinline__ AttnRequest attn_request(const kda_attention_params& 
     q.kv = 0;
   }
   return q;
+}
+
+__device__ __forceinline__ AttnRequest attn_request(const kda_attention_params& p, int r) {
+  return paged_request(p, p.cu_new, r);
+}
+
+// The scale of token `place` of a page in a cache in 8 bits.
+__device__ __forceinline__ float block_scale(const kda_page_scales& s, int64_t page, int place, int head) {
+  return s.ptr[page * s.page_stride + (int64_t)(place / KDA_FP8_SCALE_TOKENS) * s.block_stride + head * s.head_stride];
 }
 
 // The first key a row at position pos sees (window 0: all before it).

@@ -1,4 +1,4 @@
-// kda_paged_api.cu - the C ABI of include/kda_paged.h: host-side argument
+// kda_paged_api.cu - the C ABI of include/kda_paged.h and kda_paged_fp8.h: host-side argument
 // validation, the choice of kernel and dispatch.
 #include <cuda_runtime.h>
 #include <math.h>
@@ -7,7 +7,7 @@
 #include <numeric>
 
 #include "kda_error.h"
-#include "kda_paged.h"
+#include "kda_paged_fp8.h"
 #include "kda_paged_launch.h"
 
 namespace {
@@ -34,10 +34,19 @@ Extent rows_extent(const void* p, int64_t n, int64_t b_stride, int64_t heads, in
   return n < 1 ? Extent() : bytes_extent(p, (size_t)((n - 1) * b_stride + (heads - 1) * h_stride + dim) * 2);
 }
 
-Extent pages_extent(const kda_pages& g, const kda_paged_cache& c) {
+// elem: bytes an element, 2 (bf16) or 1 (codes)
+Extent pages_extent(const kda_pages& g, const kda_paged_cache& c, int elem = 2) {
   if (c.num_pages < 1) return Extent();
   return bytes_extent(g.ptr, (size_t)((int64_t)(c.num_pages - 1) * g.page_stride + (int64_t)(c.page_size - 1) * g.token_stride +
-                                      (int64_t)(c.num_heads - 1) * g.head_stride + c.head_dim) * 2);
+                                      (int64_t)(c.num_heads - 1) * g.head_stride + c.head_dim) * elem);
+}
+
+int64_t page_blocks(const kda_paged_cache& c) { return (c.page_size - 1) / KDA_FP8_SCALE_TOKENS + 1; }
+
+Extent scales_extent(const kda_page_scales& f, const kda_paged_cache& c) {
+  if (c.num_pages < 1) return Extent();
+  return bytes_extent(f.ptr, (size_t)((int64_t)(c.num_pages - 1) * f.page_stride + (page_blocks(c) - 1) * f.block_stride +
+                                      (int64_t)(c.num_heads - 1) * f.head_stride + 1) * 4);
 }
 
 bool overlaps(const Extent& a, const Extent& b) {
@@ -93,10 +102,10 @@ kda_status check_rows(const char* name, const void* p, int64_t n, int64_t b_stri
   return KDA_OK;
 }
 
-kda_status check_pages(const char* name, const kda_pages& g, const kda_paged_cache& c) {
+kda_status check_pages(const char* name, const kda_pages& g, const kda_paged_cache& c, int elem) {
   if (c.num_pages == 0) return KDA_OK;
   if (g.ptr == nullptr) return fail(KDA_EINVAL, "%s.ptr is NULL with num_pages = %d", name, c.num_pages);
-  if (!aligned(g.ptr, 2)) return fail(KDA_EINVAL, "%s.ptr is not 2-byte aligned", name);
+  if (!aligned(g.ptr, elem)) return fail(KDA_EINVAL, "%s.ptr is not 2-byte aligned", name);
   if (g.page_stride < 0 || g.token_stride < 0 || g.head_stride < 0)
     return fail(KDA_EINVAL, "%s has a negative stride", name);
   if (g.page_stride >> 31 || g.token_stride >> 31 || g.head_stride >> 31)
@@ -104,7 +113,7 @@ kda_status check_pages(const char* name, const kda_pages& g, const kda_paged_cac
   return KDA_OK;
 }
 
-kda_status check_cache(const kda_paged_cache& c) {
+kda_status check_cache(const kda_paged_cache& c, int elem = 2) {
   if (c.num_pages < 0) return fail(KDA_EINVAL, "cache.num_pages = %d is negative", c.num_pages);
   if (c.page_size < 1) return fail(KDA_EINVAL, "cache.page_size = %d is below 1", c.page_size);
   if (c.num_heads < 1) return fail(KDA_EINVAL, "cache.num_heads = %d is below 1", c.num_heads);
@@ -113,8 +122,26 @@ kda_status check_cache(const kda_paged_cache& c) {
   if ((long long)c.num_pages * c.page_size > 0x7fffffffLL)
     return fail(KDA_EUNSUPPORTED, "num_pages * page_size = %lld tokens, 2^31 or more",
                 (long long)c.num_pages * c.page_size);
-  kda_status s = check_pages("cache.k", c.k, c);
-  return s != KDA_OK ? s : check_pages("cache.v", c.v, c);
+  kda_status s = check_pages("cache.k", c.k, c, elem);
+  return s != KDA_OK ? s : check_pages("cache.v", c.v, c, elem);
+}
+
+kda_status check_scales(const kda_paged_scales* sc, const kda_paged_cache& c) {
+  if (sc == nullptr) return fail(KDA_EINVAL, "scales is NULL");
+  if (c.num_pages == 0) return KDA_OK;
+  const struct {
+    const char* name;
+    const kda_page_scales* f;
+  } sides[] = {{"scales.k", &sc->k}, {"scales.v", &sc->v}};
+  for (const auto& x : sides) {
+    if (x.f->ptr == nullptr) return fail(KDA_EINVAL, "%s.ptr is NULL with num_pages = %d", x.name, c.num_pages);
+    if (!aligned(x.f->ptr, 4)) return fail(KDA_EINVAL, "%s.ptr is not 4-byte aligned", x.name);
+    if (x.f->page_stride < 0 || x.f->block_stride < 0 || x.f->head_stride < 0)
+      return fail(KDA_EINVAL, "%s has a negative stride", x.name);
+    if (x.f->page_stride >> 31 || x.f->block_stride >> 31 || x.f->head_stride >> 31)
+      return fail(KDA_EUNSUPPORTED, "%s has a stride of 2^31 elements or more", x.name);
+  }
+  return KDA_OK;
 }
 
 kda_status check_table(const int32_t* table, int64_t stride, int32_t width, int32_t page_size, int32_t requests) {
@@ -148,8 +175,142 @@ int attention_ctas() {
   return sms < most ? sms : most;
 }
 
-bool wide_pages(const kda_pages& g) {
-  return aligned(g.ptr, 16) && g.page_stride % 8 == 0 && g.token_stride % 8 == 0 && g.head_stride % 8 == 0;
+// Rows of pages on `bytes` bytes, of `elems` elements.
+bool wide_pages(const kda_pages& g, uintptr_t bytes, int elems) {
+  return aligned(g.ptr, bytes) && g.page_stride % elems == 0 && g.token_stride % elems == 0 && g.head_stride % elems == 0;
+}
+
+// kda_rope_append, or with scales kda_rope_append_fp8.
+kda_status rope_append(const char* call, const kda_rope_params* p, bool fp8, const kda_paged_scales* sc, void* stream) {
+  if (p == nullptr) return fail(KDA_EINVAL, "params is NULL");
+  const int elem = fp8 ? 1 : 2;
+  kda_status s = check_cache(p->cache, elem);
+  if (s != KDA_OK) return s;
+  if (fp8 && (s = check_scales(sc, p->cache)) != KDA_OK) return s;
+  const int D = p->cache.head_dim, Hkv = p->cache.num_heads;
+  if (p->num_tokens < 0) return fail(KDA_EINVAL, "num_tokens = %d is negative", p->num_tokens);
+  if (p->num_q_heads < 1) return fail(KDA_EINVAL, "num_q_heads = %d is below 1", p->num_q_heads);
+  if (p->num_q_heads > 16384) return fail(KDA_EUNSUPPORTED, "num_q_heads = %d is above 16384", p->num_q_heads);
+  if (p->rotary_dim < 0 || p->rotary_dim > D || p->rotary_dim % 2)
+    return fail(KDA_EINVAL, "rotary_dim = %d is not an even number in 0..%d", p->rotary_dim, D);
+  if (!isfinite(p->mscale)) return fail(KDA_EINVAL, "mscale is not finite");
+  if (p->num_tokens == 0) return ok();
+  if ((s = check_rows("q", p->q.ptr, p->num_tokens, p->q.b_stride, p->q.h_stride)) != KDA_OK) return s;
+  if ((s = check_rows("k", p->k.ptr, p->num_tokens, p->k.b_stride, p->k.h_stride)) != KDA_OK) return s;
+  if ((s = check_rows("v", p->v.ptr, p->num_tokens, p->v.b_stride, p->v.h_stride)) != KDA_OK) return s;
+  if ((s = check_rows("q_out", p->q_out, p->num_tokens, p->q_out_b_stride, p->q_out_h_stride)) != KDA_OK) return s;
+  if ((s = check_words("positions", p->positions, true)) != KDA_OK) return s;
+  if ((s = check_words("slots", p->slots, true)) != KDA_OK) return s;
+  if ((s = check_words("error_word", p->error_word, false)) != KDA_OK) return s;
+  if (p->rotary_dim > 0 && (p->freqs == nullptr || !aligned(p->freqs, 8)))
+    return fail(KDA_EINVAL, "freqs is NULL or not 8-byte aligned");
+  const int64_t T = p->num_tokens;
+  const Rows q = rows_of(p->q.ptr, T, p->q.b_stride, p->num_q_heads, p->q.h_stride, D);
+  const Rows k = rows_of(p->k.ptr, T, p->k.b_stride, Hkv, p->k.h_stride, D);
+  const Rows v = rows_of(p->v.ptr, T, p->v.b_stride, Hkv, p->v.h_stride, D);
+  const Rows o = rows_of(p->q_out, T, p->q_out_b_stride, p->num_q_heads, p->q_out_h_stride, D);
+  const Extent ck = pages_extent(p->cache.k, p->cache, elem), cv = pages_extent(p->cache.v, p->cache, elem);
+  const Extent fk = fp8 ? scales_extent(sc->k, p->cache) : Extent(), fv = fp8 ? scales_extent(sc->v, p->cache) : Extent();
+  const bool in_place = p->q_out == p->q.ptr;
+  if (in_place && ((p->q_out_b_stride != p->q.b_stride && T > 1) ||
+                   (p->q_out_h_stride != p->q.h_stride && p->num_q_heads > 1)))
+    return fail(KDA_EINVAL, "q_out is q with other strides");
+  if (!in_place && (overlaps(o, q) || overlaps(o, k) || overlaps(o, v)))
+    return fail(KDA_EINVAL, "q_out overlaps q, k or v");
+  for (const Extent& c : {ck, cv})
+    if (overlaps(c, q.e) || overlaps(c, k.e) || overlaps(c, v.e) || overlaps(c, o.e))
+      return fail(KDA_EINVAL, "the cache overlaps q, k, v or q_out");
+  for (const Extent& f : {fk, fv})
+    if (overlaps(f, q.e) || overlaps(f, k.e) || overlaps(f, v.e) || overlaps(f, o.e))
+      return fail(KDA_EINVAL, "the scales overlap q, k, v or q_out");
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool q_wide = D % 16 == 0 && p->rotary_dim % 16 == 0 && wide_rows(p->q.ptr, p->q.b_stride, p->q.h_stride) &&
+                      wide_rows(p->q_out, p->q_out_b_stride, p->q_out_h_stride);
+  cudaError_t e;
+  if (fp8) {
+    // key and value rows of 32 runs of `run` elements: the runs aligned, each pair's halves (or the pair) a run's own
+    const int run = D / 32;
+    auto rows = [&](const kda_view& x) { return aligned(x.ptr, 2 * run) && x.b_stride % run == 0 && x.h_stride % run == 0; };
+    const bool runs = (D == 64 || D == 128) && p->rotary_dim % (2 * run) == 0 && rows(p->k) && rows(p->v) &&
+                      (p->cache.num_pages == 0 || (wide_pages(p->cache.k, run, run) && wide_pages(p->cache.v, run, run)));
+    e = kda::launch_rope_append_fp8(*p, *sc, q_wide, runs ? run : 0, st);
+  } else {
+    const bool wide = q_wide && wide_rows(p->k.ptr, p->k.b_stride, p->k.h_stride) &&
+                      wide_rows(p->v.ptr, p->v.b_stride, p->v.h_stride) &&
+                      (p->cache.num_pages == 0 || (wide_pages(p->cache.k, 16, 8) && wide_pages(p->cache.v, 16, 8)));
+    e = kda::launch_rope_append(*p, wide, st);
+  }
+  if (e != cudaSuccess) return fail(KDA_ELAUNCH, "%s launch: %s", call, cudaGetErrorString(e));
+  return ok();
+}
+
+// kda_paged_attention, or with scales kda_paged_attention_fp8.
+kda_status paged_attention(const char* call, const kda_attention_params* p, bool fp8, const kda_paged_scales* sc,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  if (p == nullptr) return fail(KDA_EINVAL, "params is NULL");
+  kda_status s = check_requests(p->num_requests);
+  if (s != KDA_OK) return s;
+  const int elem = fp8 ? 1 : 2;
+  if ((s = check_cache(p->cache, elem)) != KDA_OK) return s;
+  if (fp8 && (s = check_scales(sc, p->cache)) != KDA_OK) return s;
+  const int D = p->cache.head_dim, Hkv = p->cache.num_heads;
+  if (p->num_tokens < 0) return fail(KDA_EINVAL, "num_tokens = %d is negative", p->num_tokens);
+  if (p->num_q_heads < 1 || p->num_q_heads % Hkv)
+    return fail(KDA_EINVAL, "num_q_heads = %d is not a multiple of cache.num_heads = %d", p->num_q_heads, Hkv);
+  if (p->num_q_heads / Hkv > 128)
+    return fail(KDA_EUNSUPPORTED, "%d query heads share a key-value head, more than 128", p->num_q_heads / Hkv);
+  if ((long long)p->num_tokens * p->num_q_heads > 0x7fffffffLL)
+    return fail(KDA_EUNSUPPORTED, "num_tokens * num_q_heads = %lld, 2^31 or more",
+                (long long)p->num_tokens * p->num_q_heads);
+  if (p->window < 0) return fail(KDA_EINVAL, "window = %d is negative", p->window);
+  if (!isfinite(p->scale) || !(p->scale > 0.f)) return fail(KDA_EINVAL, "scale is not a finite number above 0");
+  if (p->num_requests == 0 || p->num_tokens == 0) return ok();
+  if ((s = check_table(p->table, p->table_stride, p->table_width, p->cache.page_size, p->num_requests)) != KDA_OK) return s;
+  if ((s = check_rows("q", p->q.ptr, p->num_tokens, p->q.b_stride, p->q.h_stride)) != KDA_OK) return s;
+  if ((s = check_rows("out", p->out, p->num_tokens, p->out_b_stride, p->out_h_stride)) != KDA_OK) return s;
+  if ((s = check_words("cu_new", p->cu_new, true)) != KDA_OK) return s;
+  if ((s = check_words("kv_len", p->kv_len, true)) != KDA_OK) return s;
+  if ((s = check_words("lse", p->lse, false)) != KDA_OK) return s;
+  if ((s = check_words("error_word", p->error_word, false)) != KDA_OK) return s;
+  const size_t rows = (size_t)p->num_tokens * p->num_q_heads, R = (size_t)p->num_requests;
+  const Rows q = rows_of(p->q.ptr, p->num_tokens, p->q.b_stride, p->num_q_heads, p->q.h_stride, D);
+  const Rows out = rows_of(p->out, p->num_tokens, p->out_b_stride, p->num_q_heads, p->out_h_stride, D);
+  const Extent& o = out.e;
+  const Extent l = bytes_extent(p->lse, p->lse ? rows * 4 : 0);
+  const struct {
+    const char* name;
+    Extent e;
+  } inputs[] = {{"q", q.e},
+                {"cache.k", pages_extent(p->cache.k, p->cache, elem)},
+                {"cache.v", pages_extent(p->cache.v, p->cache, elem)},
+                {"scales.k", fp8 ? scales_extent(sc->k, p->cache) : Extent()},
+                {"scales.v", fp8 ? scales_extent(sc->v, p->cache) : Extent()},
+                {"table", bytes_extent(p->table, (size_t)((R - 1) * p->table_stride + p->table_width) * 4)},
+                {"cu_new", bytes_extent(p->cu_new, (R + 1) * 4)},
+                {"kv_len", bytes_extent(p->kv_len, R * 4)}};
+  if (overlaps(out, q)) return fail(KDA_EINVAL, "out overlaps q");
+  for (const auto& in : inputs) {
+    if (&in != inputs && overlaps(o, in.e)) return fail(KDA_EINVAL, "out overlaps %s", in.name);
+    if (overlaps(l, in.e)) return fail(KDA_EINVAL, "lse overlaps %s", in.name);
+  }
+  if (overlaps(o, l)) return fail(KDA_EINVAL, "out overlaps lse");
+  const size_t need = kda_paged_attention_workspace_bytes(D);
+  if (need == 0) return fail(KDA_ELAUNCH, "%s: no current device", call);
+  if (workspace == nullptr || !aligned(workspace, 16)) return fail(KDA_EINVAL, "workspace is NULL or not 16-byte aligned");
+  if (workspace_bytes < need)
+    return fail(KDA_EINVAL, "workspace_bytes = %zu is below the %zu this call needs (kda_paged_attention_workspace_bytes)",
+                workspace_bytes, need);
+  const Extent w = bytes_extent(workspace, need);
+  for (const auto& in : inputs)
+    if (overlaps(w, in.e)) return fail(KDA_EINVAL, "workspace overlaps %s", in.name);
+  if (overlaps(w, o) || overlaps(w, l)) return fail(KDA_EINVAL, "workspace overlaps out or lse");
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaErrorNotSupported;
+  if (!fp8 && kda::paged_attention_on_tensor_cores(p->cache))
+    e = kda::launch_paged_attention_tc(*p, workspace, attention_ctas(), st);
+  if (e == cudaErrorNotSupported) e = kda::launch_paged_attention_simt(*p, fp8 ? sc : nullptr, st);
+  if (e != cudaSuccess) return fail(KDA_ELAUNCH, "%s launch: %s", call, cudaGetErrorString(e));
+  return ok();
 }
 
 }  // namespace
@@ -209,52 +370,6 @@ kda_status kda_paged_plan(const kda_plan_params* p, void* stream) {
   return ok();
 }
 
-kda_status kda_rope_append(const kda_rope_params* p, void* stream) {
-  if (p == nullptr) return fail(KDA_EINVAL, "params is NULL");
-  kda_status s = check_cache(p->cache);
-  if (s != KDA_OK) return s;
-  const int D = p->cache.head_dim, Hkv = p->cache.num_heads;
-  if (p->num_tokens < 0) return fail(KDA_EINVAL, "num_tokens = %d is negative", p->num_tokens);
-  if (p->num_q_heads < 1) return fail(KDA_EINVAL, "num_q_heads = %d is below 1", p->num_q_heads);
-  if (p->num_q_heads > 16384) return fail(KDA_EUNSUPPORTED, "num_q_heads = %d is above 16384", p->num_q_heads);
-  if (p->rotary_dim < 0 || p->rotary_dim > D || p->rotary_dim % 2)
-    return fail(KDA_EINVAL, "rotary_dim = %d is not an even number in 0..%d", p->rotary_dim, D);
-  if (!isfinite(p->mscale)) return fail(KDA_EINVAL, "mscale is not finite");
-  if (p->num_tokens == 0) return ok();
-  if ((s = check_rows("q", p->q.ptr, p->num_tokens, p->q.b_stride, p->q.h_stride)) != KDA_OK) return s;
-  if ((s = check_rows("k", p->k.ptr, p->num_tokens, p->k.b_stride, p->k.h_stride)) != KDA_OK) return s;
-  if ((s = check_rows("v", p->v.ptr, p->num_tokens, p->v.b_stride, p->v.h_stride)) != KDA_OK) return s;
-  if ((s = check_rows("q_out", p->q_out, p->num_tokens, p->q_out_b_stride, p->q_out_h_stride)) != KDA_OK) return s;
-  if ((s = check_words("positions", p->positions, true)) != KDA_OK) return s;
-  if ((s = check_words("slots", p->slots, true)) != KDA_OK) return s;
-  if ((s = check_words("error_word", p->error_word, false)) != KDA_OK) return s;
-  if (p->rotary_dim > 0 && (p->freqs == nullptr || !aligned(p->freqs, 8)))
-    return fail(KDA_EINVAL, "freqs is NULL or not 8-byte aligned");
-  const int64_t T = p->num_tokens;
-  const Rows q = rows_of(p->q.ptr, T, p->q.b_stride, p->num_q_heads, p->q.h_stride, D);
-  const Rows k = rows_of(p->k.ptr, T, p->k.b_stride, Hkv, p->k.h_stride, D);
-  const Rows v = rows_of(p->v.ptr, T, p->v.b_stride, Hkv, p->v.h_stride, D);
-  const Rows o = rows_of(p->q_out, T, p->q_out_b_stride, p->num_q_heads, p->q_out_h_stride, D);
-  const Extent ck = pages_extent(p->cache.k, p->cache), cv = pages_extent(p->cache.v, p->cache);
-  const bool in_place = p->q_out == p->q.ptr;
-  if (in_place && ((p->q_out_b_stride != p->q.b_stride && T > 1) ||
-                   (p->q_out_h_stride != p->q.h_stride && p->num_q_heads > 1)))
-    return fail(KDA_EINVAL, "q_out is q with other strides");
-  if (!in_place && (overlaps(o, q) || overlaps(o, k) || overlaps(o, v)))
-    return fail(KDA_EINVAL, "q_out overlaps q, k or v");
-  for (const Extent& c : {ck, cv})
-    if (overlaps(c, q.e) || overlaps(c, k.e) || overlaps(c, v.e) || overlaps(c, o.e))
-      return fail(KDA_EINVAL, "the cache overlaps q, k, v or q_out");
-  const bool wide = D % 16 == 0 && p->rotary_dim % 16 == 0 && wide_rows(p->q.ptr, p->q.b_stride, p->q.h_stride) &&
-                    wide_rows(p->k.ptr, p->k.b_stride, p->k.h_stride) &&
-                    wide_rows(p->v.ptr, p->v.b_stride, p->v.h_stride) &&
-                    wide_rows(p->q_out, p->q_out_b_stride, p->q_out_h_stride) &&
-                    (p->cache.num_pages == 0 || (wide_pages(p->cache.k) && wide_pages(p->cache.v)));
-  const cudaError_t e = kda::launch_rope_append(*p, wide, static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return fail(KDA_ELAUNCH, "kda_rope_append launch: %s", cudaGetErrorString(e));
-  return ok();
-}
-
 kda_status kda_rope_freqs(uint64_t* freqs, int32_t rotary_dim, double base, int32_t scaling, double factor,
                           double original_len, double low, double high) {
   if (freqs == nullptr) return fail(KDA_EINVAL, "freqs is NULL");
@@ -293,65 +408,61 @@ size_t kda_paged_attention_workspace_bytes(int32_t head_dim) {
   return KDA_ATTENTION_WORKSPACE_ZEROED + parts;
 }
 
+kda_status kda_rope_append(const kda_rope_params* p, void* stream) {
+  return rope_append("kda_rope_append", p, false, nullptr, stream);
+}
+
+kda_status kda_rope_append_fp8(const kda_rope_params* p, const kda_paged_scales* s, void* stream) {
+  return rope_append("kda_rope_append_fp8", p, true, s, stream);
+}
+
 kda_status kda_paged_attention(const kda_attention_params* p, void* workspace, size_t workspace_bytes, void* stream) {
+  return paged_attention("kda_paged_attention", p, false, nullptr, workspace, workspace_bytes, stream);
+}
+
+kda_status kda_paged_attention_fp8(const kda_attention_params* p, const kda_paged_scales* s, void* workspace,
+                                   size_t workspace_bytes, void* stream) {
+  return paged_attention("kda_paged_attention_fp8", p, true, s, workspace, workspace_bytes, stream);
+}
+
+kda_status kda_paged_read_fp8(const kda_read_params* p, const kda_paged_scales* sc, void* stream) {
   if (p == nullptr) return fail(KDA_EINVAL, "params is NULL");
   kda_status s = check_requests(p->num_requests);
   if (s != KDA_OK) return s;
-  if ((s = check_cache(p->cache)) != KDA_OK) return s;
-  const int D = p->cache.head_dim, Hkv = p->cache.num_heads;
+  if ((s = check_cache(p->cache, 1)) != KDA_OK) return s;
+  if ((s = check_scales(sc, p->cache)) != KDA_OK) return s;
   if (p->num_tokens < 0) return fail(KDA_EINVAL, "num_tokens = %d is negative", p->num_tokens);
-  if (p->num_q_heads < 1 || p->num_q_heads % Hkv)
-    return fail(KDA_EINVAL, "num_q_heads = %d is not a multiple of cache.num_heads = %d", p->num_q_heads, Hkv);
-  if (p->num_q_heads / Hkv > 128)
-    return fail(KDA_EUNSUPPORTED, "%d query heads share a key-value head, more than 128", p->num_q_heads / Hkv);
-  if ((long long)p->num_tokens * p->num_q_heads > 0x7fffffffLL)
-    return fail(KDA_EUNSUPPORTED, "num_tokens * num_q_heads = %lld, 2^31 or more",
-                (long long)p->num_tokens * p->num_q_heads);
-  if (p->window < 0) return fail(KDA_EINVAL, "window = %d is negative", p->window);
-  if (!isfinite(p->scale) || !(p->scale > 0.f)) return fail(KDA_EINVAL, "scale is not a finite number above 0");
   if (p->num_requests == 0 || p->num_tokens == 0) return ok();
   if ((s = check_table(p->table, p->table_stride, p->table_width, p->cache.page_size, p->num_requests)) != KDA_OK) return s;
-  if ((s = check_rows("q", p->q.ptr, p->num_tokens, p->q.b_stride, p->q.h_stride)) != KDA_OK) return s;
-  if ((s = check_rows("out", p->out, p->num_tokens, p->out_b_stride, p->out_h_stride)) != KDA_OK) return s;
-  if ((s = check_words("cu_new", p->cu_new, true)) != KDA_OK) return s;
+  if ((s = check_rows("k_out", p->k_out, p->num_tokens, p->k_out_b_stride, p->k_out_h_stride)) != KDA_OK) return s;
+  if ((s = check_rows("v_out", p->v_out, p->num_tokens, p->v_out_b_stride, p->v_out_h_stride)) != KDA_OK) return s;
+  if ((s = check_words("cu_rows", p->cu_rows, true)) != KDA_OK) return s;
   if ((s = check_words("kv_len", p->kv_len, true)) != KDA_OK) return s;
-  if ((s = check_words("lse", p->lse, false)) != KDA_OK) return s;
   if ((s = check_words("error_word", p->error_word, false)) != KDA_OK) return s;
-  const size_t rows = (size_t)p->num_tokens * p->num_q_heads, R = (size_t)p->num_requests;
-  const Rows q = rows_of(p->q.ptr, p->num_tokens, p->q.b_stride, p->num_q_heads, p->q.h_stride, D);
-  const Rows out = rows_of(p->out, p->num_tokens, p->out_b_stride, p->num_q_heads, p->out_h_stride, D);
-  const Extent& o = out.e;
-  const Extent l = bytes_extent(p->lse, p->lse ? rows * 4 : 0);
+  const int D = p->cache.head_dim, Hkv = p->cache.num_heads;
+  const size_t R = (size_t)p->num_requests;
+  const Rows k = rows_of(p->k_out, p->num_tokens, p->k_out_b_stride, Hkv, p->k_out_h_stride, D);
+  const Rows v = rows_of(p->v_out, p->num_tokens, p->v_out_b_stride, Hkv, p->v_out_h_stride, D);
   const struct {
     const char* name;
     Extent e;
-  } inputs[] = {{"q", q.e},
-                {"cache.k", pages_extent(p->cache.k, p->cache)},
-                {"cache.v", pages_extent(p->cache.v, p->cache)},
+  } inputs[] = {{"cache.k", pages_extent(p->cache.k, p->cache, 1)},
+                {"cache.v", pages_extent(p->cache.v, p->cache, 1)},
+                {"scales.k", scales_extent(sc->k, p->cache)},
+                {"scales.v", scales_extent(sc->v, p->cache)},
                 {"table", bytes_extent(p->table, (size_t)((R - 1) * p->table_stride + p->table_width) * 4)},
-                {"cu_new", bytes_extent(p->cu_new, (R + 1) * 4)},
+                {"cu_rows", bytes_extent(p->cu_rows, (R + 1) * 4)},
                 {"kv_len", bytes_extent(p->kv_len, R * 4)}};
-  if (overlaps(out, q)) return fail(KDA_EINVAL, "out overlaps q");
+  if (overlaps(k, v)) return fail(KDA_EINVAL, "k_out overlaps v_out");
   for (const auto& in : inputs) {
-    if (&in != inputs && overlaps(o, in.e)) return fail(KDA_EINVAL, "out overlaps %s", in.name);
-    if (overlaps(l, in.e)) return fail(KDA_EINVAL, "lse overlaps %s", in.name);
+    if (overlaps(k.e, in.e)) return fail(KDA_EINVAL, "k_out overlaps %s", in.name);
+    if (overlaps(v.e, in.e)) return fail(KDA_EINVAL, "v_out overlaps %s", in.name);
   }
-  if (overlaps(o, l)) return fail(KDA_EINVAL, "out overlaps lse");
-  const size_t need = kda_paged_attention_workspace_bytes(D);
-  if (need == 0) return fail(KDA_ELAUNCH, "kda_paged_attention: no current device");
-  if (workspace == nullptr || !aligned(workspace, 16)) return fail(KDA_EINVAL, "workspace is NULL or not 16-byte aligned");
-  if (workspace_bytes < need)
-    return fail(KDA_EINVAL, "workspace_bytes = %zu is below the %zu this call needs (kda_paged_attention_workspace_bytes)",
-                workspace_bytes, need);
-  const Extent w = bytes_extent(workspace, need);
-  for (const auto& in : inputs)
-    if (overlaps(w, in.e)) return fail(KDA_EINVAL, "workspace overlaps %s", in.name);
-  if (overlaps(w, o) || overlaps(w, l)) return fail(KDA_EINVAL, "workspace overlaps out or lse");
-  const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = cudaErrorNotSupported;
-  if (kda::paged_attention_on_tensor_cores(p->cache)) e = kda::launch_paged_attention_tc(*p, workspace, attention_ctas(), st);
-  if (e == cudaErrorNotSupported) e = kda::launch_paged_attention_simt(*p, st);
-  if (e != cudaSuccess) return fail(KDA_ELAUNCH, "kda_paged_attention launch: %s", cudaGetErrorString(e));
+  const bool wide = D % 16 == 0 && wide_rows(p->k_out, p->k_out_b_stride, p->k_out_h_stride) &&
+                    wide_rows(p->v_out, p->v_out_b_stride, p->v_out_h_stride) &&
+                    (p->cache.num_pages == 0 || (wide_pages(p->cache.k, 16, 16) && wide_pages(p->cache.v, 16, 16)));
+  const cudaError_t e = kda::launch_paged_read_fp8(*p, *sc, wide, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(KDA_ELAUNCH, "kda_paged_read_fp8 launch: %s", cudaGetErrorString(e));
   return ok();
 }
 

@@ -2,7 +2,7 @@
 #pragma once
 
 #include "kda_launch.h"
-#include "kda_paged.h"
+#include "kda_paged_fp8.h"
 
 namespace kda {
 
@@ -11,8 +11,16 @@ cudaError_t launch_paged_plan(const kda_plan_params& p, cudaStream_t s);
 // wide: 16-byte accesses (every row 16-byte aligned, head_dim a multiple of 16, the turned part in whole runs of 8 pairs).
 cudaError_t launch_rope_append(const kda_rope_params& p, bool wide, cudaStream_t s);
 
-// A block of eight warps per (row, query head) on the CUDA cores: any cache.
-cudaError_t launch_paged_attention_simt(const kda_attention_params& p, cudaStream_t s);
+// A block of eight warps per (row, query head) on the CUDA cores: any cache, in 8 bits where there are scales.
+cudaError_t launch_paged_attention_simt(const kda_attention_params& p, const kda_paged_scales* scales, cudaStream_t s);
+
+// q_wide: as `wide` above, for q and q_out. lane_elems: key and value elements that a lane takes of a row at a time, 4
+// (head_dim 128) or 2 (64) where all rows allow it, 0 for any others.
+cudaError_t launch_rope_append_fp8(const kda_rope_params& p, const kda_paged_scales& sc, bool q_wide, int lane_elems,
+                                   cudaStream_t s);
+
+// wide: 16 codes at a time (head_dim a multiple of 16, every row on 16 bytes).
+cudaError_t launch_paged_read_fp8(const kda_read_params& p, const kda_paged_scales& sc, bool wide, cudaStream_t s);
 
 // One side of a paged cache as a tensor map for copies of 64 columns of `box` tokens (kda_tmap.cu).
 cudaError_t pages_tensor_map(const kda_pages& g, const kda_paged_cache& c, int box, CUtensorMap* out);

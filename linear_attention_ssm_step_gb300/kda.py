@@ -1,4 +1,5 @@
-"""Thin ctypes binding of libkda_gb300.so (include/kda.h, kda_fp8.h, kda_prefill.h, kda_paged.h).
+"""Thin ctypes binding of libkda_gb300.so (include/kda.h, kda_fp8.h, kda_prefill.h, kda_paged.h,
+kda_paged_fp8.h).
 
 Argument marshalling only: torch tensors supply device pointers, strides and
 the current CUDA stream; every step of the computation runs in the library's
@@ -23,6 +24,7 @@ KDA_ERR_PAGES = 16
 KDA_ERR_LENGTHS = 32
 KDA_MAX_REQUESTS = 4096
 KDA_ATTENTION_WORKSPACE_ZEROED = 4096
+KDA_FP8_SCALE_TOKENS = 16
 KDA_ROPE_PLAIN, KDA_ROPE_LINEAR, KDA_ROPE_BASE, KDA_ROPE_PARTS = 0, 1, 2, 3
 KDA_MAX_T = 16
 KDA_GATE_RAW, KDA_GATE_PRECOMPUTED = 0, 1
@@ -134,6 +136,32 @@ class KdaAttentionParams(ctypes.Structure):
     ]
 
 
+class KdaPageScales(ctypes.Structure):
+    """kda_page_scales of include/kda_paged_fp8.h."""
+
+    _fields_ = [("ptr", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("block_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class KdaPagedScales(ctypes.Structure):
+    """kda_paged_scales of include/kda_paged_fp8.h."""
+
+    _fields_ = [("k", KdaPageScales), ("v", KdaPageScales)]
+
+
+class KdaReadParams(ctypes.Structure):
+    """kda_read_params of include/kda_paged_fp8.h."""
+
+    _fields_ = [
+        ("num_requests", ctypes.c_int32), ("num_tokens", ctypes.c_int32),
+        ("k_out", ctypes.c_void_p), ("k_out_b_stride", ctypes.c_int64), ("k_out_h_stride", ctypes.c_int64),
+        ("v_out", ctypes.c_void_p), ("v_out_b_stride", ctypes.c_int64), ("v_out_h_stride", ctypes.c_int64),
+        ("cu_rows", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+        ("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("table_width", ctypes.c_int32),
+        ("cache", KdaPagedCache), ("error_word", ctypes.c_void_p),
+    ]
+
+
 EXPORTS = {
     "kda_decode": ([ctypes.POINTER(KdaParams), ctypes.c_void_p], ctypes.c_int),
     "kda_decode_fp8": ([ctypes.POINTER(KdaParams), ctypes.POINTER(KdaFp8Pool), ctypes.c_void_p], ctypes.c_int),
@@ -163,6 +191,12 @@ EXPORTS = {
     "kda_paged_attention": ([ctypes.POINTER(KdaAttentionParams), ctypes.c_void_p, ctypes.c_size_t,
                              ctypes.c_void_p], ctypes.c_int),
     "kda_paged_attention_workspace_bytes": ([ctypes.c_int32], ctypes.c_size_t),
+    "kda_rope_append_fp8": ([ctypes.POINTER(KdaRopeParams), ctypes.POINTER(KdaPagedScales), ctypes.c_void_p],
+                            ctypes.c_int),
+    "kda_paged_attention_fp8": ([ctypes.POINTER(KdaAttentionParams), ctypes.POINTER(KdaPagedScales), ctypes.c_void_p,
+                                 ctypes.c_size_t, ctypes.c_void_p], ctypes.c_int),
+    "kda_paged_read_fp8": ([ctypes.POINTER(KdaReadParams), ctypes.POINTER(KdaPagedScales), ctypes.c_void_p],
+                           ctypes.c_int),
 }
 
 _lib = None
@@ -615,21 +649,35 @@ def _table(block_table, num_requests):
     return block_table.data_ptr(), block_table.stride(0), block_table.shape[1]
 
 
-def _paged_cache(k_cache, v_cache, num_heads=None, head_dim=None):
+def _paged_cache(k_cache, v_cache, num_heads=None, head_dim=None, dtype=torch.bfloat16):
     """KdaPagedCache of k_cache and v_cache, views [pages, page_size, heads, head_dim] with any strides."""
     c = KdaPagedCache()
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _need(t, name, torch.bfloat16)
+    kind = "codes" if dtype == torch.uint8 else "cache"
+    for name, t in (("k_" + kind, k_cache), ("v_" + kind, v_cache)):
+        _need(t, name, dtype)
         if t.dim() != 4 or (t.shape[3] > 1 and t.stride(3) != 1):
             raise ValueError(f"{name} must be [pages, page_size, heads, head_dim] with a contiguous last dim")
         if t.shape != k_cache.shape:
-            raise ValueError(f"v_cache has shape {tuple(t.shape)}, k_cache {tuple(k_cache.shape)}")
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, k_{kind} {tuple(k_cache.shape)}")
         if (num_heads is not None and t.shape[2] != num_heads) or (head_dim is not None and t.shape[3] != head_dim):
             raise ValueError(f"{name} must have heads of {head_dim}, got {tuple(t.shape)}")
     c.k = KdaPages(k_cache.data_ptr(), *k_cache.stride()[:3])
     c.v = KdaPages(v_cache.data_ptr(), *v_cache.stride()[:3])
     c.num_pages, c.page_size, c.num_heads, c.head_dim = k_cache.shape
     return c
+
+
+def _scales(k_scales, v_scales, cache):
+    """KdaPagedScales of fp32 views [pages, blocks of 16 tokens a page, heads] with any strides."""
+    blocks = -(-cache.page_size // KDA_FP8_SCALE_TOKENS)
+    want = (cache.num_pages, blocks, cache.num_heads)
+    for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
+        _need(t, name, torch.float32)
+        if tuple(t.shape) != want:
+            raise ValueError(f"{name} must be {list(want)} (pages, blocks of {KDA_FP8_SCALE_TOKENS} tokens, heads), "
+                             f"got {tuple(t.shape)}")
+    return KdaPagedScales(KdaPageScales(k_scales.data_ptr(), *k_scales.stride()),
+                          KdaPageScales(v_scales.data_ptr(), *v_scales.stride()))
 
 
 def _rows(t, name, num_tokens=None, num_heads=None, head_dim=None):
@@ -697,10 +745,18 @@ def rope_freqs(rotary_dim, base=10000.0, scaling=KDA_ROPE_PLAIN, factor=1.0, ori
 def prepare_rope_append(q, k, v, positions, slots, freqs, k_cache, v_cache, q_out=None, interleaved=False, mscale=1.0,
                         error_word=None, stream=None):
     """kda_rope_append bound to these tensors (see PreparedCall); same arguments. out is q_out."""
+    p, q_out, keep = _rope_params(q, k, v, positions, slots, freqs, k_cache, v_cache, q_out, interleaved, mscale,
+                                  error_word, stream, torch.bfloat16)
+    return PreparedCall(load_library().kda_rope_append, (ctypes.byref(p), _stream_handle(stream, q.device)), q_out,
+                        keep)
+
+
+def _rope_params(q, k, v, positions, slots, freqs, k_cache, v_cache, q_out, interleaved, mscale, error_word, stream,
+                 dtype):
     p = KdaRopeParams()
     p.q = _rows(q, "q")
     T, Hq, D = q.shape
-    p.cache = _paged_cache(k_cache, v_cache, head_dim=D)
+    p.cache = _paged_cache(k_cache, v_cache, head_dim=D, dtype=dtype)
     Hkv = p.cache.num_heads
     p.num_tokens, p.num_q_heads = T, Hq
     p.k, p.v = _rows(k, "k", T, Hkv, D), _rows(v, "v", T, Hkv, D)
@@ -715,9 +771,7 @@ def prepare_rope_append(q, k, v, positions, slots, freqs, k_cache, v_cache, q_ou
     p.freqs, p.rotary_dim = freqs.data_ptr(), 2 * freqs.shape[0]
     p.interleaved, p.mscale = int(bool(interleaved)), mscale
     p.error_word = _error_word(error_word)
-    keep = (p, q, k, v, positions, slots, freqs, k_cache, v_cache, error_word)
-    return PreparedCall(load_library().kda_rope_append, (ctypes.byref(p), _stream_handle(stream, q.device)), q_out,
-                        keep)
+    return p, q_out, (p, q, k, v, positions, slots, freqs, k_cache, v_cache, error_word)
 
 
 def kda_rope_append(q, k, v, positions, slots, freqs, k_cache, v_cache, q_out=None, interleaved=False, mscale=1.0,
@@ -751,10 +805,18 @@ def paged_attention_workspace(head_dim, device, stream=None):
 def prepare_paged_attention(q, k_cache, v_cache, block_table, cu_new, kv_len, out=None, lse=None, scale=None,
                             window=0, workspace=None, error_word=None, stream=None):
     """kda_paged_attention bound to these tensors (see PreparedCall); same arguments."""
+    p, out, workspace, keep = _attention_params(q, k_cache, v_cache, block_table, cu_new, kv_len, out, lse, scale,
+                                                window, workspace, error_word, stream, torch.bfloat16)
+    args = (ctypes.byref(p), workspace.data_ptr(), workspace.numel(), _stream_handle(stream, q.device))
+    return PreparedCall(load_library().kda_paged_attention, args, out, keep)
+
+
+def _attention_params(q, k_cache, v_cache, block_table, cu_new, kv_len, out, lse, scale, window, workspace, error_word,
+                      stream, dtype):
     p = KdaAttentionParams()
     p.q = _rows(q, "q")
     T, Hq, D = q.shape
-    p.cache = _paged_cache(k_cache, v_cache, head_dim=D)
+    p.cache = _paged_cache(k_cache, v_cache, head_dim=D, dtype=dtype)
     _need(kv_len, "kv_len", torch.int32)
     R = kv_len.numel()
     p.num_requests, p.num_tokens, p.num_q_heads, p.window = R, T, Hq, window
@@ -776,9 +838,7 @@ def prepare_paged_attention(q, k_cache, v_cache, block_table, cu_new, kv_len, ou
     _need(workspace, "workspace", torch.uint8)
     if not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous byte tensor")
-    keep = (p, q, k_cache, v_cache, block_table, cu_new, kv_len, lse, workspace, error_word)
-    args = (ctypes.byref(p), workspace.data_ptr(), workspace.numel(), _stream_handle(stream, q.device))
-    return PreparedCall(load_library().kda_paged_attention, args, out, keep)
+    return p, out, workspace, (p, q, k_cache, v_cache, block_table, cu_new, kv_len, lse, workspace, error_word)
 
 
 def kda_paged_attention(q, k_cache, v_cache, block_table, cu_new, kv_len, out=None, lse=None, scale=None, window=0,
@@ -793,3 +853,89 @@ def kda_paged_attention(q, k_cache, v_cache, block_table, cu_new, kv_len, out=No
     zeroed on the call's stream when None). Returns out bf16 [T, Hq, D]."""
     return prepare_paged_attention(q, k_cache, v_cache, block_table, cu_new, kv_len, out, lse, scale, window,
                                    workspace, error_word, stream)()
+
+
+def paged_fp8_cache(num_pages, page_size, num_heads, head_dim, device, stream=None):
+    """An empty cache in 8 bits, (k_codes, v_codes, k_scales, v_scales): uint8 [num_pages, page_size, num_heads,
+    head_dim] and fp32 [num_pages, blocks of 16 tokens, num_heads]. Nothing of it needs a first value."""
+    device = torch.device(device)
+    codes = (num_pages, page_size, num_heads, head_dim)
+    scales = (num_pages, -(-page_size // KDA_FP8_SCALE_TOKENS), num_heads)
+    return tuple(_empty(shape, dtype, device, stream)
+                 for shape, dtype in ((codes, torch.uint8), (codes, torch.uint8), (scales, torch.float32), (scales, torch.float32)))
+
+
+def prepare_rope_append_fp8(q, k, v, positions, slots, freqs, k_codes, v_codes, k_scales, v_scales, q_out=None,
+                            interleaved=False, mscale=1.0, error_word=None, stream=None):
+    """kda_rope_append_fp8 bound to these tensors (see PreparedCall); same arguments. out is q_out."""
+    p, q_out, keep = _rope_params(q, k, v, positions, slots, freqs, k_codes, v_codes, q_out, interleaved, mscale,
+                                  error_word, stream, torch.uint8)
+    sc = _scales(k_scales, v_scales, p.cache)
+    args = (ctypes.byref(p), ctypes.byref(sc), _stream_handle(stream, q.device))
+    return PreparedCall(load_library().kda_rope_append_fp8, args, q_out, keep + (sc, k_scales, v_scales))
+
+
+def kda_rope_append_fp8(q, k, v, positions, slots, freqs, k_codes, v_codes, k_scales, v_scales, q_out=None,
+                        interleaved=False, mscale=1.0, error_word=None, stream=None):
+    """Rotary positions and the append to a cache in 8 bits (include/kda_paged_fp8.h).
+    As kda_rope_append, with k_codes, v_codes: uint8 [pages, page_size, Hkv, D]
+    and k_scales, v_scales: fp32 [pages, blocks of 16 tokens, Hkv], views with
+    any strides, written at the slots and their blocks. Returns q_out."""
+    return prepare_rope_append_fp8(q, k, v, positions, slots, freqs, k_codes, v_codes, k_scales, v_scales, q_out,
+                                   interleaved, mscale, error_word, stream)()
+
+
+def prepare_paged_attention_fp8(q, k_codes, v_codes, k_scales, v_scales, block_table, cu_new, kv_len, out=None,
+                                lse=None, scale=None, window=0, workspace=None, error_word=None, stream=None):
+    """kda_paged_attention_fp8 bound to these tensors (see PreparedCall); same arguments."""
+    p, out, workspace, keep = _attention_params(q, k_codes, v_codes, block_table, cu_new, kv_len, out, lse, scale,
+                                                window, workspace, error_word, stream, torch.uint8)
+    sc = _scales(k_scales, v_scales, p.cache)
+    args = (ctypes.byref(p), ctypes.byref(sc), workspace.data_ptr(), workspace.numel(),
+            _stream_handle(stream, q.device))
+    return PreparedCall(load_library().kda_paged_attention_fp8, args, out, keep + (sc, k_scales, v_scales))
+
+
+def kda_paged_attention_fp8(q, k_codes, v_codes, k_scales, v_scales, block_table, cu_new, kv_len, out=None, lse=None,
+                            scale=None, window=0, workspace=None, error_word=None, stream=None):
+    """Attention of each request's new tokens over a paged cache in 8 bits
+    (include/kda_paged_fp8.h). As kda_paged_attention, with the cache of
+    kda_rope_append_fp8. Returns out bf16 [T, Hq, D]."""
+    return prepare_paged_attention_fp8(q, k_codes, v_codes, k_scales, v_scales, block_table, cu_new, kv_len, out, lse,
+                                       scale, window, workspace, error_word, stream)()
+
+
+PagedRead = collections.namedtuple("PagedRead", "k v")
+
+
+def prepare_paged_read_fp8(k_codes, v_codes, k_scales, v_scales, block_table, cu_rows, kv_len, num_tokens, out=None,
+                           error_word=None, stream=None):
+    """kda_paged_read_fp8 bound to these tensors (see PreparedCall); same arguments. out is its PagedRead."""
+    p = KdaReadParams()
+    p.cache = _paged_cache(k_codes, v_codes, dtype=torch.uint8)
+    sc = _scales(k_scales, v_scales, p.cache)
+    H, D = p.cache.num_heads, p.cache.head_dim
+    _need(kv_len, "kv_len", torch.int32)
+    R = kv_len.numel()
+    p.num_requests, p.num_tokens = R, num_tokens
+    if out is None:
+        out = PagedRead(*(_empty((num_tokens, H, D), torch.bfloat16, k_codes.device, stream) for _ in range(2)))
+    k, v = _rows(out.k, "out.k", num_tokens, H, D), _rows(out.v, "out.v", num_tokens, H, D)
+    p.k_out, p.k_out_b_stride, p.k_out_h_stride = k.ptr, k.b_stride, k.h_stride
+    p.v_out, p.v_out_b_stride, p.v_out_h_stride = v.ptr, v.b_stride, v.h_stride
+    p.cu_rows, p.kv_len = _ints(cu_rows, "cu_rows", (R + 1,)), _ints(kv_len, "kv_len", (R,))
+    p.table, p.table_stride, p.table_width = _table(block_table, R)
+    p.error_word = _error_word(error_word)
+    keep = (p, sc, k_codes, v_codes, k_scales, v_scales, block_table, cu_rows, kv_len, error_word)
+    args = (ctypes.byref(p), ctypes.byref(sc), _stream_handle(stream, k_codes.device))
+    return PreparedCall(load_library().kda_paged_read_fp8, args, out, keep)
+
+
+def kda_paged_read_fp8(k_codes, v_codes, k_scales, v_scales, block_table, cu_rows, kv_len, num_tokens, out=None,
+                       error_word=None, stream=None):
+    """Cached tokens of a cache in 8 bits read back as packed bf16 rows
+    (include/kda_paged_fp8.h): request r has rows cu_rows[r] .. cu_rows[r+1]-1,
+    its last tokens up to kv_len[r]. Returns PagedRead(k, v), bf16
+    [num_tokens, Hkv, D]."""
+    return prepare_paged_read_fp8(k_codes, v_codes, k_scales, v_scales, block_table, cu_rows, kv_len, num_tokens, out,
+                                  error_word, stream)()

@@ -55,3 +55,10 @@ from .kda_paged_oracle import (  # noqa: F401,E402
     rope_frequencies,
     paged_attention,
 )
+from .kda_paged_fp8_oracle import (  # noqa: F401,E402
+    scale_exponent,
+    dequantized,
+    write_side,
+    rope_append_fp8,
+    paged_read_fp8,
+)
