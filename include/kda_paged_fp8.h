@@ -73,8 +73,8 @@ kda_status kda_rope_append_fp8(const kda_rope_params* p, const kda_paged_scales*
  * code * scale. Scores, maxima, sums and outputs are kept in fp32, out is
  * rounded to bf16 once. On the tensor cores
  *   - a query enters as two E4M3 numbers by a power of two for its row and
- *     head, exact within 2^8 of the largest magnitude of its head and off by
- *     2^-18 of that below;
+ *     head, exact within 2^9 of the largest magnitude of its head and off by
+ *     less than 2^-17 of that below;
  *   - a weight, times its key's value scale, enters as fp16, by a power of two
  *     for the row that follows its largest; its sum does not.
  * A query with an infinite or NaN number gives NaN in out and lse. NaN codes

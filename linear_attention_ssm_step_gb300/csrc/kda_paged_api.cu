@@ -306,9 +306,10 @@ kda_status paged_attention(const char* call, const kda_attention_params* p, bool
   if (overlaps(w, o) || overlaps(w, l)) return fail(KDA_EINVAL, "workspace overlaps out or lse");
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaErrorNotSupported;
-  if (!fp8 && kda::paged_attention_on_tensor_cores(p->cache))
-    e = kda::launch_paged_attention_tc(*p, workspace, attention_ctas(), st);
-  if (e == cudaErrorNotSupported) e = kda::launch_paged_attention_simt(*p, fp8 ? sc : nullptr, st);
+  const kda_paged_scales* const scales = fp8 ? sc : nullptr;
+  if (kda::paged_attention_on_tensor_cores(p->cache, fp8))
+    e = kda::launch_paged_attention_tc(*p, scales, workspace, attention_ctas(), st);
+  if (e == cudaErrorNotSupported) e = kda::launch_paged_attention_simt(*p, scales, st);
   if (e != cudaSuccess) return fail(KDA_ELAUNCH, "%s launch: %s", call, cudaGetErrorString(e));
   return ok();
 }

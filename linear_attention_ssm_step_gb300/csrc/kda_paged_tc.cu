@@ -46,6 +46,7 @@
 // is kept short and in loops that are not unrolled: it is fetched anew each run.
 #include <math.h>
 
+#include "kda_fp8_codec.cuh"
 #include "kda_paged.cuh"
 #include "kda_paged_launch.h"
 #include "kda_tc.cuh"
@@ -56,28 +57,37 @@ namespace {
 
 constexpr int UNIT = 128;   // keys a unit
 constexpr int TILE = 128;   // rows a tile
-constexpr int THREADS = 384;
 constexpr int SOFTMAX_THREADS = 256;
 // Which of the SM's four schedulers (warp mod 4) has which of them: with the loads on 1, beside softmax warps 1 and 5,
 // verify and decode steps take 54.6 and 193.6 us, on 0 57.2 and 195.0; chunks 561 against 560.
 constexpr int PRODUCT_WARP = 8, LOAD_WARP = 9, WALK_WARP = 10, AHEAD_WARP = 11;
+constexpr int CONVERT_WARP = 12, CONVERT_WARPS = 3, SCALE_WARP = 15;  // of a cache in 8 bits
 constexpr int FIRST = 96;   // keys of a unit whose weights are handed over first, while the others' are formed
 constexpr int RING = 4;  // segments the walking warp may be ahead
 // What an item costs beside its units (its queries, its end), in units: each item takes LEAD + its units of the line. A
 // first chunk of 4096 tokens, whose items have 1 to 32 units: 122 us at 3, 118 at 4, 119.5 at 5 (two tiles); 32 verify
 // requests: 56.7 us at 1, 55.7 at 2, 54.6 at 4, 56.4 at 6 (one tile).
 constexpr int LEAD = 4;
-// Registers a thread after the split: 256 x 208 + 128 x 88 = 384 x 168, what the block launches with.
-constexpr int SOFTMAX_REGS = 208, OTHER_REGS = 88;
+constexpr int SCALES = 4;                                  // units whose scales are held
+constexpr int BLOCK = KDA_FP8_SCALE_TOKENS, BLOCKS = UNIT / BLOCK;  // keys a scale, scales a unit
 
-template <int D>
+// FP8: a cache in 8 bits. A tile of queries is then two of E4M3 numbers, of half the size each.
+template <int D, bool FP8>
 struct Shape {
+  // Registers a thread after the split: 256 x 208 + 128 x 88 = 384 x 168, what the block launches with; with the warps of
+  // a cache in 8 bits 256 x 200 + 128 x 72 + 128 x 40 = 512 x 128.
+  static constexpr int THREADS = FP8 ? 512 : 384;
+  static constexpr int SOFTMAX_REGS = FP8 ? 200 : 208, OTHER_REGS = FP8 ? 72 : 88, CONVERT_REGS = 40;
   static constexpr int K_STAGES = D == 128 ? 3 : 4;
   static constexpr int V_STAGES = D == 128 ? 2 : 4;
-  static constexpr uint32_t TILE_BYTES = TILE * D * 2;  // also a unit of keys or values
+  static constexpr int R_STAGES = !FP8 ? 0 : D == 128 ? 3 : 4;  // units of values as they are in the cache
+  static constexpr uint32_t TILE_BYTES = TILE * D * 2;         // also a unit of 16-bit keys or values
+  static constexpr uint32_t CODE_BYTES = UNIT * D;             // a unit of codes
+  static constexpr uint32_t KEY_BYTES = FP8 ? CODE_BYTES : TILE_BYTES;
   static constexpr uint32_t Q0 = 0, Q1 = TILE_BYTES;
   static constexpr uint32_t K0 = 2 * TILE_BYTES;
-  static constexpr uint32_t V0 = K0 + K_STAGES * TILE_BYTES;
+  static constexpr uint32_t R0 = K0 + K_STAGES * KEY_BYTES;
+  static constexpr uint32_t V0 = R0 + R_STAGES * CODE_BYTES;
   static constexpr uint32_t END = V0 + V_STAGES * TILE_BYTES;
 };
 
@@ -93,12 +103,33 @@ struct Segment {
   int part, parts, cta0; // this run's place among the item's parts, held by the CTAs from cta0 on
 };
 
-struct Shared {
-  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
+// A unit's scales by blocks: of the keys, and log2 and reciprocal of the values'.
+struct UnitScales {
+  float key[BLOCKS], log_value[BLOCKS], inv_value[BLOCKS];
+};
+
+template <int D, bool FP8>
+struct Shared8 {};
+template <int D>
+struct Shared8<D, true> {
+  static constexpr int R_STAGES = Shape<D, true>::R_STAGES;
+  uint64_t r_full[R_STAGES], r_empty[R_STAGES], scale_full[SCALES], scale_empty[SCALES];
+  UnitScales scales[SCALES];
+};
+
+template <int D, bool FP8>
+struct Shared : Shared8<D, FP8> {
+  using S = Shape<D, FP8>;
+  uint64_t k_full[S::K_STAGES], k_empty[S::K_STAGES], v_full[S::V_STAGES], v_empty[S::V_STAGES];
   uint64_t v_tail, q_full[2], s_full[2], p_full[2][2], o_done[2], seg_full[RING], seg_empty[RING], drain;
   Segment seg[RING];
-  float m1[2][TILE], l1[2][TILE];  // the groups' m and l when both share a tile
-  int warp_sum[THREADS / 32];
+  // The groups' m and l when both share a tile. At the start of a run on a cache in 8 bits, m1[t][x] is the power of two by
+  // which the query of thread x of group t was brought down: that thread alone reads it then, and writes m there later.
+  union {
+    float m1[2][TILE];
+    int warp_sum[S::THREADS / 32];  // before the first run
+  };
+  float l1[2][TILE];
   AttnRequest start;  // the request in which this CTA's share begins, and its first unit
   int start_prefix;
   uint32_t tmem;
@@ -319,6 +350,32 @@ __device__ __forceinline__ void issue_scores(uint32_t d, uint64_t a, uint64_t b,
         : "memory");
 }
 
+// The same for E4M3 operands, 32 a K step: the upper parts of the queries, then the lower ones (`tile` bytes on, in the
+// descriptor's units of 16), with the same keys.
+template <int N>
+__device__ __forceinline__ void issue_scores8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t done, uint32_t free) {
+  static_assert(N == 64 || N == 128, "");
+#define KDA_MMA8(A, B, ACC) "@p tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], " A ", " B ", %3, " ACC ";\n\t"
+#define KDA_MMA8_AT(X, Y) "add.s64 x, %1, " X ";\n\tadd.s64 y, %2, " Y ";\n\t" KDA_MMA8("x", "y", "q")
+#define KDA_SCORES8(REST)                                                                                        \
+  asm volatile(                                                                                                  \
+      "{\n\t.reg .pred p, q, t;\n\t.reg .b32 r;\n\t.reg .b64 x, y;\n\t"                                        \
+      "elect.sync r|p, 0xffffffff;\n\tsetp.ne.b32 t, 0, 0;\n\tsetp.eq.b32 q, 0, 0;\n\t" KDA_MMA8("%1", "%2", "t") REST \
+      "@p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n\t"                      \
+      "setp.ne.and.b32 p, %5, 0, p;\n\t"                                                                        \
+      "@p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t}" ::"r"(d),           \
+      "l"(a), "l"(b), "r"(idesc), "r"(done), "r"(free)                                                           \
+      : "memory")
+  if constexpr (N == 128)
+    KDA_SCORES8(KDA_MMA8_AT("2", "2") KDA_MMA8_AT("4", "4") KDA_MMA8_AT("6", "6") KDA_MMA8_AT("1024", "0")
+                KDA_MMA8_AT("1026", "2") KDA_MMA8_AT("1028", "4") KDA_MMA8_AT("1030", "6"));
+  else
+    KDA_SCORES8(KDA_MMA8_AT("2", "2") KDA_MMA8_AT("512", "0") KDA_MMA8_AT("514", "2"));
+#undef KDA_SCORES8
+#undef KDA_MMA8_AT
+#undef KDA_MMA8
+}
+
 // D += A B over keys [0, 96) or [96, 128) of a unit (D = on the first if `fresh`), A (bf16 pairs) in tensor memory, 8
 // columns a K step; B with N contiguous, 2048 bytes a K step. The second part is followed by the arrivals.
 __device__ __forceinline__ void issue_values_first(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t fresh) {
@@ -396,12 +453,61 @@ __device__ __forceinline__ uint64_t value_desc(uint32_t saddr) {
          ((uint64_t)1u << 46) | ((uint64_t)2u << 61);
 }
 constexpr uint32_t B_MN_MAJOR = 1u << 16;  // instruction descriptor: B with N contiguous
+// Formats of A and B in it (bits 7-9, 10-12): 0 is fp16 for products of 16-bit numbers, E4M3 for those of 8-bit ones.
+constexpr uint32_t FORMATS = 63u << 7;
+
+// K-major rows of D codes: 128 bytes with the 128-byte swizzle, or 64 bytes with the 64-byte swizzle (mode 4, 8-row groups
+// 512 bytes apart; chunk c of row r sits at chunk c ^ (r / 2 % 4)).
+template <int D>
+__device__ __forceinline__ uint64_t code_desc(uint32_t saddr) {
+  if constexpr (D == 128) return sw128_desc(saddr);
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)1u << 16) | ((uint64_t)(512u >> 4) << 32) |
+         ((uint64_t)1u << 46) | ((uint64_t)4u << 61);
+}
+template <int D>
+__device__ __forceinline__ uint32_t code_chunk(uint32_t row, uint32_t c) {  // byte offset
+  return D == 128 ? row * 128 + ((c ^ (row & 7)) << 4) : row * 64 + ((c ^ (row >> 1 & 3)) << 4);
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t codes_to_f16x2(uint32_t two) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((unsigned short)two));
+  return r;
+}
+
+// Weights exp2(f s + base) of a block of 16 scores as fp16 pairs; their fp32 sum, times inv, is added to `sum`.
+__device__ __forceinline__ void block_weights(const uint32_t* s, float f, float base, float inv, uint64_t& sum, uint32_t* w) {
+  const uint64_t f2 = pair(f, f), base2 = pair(base, base);
+  uint64_t part[2] = {0, 0};
+#pragma unroll
+  for (int j = 0; j < BLOCK / 2; ++j) {
+    float e0, e1;
+    unpair(fma2(pair(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), f2, base2), e0, e1);
+    e0 = ex2(e0);
+    e1 = ex2(e1);
+    part[j & 1] = add2(part[j & 1], pair(e0, e1));
+    w[j] = pack_f16x2(e0, e1);
+  }
+  sum = fma2(add2(part[0], part[1]), pair(inv, inv), sum);
+}
+
+__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(n) : "memory");
+}
 
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float SLACK = 8.f;  // growth of the maximum (log2) that the reference may lag behind
+constexpr float LIFT = 6.f;   // log2 of the largest fp16 weight when the reference is set: SLACK above it is below 2^15
 
 struct AttnArgs {
   kda_attention_params p;
+  kda_paged_scales sc;  // of a cache in 8 bits
   float* parts;        // workspace: 2 slots a CTA, each [D / 4][2 TILE] float4 of unnormalised O, then [2 TILE] of (m, l)
   unsigned* counters;  // one a CTA, zero between calls
   int q_wide, out_wide;
@@ -423,13 +529,14 @@ __device__ __forceinline__ float2* part_ml(const AttnArgs& a, int slot) {
 
 }  // namespace
 
-template <int D>
-__global__ void __launch_bounds__(THREADS, 1)
+template <int D, bool FP8>
+__global__ void __launch_bounds__(Shape<D, FP8>::THREADS, 1)
     kda_paged_attention_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                                   const __grid_constant__ AttnArgs a) {
-  using S = Shape<D>;
+  using S = Shape<D, FP8>;
+  constexpr int THREADS = S::THREADS;
   extern __shared__ __align__(1024) uint8_t smem[];  // the swizzle's atoms are 1024-byte aligned
-  Shared& sh = *reinterpret_cast<Shared*>(smem + S::END);
+  Shared<D, FP8>& sh = *reinterpret_cast<Shared<D, FP8>*>(smem + S::END);
   const kda_attention_params& p = a.p;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = a.group, Hkv = p.cache.num_heads;
@@ -442,12 +549,23 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init_only(&sh.k_empty[lane], 1);
     }
     if (lane < S::V_STAGES) {
-      mbar_init_only(&sh.v_full[lane], 1);
+      mbar_init_only(&sh.v_full[lane], FP8 ? CONVERT_WARPS : 1);
       mbar_init_only(&sh.v_empty[lane], 1);
+    }
+    if constexpr (FP8) {
+      if (lane < S::R_STAGES) {
+        mbar_init_only(&sh.r_full[lane], 1);
+        mbar_init_only(&sh.r_empty[lane], CONVERT_WARPS);
+      }
+      if (lane < SCALES) {
+        mbar_init_only(&sh.scale_full[lane], 1);
+        mbar_init_only(&sh.scale_empty[lane], SOFTMAX_THREADS / 32);  // an arrival a warp, two where one group takes the unit
+      }
     }
     if (lane < RING) {
       mbar_init_only(&sh.seg_full[lane], 1);
-      mbar_init_only(&sh.seg_empty[lane], 5);  // the loading, product and prefetching warps, both softmax groups
+      // the loading, product and prefetching warps, both softmax groups; the converting and scale warps
+      mbar_init_only(&sh.seg_empty[lane], FP8 ? 6 + CONVERT_WARPS : 5);
     }
     if (lane < 2) {
       mbar_init_only(&sh.q_full[lane], TILE);
@@ -544,7 +662,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t S_COL = tmem, O_COL = tmem + 2 * TILE;
 
   if (warp >= SOFTMAX_THREADS / 32) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
+    if (FP8 && warp >= CONVERT_WARP)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::CONVERT_REGS));
+    else
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::OTHER_REGS));
     bool alive = true;
 
     if (warp == WALK_WARP) {
@@ -652,8 +773,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     } else if (warp == LOAD_WARP) {
       // ---- keys and values of the CTA's units, a lane per copy; keys one unit ahead
       const int P = p.cache.page_size, box = a.box;
-      const int copies = (UNIT / box) * (D / 64);
-      const int piece = lane / (D / 64), half = lane % (D / 64);  // which keys of the unit, which columns
+      constexpr int HALVES = FP8 ? 1 : D / 64;  // copies of a piece, by columns
+      const int copies = (UNIT / box) * HALVES;
+      const int piece = lane / HALVES, half = lane % HALVES;  // which keys of the unit, which columns
       uint32_t kn = 0, vn = 0, tails = 0;
       bool bad_page = false, pending = false;  // pending: a ragged unit of values is on its way
       int first = 0, last = UNIT;              // the keys of it that are in use
@@ -695,16 +817,25 @@ __global__ void __launch_bounds__(THREADS, 1)
               bad_page = true;
             }
           }
-          const uint32_t n = values ? vn : kn, stages = values ? S::V_STAGES : S::K_STAGES, st = n % stages;
-          if (!warp_wait(values ? &sh.v_empty[st] : &sh.k_empty[st], (n / stages + 1) & 1)) return false;
-          uint8_t* const dst = smem + (values ? S::V0 : S::K0) + st * S::TILE_BYTES;
-          const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, wanted)) * (uint32_t)box * 128u;
-          uint64_t* bar = values ? &sh.v_full[st] : &sh.k_full[st];
-          if (values) {
+          const uint32_t n = values ? vn : kn, stages = values ? (FP8 ? S::R_STAGES : S::V_STAGES) : S::K_STAGES, st = n % stages;
+          uint64_t *bar = values ? &sh.v_full[st] : &sh.k_full[st], *empty = values ? &sh.v_empty[st] : &sh.k_empty[st];
+          uint8_t* dst = smem + (values ? S::V0 : S::K0) + st * (values ? S::TILE_BYTES : S::KEY_BYTES);
+          if constexpr (FP8)
+            if (values) {
+              bar = &sh.r_full[st];
+              empty = &sh.r_empty[st];
+              dst = smem + S::R0 + st * S::CODE_BYTES;
+            }
+          if (!warp_wait(empty, (n / stages + 1) & 1)) return false;
+          constexpr uint32_t ROW = FP8 ? D : 128;  // bytes a copy brings of a key
+          const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, wanted)) * (uint32_t)box * ROW;
+          if (values && !FP8) {
             first = max(sg.lo - u * UNIT, 0);
             last = min(sg.hi - u * UNIT, UNIT);
             pending = first > 0 || last < UNIT;
             if (pending) bar = &sh.v_tail;
+          }
+          if (values) {
             ++vn;
           } else {
             ++kn;
@@ -712,7 +843,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (lane == 0) mbar_expect_tx(bar, bytes);
           __syncwarp();
           if (wanted)
-            tma_load_4d(dst + half * (TILE * 128) + piece * box * 128, values ? &vmap : &kmap, half * 64, key % P, sg.head,
+            tma_load_4d(dst + half * (TILE * 128) + piece * box * ROW, values ? &vmap : &kmap, half * 64, key % P, sg.head,
                         page, bar);
           return true;
         };
@@ -726,11 +857,16 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (alive && pending) alive = clear_tail();
       if (bad_page && p.error_word) atomicOr(p.error_word, KDA_ERR_PAGES);
       if (!alive) {  // copies in flight land before the CTA leaves
-        mbar_drain_bounded(&sh.v_tail, tails & 1);
+        if (!FP8) mbar_drain_bounded(&sh.v_tail, tails & 1);
         for (uint32_t i = kn > (uint32_t)S::K_STAGES ? kn - S::K_STAGES : 0; i < kn; ++i)
           mbar_drain_bounded(&sh.k_full[i % S::K_STAGES], (i / S::K_STAGES) & 1);
-        for (uint32_t i = vn > (uint32_t)S::V_STAGES ? vn - S::V_STAGES : 0; i < vn; ++i)
-          mbar_drain_bounded(&sh.v_full[i % S::V_STAGES], (i / S::V_STAGES) & 1);
+        if constexpr (FP8) {
+          for (uint32_t i = vn > (uint32_t)S::R_STAGES ? vn - S::R_STAGES : 0; i < vn; ++i)
+            mbar_drain_bounded(&sh.r_full[i % S::R_STAGES], (i / S::R_STAGES) & 1);
+        } else {
+          for (uint32_t i = vn > (uint32_t)S::V_STAGES ? vn - S::V_STAGES : 0; i < vn; ++i)
+            mbar_drain_bounded(&sh.v_full[i % S::V_STAGES], (i / S::V_STAGES) & 1);
+        }
       }
     } else if (warp == AHEAD_WARP) {
       // ---- the queries of the runs to come into L2: from memory they take 2400 cycles, in which a run could not start
@@ -755,8 +891,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       // the warp stays together and its operands in uniform registers, and a run of products is one statement (formed one by
       // one, with an election each, they took 85 cycles).
       const uint32_t base = smem_addr(smem), tm = uniform(tmem);
-      constexpr uint32_t IDESC_S = idesc_bf16_f32(TILE, UNIT);
-      constexpr uint32_t IDESC_O = idesc_bf16_f32(TILE, D) | B_MN_MAJOR;
+      constexpr uint32_t IDESC_S = idesc_bf16_f32(TILE, UNIT) & ~(FP8 ? FORMATS : 0u);
+      constexpr uint32_t IDESC_O = (idesc_bf16_f32(TILE, D) & ~(FP8 ? FORMATS : 0u)) | B_MN_MAJOR;
+      auto key_desc = [](uint32_t saddr) { return FP8 ? code_desc<D>(saddr) : sw128_desc(saddr); };
       uint32_t ks = 0, kp = 0, vs = 0, vp = 0, wp[2] = {0, 0}, qp = 0;
       for (uint32_t in = 0; alive; ++in) {
         const uint32_t slot = in % RING;
@@ -769,15 +906,20 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (ntok < 0) break;
         alive = warp_wait(&sh.q_full[0], qp) && warp_wait(&sh.q_full[1], qp);
         qp ^= 1;
-        const uint64_t dq0 = sw128_desc(base + S::Q0), dq1 = dual ? sw128_desc(base + S::Q1) : dq0;
+        const uint64_t dq0 = key_desc(base + S::Q0), dq1 = dual ? key_desc(base + S::Q1) : dq0;
         auto scores = [&](int t, bool early = false) {
           const bool first = !dual || t == 0, last = !dual || t == 1;
           if (first && !early) {
             if (!warp_wait(&sh.k_full[ks], kp)) return false;
             tc_fence_after();
           }
-          issue_scores<D>(tm + t * TILE, t ? dq1 : dq0, sw128_desc(base + S::K0 + ks * S::TILE_BYTES), IDESC_S,
-                          smem_addr(&sh.s_full[t]), last ? smem_addr(&sh.k_empty[ks]) : 0u);
+          const uint64_t dk = key_desc(base + S::K0 + ks * S::KEY_BYTES);
+          if constexpr (FP8)
+            issue_scores8<D>(tm + t * TILE, t ? dq1 : dq0, dk, IDESC_S, smem_addr(&sh.s_full[t]),
+                             last ? smem_addr(&sh.k_empty[ks]) : 0u);
+          else
+            issue_scores<D>(tm + t * TILE, t ? dq1 : dq0, dk, IDESC_S, smem_addr(&sh.s_full[t]),
+                            last ? smem_addr(&sh.k_empty[ks]) : 0u);
           if (last && ++ks == S::K_STAGES) {
             ks = 0;
             kp ^= 1;
@@ -821,15 +963,123 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc_commit_w(&sh.drain);
         mbar_drain_bounded(&sh.drain, 0);
       }
+    } else if constexpr (FP8) {
+      if (warp == SCALE_WARP) {
+        // ---- the scales of the CTA's units, two units at a time (16 lanes each: keys' blocks, then values'), and the
+        // next two on their way meanwhile
+        uint32_t n = 0;
+        const int P = p.cache.page_size, b = lane & (BLOCKS - 1);
+        const bool values = (lane & BLOCKS) != 0;
+        const kda_page_scales& from = values ? a.sc.v : a.sc.k;
+        for (uint32_t in = 0; alive; ++in) {
+          const uint32_t slot = in % RING;
+          alive = warp_wait(&sh.seg_full[slot], (in / RING) & 1);
+          if (!alive) break;
+          const Segment sg = sh.seg[slot];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.seg_empty[slot]);
+          if (sg.ntok < 0) break;
+          const int32_t* const table = p.table + (int64_t)sg.request * p.table_stride;
+          auto fetch = [&](int u0) {
+            const int u = u0 + (lane >> 4);
+            if (u >= sg.u1) return 1.f;
+            const int key = u * UNIT + b * BLOCK;
+            if (key >= sg.hi || key + BLOCK <= sg.lo) return 1.f;  // no key of it is seen
+            const int page = table[key / P];
+            return page < 0 || page >= p.cache.num_pages ? 1.f : block_scale(from, page, key % P, sg.head);
+          };
+          float next = fetch(sg.u0);
+          for (int u = sg.u0; alive && u < sg.u1; u += 2) {
+            const float x = next;
+            next = fetch(u + 2);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              if (!alive || u + half >= sg.u1) break;
+              const uint32_t st = n % SCALES;
+              alive = warp_wait(&sh.scale_empty[st], (n / SCALES + 1) & 1);
+              if (!alive) break;
+              if (lane >> 4 == half) {
+                if (!values) {
+                  sh.scales[st].key[b] = x;
+                } else {
+                  sh.scales[st].log_value[b] = log2f(x);
+                  sh.scales[st].inv_value[b] = 1.f / x;
+                }
+              }
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&sh.scale_full[st]);
+              ++n;
+            }
+          }
+        }
+      } else {
+        // ---- values from codes to fp16, which holds them exactly, in the layout of the product: 16 codes of a key a lane.
+        // Keys that are not in use become zeros: their weights are zero, but zero times what lies there need not be.
+        uint32_t n = 0;
+        for (uint32_t in = 0; alive; ++in) {
+          const uint32_t slot = in % RING;
+          alive = warp_wait(&sh.seg_full[slot], (in / RING) & 1);
+          if (!alive) break;
+          const int ntok = sh.seg[slot].ntok, u0 = sh.seg[slot].u0, u1 = sh.seg[slot].u1, lo = sh.seg[slot].lo, hi = sh.seg[slot].hi;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.seg_empty[slot]);
+          if (ntok < 0) break;
+          for (int u = u0; u < u1; ++u, ++n) {
+            const uint32_t rs = n % S::R_STAGES, vs = n % S::V_STAGES;
+            alive = warp_wait(&sh.r_full[rs], (n / S::R_STAGES) & 1) && warp_wait(&sh.v_empty[vs], (n / S::V_STAGES + 1) & 1);
+            if (!alive) break;
+            const uint8_t* const src = smem + S::R0 + rs * S::CODE_BYTES;
+            uint8_t* const dst = smem + S::V0 + vs * S::TILE_BYTES;
+            const int first = lo - u * UNIT, last = hi - u * UNIT;
+            constexpr int CHUNKS = D / 16, ROUNDS8 = UNIT * CHUNKS / 32, GROUP = 4;
+#pragma unroll 1
+            for (int k = warp - CONVERT_WARP; k < ROUNDS8; k += GROUP * CONVERT_WARPS) {
+              uint4 z[GROUP];
+#pragma unroll
+              for (int i = 0; i < GROUP; ++i) {
+                const int x = (k + i * CONVERT_WARPS) * 32 + lane;
+                z[i] = make_uint4(0, 0, 0, 0);
+                if (x < UNIT * CHUNKS && x / CHUNKS >= first && x / CHUNKS < last)
+                  z[i] = *reinterpret_cast<const uint4*>(src + x * 16);
+              }
+#pragma unroll
+              for (int i = 0; i < GROUP; ++i) {
+                const int x = (k + i * CONVERT_WARPS) * 32 + lane;
+                if (x >= UNIT * CHUNKS) continue;
+                const uint32_t row = x / CHUNKS, c = x % CHUNKS;
+                const uint4 h0 = make_uint4(codes_to_f16x2(z[i].x), codes_to_f16x2(z[i].x >> 16), codes_to_f16x2(z[i].y),
+                                            codes_to_f16x2(z[i].y >> 16));
+                const uint4 h1 = make_uint4(codes_to_f16x2(z[i].z), codes_to_f16x2(z[i].z >> 16), codes_to_f16x2(z[i].w),
+                                            codes_to_f16x2(z[i].w >> 16));
+                // the second half of a row's lanes store their second chunk first, so that eight neighbours meet eight banks
+                const uint32_t flip = c >> 2;
+                uint8_t* const at = dst + (c >> 2) * (TILE * 128) + row * 128;
+                const uint32_t ch = (2 * c) & 7;
+                *reinterpret_cast<uint4*>(at + (((ch + flip) ^ (row & 7)) << 4)) = flip ? h1 : h0;
+                *reinterpret_cast<uint4*>(at + (((ch + 1 - flip) ^ (row & 7)) << 4)) = flip ? h0 : h1;
+              }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&sh.v_full[vs]);
+              mbar_arrive(&sh.r_empty[rs]);
+            }
+          }
+        }
+      }
     }
     if (!alive && lane == 0 && p.error_word) atomicOr(p.error_word, KDA_ERR_TIMEOUT);
     __syncwarp();
   } else {
     // ---- softmax: group t, thread (row) x
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SOFTMAX_REGS));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::SOFTMAX_REGS));
     const int t = warp >> 2;
     const float c = p.scale * LOG2E;
+    // A reference m is in units of the scores, or (FP8) their log2: times to_log2 it is log2, times to_ln ln.
+    const float to_log2 = FP8 ? 1.f : c, to_ln = FP8 ? 0.6931471805599453f : p.scale;
     uint32_t seen_s = 0, runs = 0;  // scores waited for; ends of runs
+    uint32_t units_before = 0;      // FP8: the CTA's units before this run
     bool alive = true;
     auto div_g = [&](int row) { return (int)((uint32_t)row * a.inv_group >> 16); };
     // Where a thread stands is worked out anew for each part of a run: kept over the units, it would cost them registers.
@@ -852,6 +1102,40 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int tk = div_g(r);
       return (int64_t)tk * (int)b_stride + (int64_t)(r - tk * g) * (int)h_stride;
     };
+    // FP8: a query x becomes hi + lo, two E4M3 numbers of x 2^-e with the head's largest in (224, 448]. bf16's eight bits
+    // are four in each, exact down to 2^-2 (2^-9 of the largest or more); below, lo is off by half the subnormals' step,
+    // 2^-10, less than 2^-17 of the largest.
+    auto put_codes = [&](uint4 z, bool there, int r, int ch, uint8_t* tile, bool both) {
+      const uint32_t words[4] = {z.x, z.y, z.z, z.w};
+      float x[8], top = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) unpack_bf16x2(words[j], x[2 * j], x[2 * j + 1]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[j]));
+#pragma unroll
+      for (int o = D / 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const int e = top > 0.f ? max(row_exponent(top), -100) : 0;
+      const float down = top < INFINITY ? pow2f(-e) : __uint_as_float(0x7fc00000u);  // an infinite query: NaN
+      uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float u = x[2 * j] * down, w = x[2 * j + 1] * down;
+        const uint32_t h = f32x2_to_e4m3x2(pk2(u, w));
+        float hu, hw;
+        upk2(e4m3x2_to_f32x2(h), hu, hw);
+        hi[j >> 1] |= h << (16 * (j & 1));
+        lo[j >> 1] |= f32x2_to_e4m3x2(pk2(u - hu, w - hw)) << (16 * (j & 1));
+      }
+      if (!there) return;
+      uint8_t* const at = tile + code_chunk<D>(r, ch >> 1) + (ch & 1) * 8;
+      *reinterpret_cast<uint2*>(at) = make_uint2(hi[0], hi[1]);
+      *reinterpret_cast<uint2*>(at + S::CODE_BYTES) = make_uint2(lo[0], lo[1]);
+      if (ch == 0) {
+        const float up = pow2f(e);
+        sh.m1[t][r] = up;
+        if (both) sh.m1[1 - t][r] = up;
+      }
+    };
     // The queries of a run: a group's tile, or its half of the tile that both share.
     auto fetch_q = [&](const Segment& n) {
       const Place me = place();
@@ -861,7 +1145,32 @@ __global__ void __launch_bounds__(THREADS, 1)
       const uint16_t* const qg = static_cast<const uint16_t*>(p.q.ptr) + (int64_t)(n.row0 + tile0) * p.q.b_stride +
                                  (int64_t)(n.head * g) * p.q.h_stride + me.ch * 8;
       uint8_t* const qs = smem + (n.dual && t ? S::Q1 : S::Q0) + me.at + from * 128;
-      if (a.q_wide) {  // asynchronously, all rounds in flight
+      if constexpr (FP8) {
+#pragma unroll 1
+        for (int k0 = 0; from + k0 * ROWS_A_ROUND < to; k0 += 4) {  // the same for the whole warp
+          uint4 z[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int r = from + me.row + (k0 + k) * ROWS_A_ROUND;
+            z[k] = make_uint4(0, 0, 0, 0);
+            if (r >= to) continue;
+            const uint16_t* const src = qg + row_offset(r, p.q.b_stride, p.q.h_stride);
+            if (a.q_wide) {
+              z[k] = *reinterpret_cast<const uint4*>(src);
+            } else {
+              uint32_t e[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) e[j] = (uint32_t)src[2 * j] | ((uint32_t)src[2 * j + 1] << 16);
+              z[k] = make_uint4(e[0], e[1], e[2], e[3]);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int r = from + me.row + (k0 + k) * ROWS_A_ROUND;
+            put_codes(z[k], r < to, r, me.ch, smem + (n.dual && t ? S::Q1 : S::Q0), !n.dual);
+          }
+        }
+      } else if (a.q_wide) {  // asynchronously, all rounds in flight
 #pragma unroll 4
         for (int k = 0; k < ROUNDS; ++k) {
           const int r = from + me.row + k * ROWS_A_ROUND;
@@ -894,6 +1203,11 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (sg.ntok < 0) break;
       const int dual = sg.dual;
       fetch_q(sg);
+      float query_scale = 0.f;
+      if constexpr (FP8) {
+        bar_sync(2, SOFTMAX_THREADS);
+        query_scale = c * sh.m1[t][fresh_tid() & (TILE - 1)];
+      }
 
       // Keys [lo, hi) that this thread's row sees; a row of no token is carried along unmasked and goes nowhere.
       struct Row {
@@ -926,6 +1240,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       int units = 0;
       for (int u = sg.u0 + (dual ? 0 : t); u < sg.u1; u += step) {
         alive = alive && warp_wait(&sh.s_full[t], seen_s & 1);
+        const uint32_t unit = units_before + (uint32_t)(u - sg.u0);
+        if constexpr (FP8) alive = alive && warp_wait(&sh.scale_full[unit % SCALES], (unit / SCALES) & 1);
         if (!alive) break;
         if (warp_valid) {
           tc_fence_after();
@@ -948,9 +1264,64 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (!(bits >> i & 1u)) s[b + i] = 0xff800000u;  // -inf
             }
           }
+          auto give = [&](int h) {  // these weights are there: the products that take them may start
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.p_full[t][h]);
+          };
+          auto fade_o = [&](float fade) {
+#pragma unroll 1
+            for (int i = 0; i < D; i += 16) {  // 16 columns at a time: the 128 scores stay in registers
+              float o[16];
+              tmem_ld16(o_addr + i, o);
+              uint32_t o2[16];
+#pragma unroll
+              for (int j = 0; j < 16; ++j) o2[j] = __float_as_uint(o[j] * fade);
+              tmem_st16(o_addr + i, o2);
+            }
+          };
+          uint32_t wa[16];
+          if constexpr (FP8) {
+            // y = f s is a score in log2 units, f its block's factor; weights times value scales are exp2(y + log2 vs - m)
+            const UnitScales& us = sh.scales[unit % SCALES];
+            float top = -INFINITY;
+#pragma unroll
+            for (int b = 0; b < BLOCKS; ++b) {
+              float t0 = __uint_as_float(s[b * BLOCK]), t1 = __uint_as_float(s[b * BLOCK + 1]);
+#pragma unroll
+              for (int j = 2; j < BLOCK; j += 4) {
+                t0 = max3(t0, __uint_as_float(s[b * BLOCK + j]), __uint_as_float(s[b * BLOCK + j + 1]));
+                if (j + 2 < BLOCK) t1 = max3(t1, __uint_as_float(s[b * BLOCK + j + 2]), __uint_as_float(s[b * BLOCK + j + 3]));
+              }
+              top = fmaxf(top, fmaf(fmaxf(t0, t1), query_scale * us.key[b], us.log_value[b]));
+            }
+            const bool grown = valid && top - m > LIFT + SLACK;  // m = -inf: any key (-inf less itself is no number)
+            if (__builtin_expect(__any_sync(0xffffffffu, grown), 0)) {
+              const float fade = grown ? ex2(m - (top - LIFT)) : 1.f;
+              if (grown) m = top - LIFT;
+              l *= fade;
+              if (units > 0) fade_o(fade);  // the product of the unit before is done: these scores waited for it
+            }
+            const float base = m == -INFINITY ? 0.f : -m;
+            uint64_t sum = 0;
+#pragma unroll
+            for (int i = 0; i < UNIT; i += 32) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int b = i / BLOCK + h;
+                block_weights(s + b * BLOCK, query_scale * us.key[b], base + us.log_value[b], us.inv_value[b], sum, wa + 8 * h);
+              }
+              st16(s_addr + i / 2, wa);
+              if (i + 32 == FIRST) give(0);
+            }
+            give(1);
+            float l0, l1;
+            unpair(sum, l0, l1);
+            l += l0 + l1;
+          } else {
           const uint64_t c2 = pair(c, c);
           uint64_t sum[4] = {0, 0, 0, 0}, base2 = reference(m, c);
-          uint32_t wa[16];
           float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
           for (int i = 0; i < UNIT; i += 8)
@@ -963,26 +1334,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             const float fade = grown ? ex2((m - top) * c) : 1.f;
             if (grown) m = top;
             l *= fade;
-            if (units > 0) {  // the product of the unit before is done: these scores waited for it
-#pragma unroll 1
-              for (int i = 0; i < D; i += 16) {  // 16 columns at a time: the 128 scores stay in registers
-                float o[16];
-                tmem_ld16(o_addr + i, o);
-                uint32_t o2[16];
-#pragma unroll
-                for (int j = 0; j < 16; ++j) o2[j] = __float_as_uint(o[j] * fade);
-                tmem_st16(o_addr + i, o2);
-              }
-            }
+            if (units > 0) fade_o(fade);  // the product of the unit before is done: these scores waited for it
             base2 = reference(m, c);
           }
           weights<32>(s, c2, base2, sum, wa);
-          auto give = [&](int h) {  // these weights are there: the products that take them may start
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.p_full[t][h]);
-          };
           st16(s_addr, wa);
           weights<32>(s + 32, c2, base2, sum, wa);
           st16(s_addr + 16, wa);
@@ -995,13 +1350,20 @@ __global__ void __launch_bounds__(THREADS, 1)
           float l0, l1;
           unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), l0, l1);
           l += l0 + l1;
+          }
         } else if (lane == 0) {
           mbar_arrive(&sh.p_full[t][0]);
           mbar_arrive(&sh.p_full[t][1]);
         }
+        if constexpr (FP8) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive_n(&sh.scale_empty[unit % SCALES], dual ? 1 : 2);
+        }
         ++seen_s;
         ++units;
       }
+
+      units_before += (uint32_t)(sg.u1 - sg.u0);
 
       // ---- the end of the run
       const Place me = place();
@@ -1020,7 +1382,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (!dual) {  // the same bits of m and l in both groups
         const float m0 = sh.m1[0][x], m1 = sh.m1[1][x];
         m = fmaxf(m0, m1);
-        const float mb = m == -INFINITY ? 0.f : m, fade0 = ex2((m0 - mb) * c), fade1 = ex2((m1 - mb) * c);
+        const float mb = m == -INFINITY ? 0.f : m, fade0 = ex2((m0 - mb) * to_log2), fade1 = ex2((m1 - mb) * to_log2);
         l = sh.l1[0][x] * fade0 + sh.l1[1][x] * fade1;
         fade = t ? fade1 : fade0;
         fade_other = t ? fade0 : fade1;
@@ -1114,9 +1476,9 @@ __global__ void __launch_bounds__(THREADS, 1)
               top = fmaxf(top, z[i].x);
             }
             const float mb = top == -INFINITY ? 0.f : top;
-            ll *= ex2((mm - mb) * c);
+            ll *= ex2((mm - mb) * to_log2);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) ll = fmaf(z[i].y, ex2((z[i].x - mb) * c), ll);
+            for (int i = 0; i < 8; ++i) ll = fmaf(z[i].y, ex2((z[i].x - mb) * to_log2), ll);
             mm = top;
           }
           return make_float2(mm, ll);
@@ -1146,7 +1508,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                   const float4* const o = part_o<D>(a, sid) + (col / 4) * (2 * TILE) + part_row;
 #pragma unroll
                   for (int j = 0; j < 8; ++j) v[i][j] = on ? __ldcg(o + j * (2 * TILE)) : make_float4(0.f, 0.f, 0.f, 0.f);
-                  w[i] = ex2((__ldcg(&part_ml<D>(a, sid)[part_row].x) - mb) * c);
+                  w[i] = ex2((__ldcg(&part_ml<D>(a, sid)[part_row].x) - mb) * to_log2);
                 }
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
@@ -1186,12 +1548,12 @@ __global__ void __launch_bounds__(THREADS, 1)
               float top = mm;
 #pragma unroll
               for (int i = 0; i < 8; ++i) top = fmaxf(top, z[i].x);
-              const float mb = top == -INFINITY ? 0.f : top, f = ex2((mm - mb) * c);
+              const float mb = top == -INFINITY ? 0.f : top, f = ex2((mm - mb) * to_log2);
               ll *= f;
               acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
-                const float w = ex2((z[i].x - mb) * c);
+                const float w = ex2((z[i].x - mb) * to_log2);
                 ll = fmaf(z[i].y, w, ll);
                 acc.x = fmaf(v[i].x, w, acc.x);
                 acc.y = fmaf(v[i].y, w, acc.y);
@@ -1215,7 +1577,7 @@ __global__ void __launch_bounds__(THREADS, 1)
               dst[2] = (uint16_t)b1;
               dst[3] = (uint16_t)(b1 >> 16);
             }
-            if (group == 0 && p.lse != nullptr) p.lse[row0 * p.num_q_heads + h] = mm * p.scale + ln(ll);
+            if (group == 0 && p.lse != nullptr) p.lse[row0 * p.num_q_heads + h] = mm * to_ln + ln(ll);
           }
         }
       }
@@ -1254,7 +1616,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       if (whole && writes && p.lse != nullptr)
         p.lse[((int64_t)sg.row0 + (dual ? t * tpt : 0) + div_g(x)) * p.num_q_heads + sg.head * g + (x - div_g(x) * g)] =
-            m * p.scale + ln(l);  // no key, or scores of -inf alone: -inf; a score of +inf or NaN: NaN
+            m * to_ln + ln(l);  // no key, or scores of -inf alone: -inf; a score of +inf or NaN: NaN
       if (t == 0)
         bar_sync(3, TILE);
       else
@@ -1274,26 +1636,28 @@ size_t paged_attention_parts_bytes(int head_dim, int ctas) {
   return (size_t)ctas * 2 * (2 * TILE) * (head_dim + 2) * sizeof(float);
 }
 
-bool paged_attention_on_tensor_cores(const kda_paged_cache& c) {
-  auto rows16 = [](const kda_pages& g) {
-    return (reinterpret_cast<uintptr_t>(g.ptr) & 15) == 0 && g.page_stride % 8 == 0 && g.token_stride % 8 == 0 &&
-           g.head_stride % 8 == 0;
+bool paged_attention_on_tensor_cores(const kda_paged_cache& c, bool fp8) {
+  const int elems = fp8 ? 16 : 8;  // of 16 bytes
+  auto rows16 = [&](const kda_pages& g) {
+    return (reinterpret_cast<uintptr_t>(g.ptr) & 15) == 0 && g.page_stride % elems == 0 && g.token_stride % elems == 0 &&
+           g.head_stride % elems == 0;
   };
   return (c.head_dim == 64 || c.head_dim == 128) && c.num_pages > 0 && c.page_size >= 16 &&
          (c.page_size & (c.page_size - 1)) == 0 && rows16(c.k) && rows16(c.v);
 }
 
-template <int D>
+template <int D, bool FP8>
 static cudaError_t launch_tc(const CUtensorMap& km, const CUtensorMap& vm, const AttnArgs& a, int ctas, cudaStream_t s) {
-  constexpr size_t bytes = Shape<D>::END + sizeof(Shared);
+  constexpr size_t bytes = Shape<D, FP8>::END + sizeof(Shared<D, FP8>);
   static_assert(bytes <= 232448, "shared memory of one CTA");
   static DeviceFlags done;
-  const cudaError_t e = set_smem_limit_once(kda_paged_attention_tc_kernel<D>, bytes, done);
+  const cudaError_t e = set_smem_limit_once(kda_paged_attention_tc_kernel<D, FP8>, bytes, done);
   if (e != cudaSuccess) return e;
-  return launch_early(kda_paged_attention_tc_kernel<D>, dim3((unsigned)ctas), THREADS, bytes, s, km, vm, a);
+  return launch_early(kda_paged_attention_tc_kernel<D, FP8>, dim3((unsigned)ctas), Shape<D, FP8>::THREADS, bytes, s, km, vm, a);
 }
 
-cudaError_t launch_paged_attention_tc(const kda_attention_params& p, void* workspace, int ctas, cudaStream_t s) {
+cudaError_t launch_paged_attention_tc(const kda_attention_params& p, const kda_paged_scales* scales, void* workspace,
+                                      int ctas, cudaStream_t s) {
   if ((p.q.b_stride | p.q.h_stride | p.out_b_stride | p.out_h_stride) >> 31) return cudaErrorNotSupported;
   // the line of units is counted in 32 bits: at most so many items of so many units a key-value head (for ranges that
   // share no rows; the kernel turns away others that hold more than num_tokens)
@@ -1305,6 +1669,7 @@ cudaError_t launch_paged_attention_tc(const kda_attention_params& p, void* works
   if (items * (keys / UNIT + 2 + LEAD) > 0x7fffffffLL / p.cache.num_heads) return cudaErrorNotSupported;
   AttnArgs a;
   a.p = p;
+  a.sc = scales ? *scales : kda_paged_scales{};
   a.counters = static_cast<unsigned*>(workspace);
   a.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + KDA_ATTENTION_WORKSPACE_ZEROED);
   auto rows16 = [](const void* x, int64_t b, int64_t h) {
@@ -1317,10 +1682,17 @@ cudaError_t launch_paged_attention_tc(const kda_attention_params& p, void* works
   a.tile_tokens = TILE / a.group;
   a.inv_group = 65536u / (unsigned)a.group + 1u;  // for row < 128 and group <= 128 the excess is below 128 / 2^16 < 1 / group
   CUtensorMap km, vm;
+  const bool wide = p.cache.head_dim == 128;
+  if (scales != nullptr) {
+    cudaError_t e = code_pages_tensor_map(p.cache.k, p.cache, a.box, true, &km);
+    if (e == cudaSuccess) e = code_pages_tensor_map(p.cache.v, p.cache, a.box, false, &vm);
+    if (e != cudaSuccess) return e;
+    return wide ? launch_tc<128, true>(km, vm, a, ctas, s) : launch_tc<64, true>(km, vm, a, ctas, s);
+  }
   cudaError_t e = pages_tensor_map(p.cache.k, p.cache, a.box, &km);
   if (e == cudaSuccess) e = pages_tensor_map(p.cache.v, p.cache, a.box, &vm);
   if (e != cudaSuccess) return e;
-  return p.cache.head_dim == 64 ? launch_tc<64>(km, vm, a, ctas, s) : launch_tc<128>(km, vm, a, ctas, s);
+  return wide ? launch_tc<128, false>(km, vm, a, ctas, s) : launch_tc<64, false>(km, vm, a, ctas, s);
 }
 
 }  // namespace kda

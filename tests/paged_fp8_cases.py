@@ -14,8 +14,8 @@ Bounds (derived, element-wise):
         that the largest of a row is 2^6 or more, and fp16's subnormals round by 2^-25: 2^-31 of that largest for each
         key seen, times |code| <= 448, and a scale s has a code of 224 or more in its block, so |v| >= 224 s in it:
         2^-30 max |v| each, 2^-29 with room;
-      - on the tensor cores a query number below 2^-8 of its head's largest is off by 2^-18 of that: a score by
-        2^-18 scale max_c |q_c| max_j sum_c |k_jc|. Added to e.
+      - on the tensor cores a query number below 2^-9 of its head's largest is off by 2^-17 of that: a score by
+        2^-17 scale max_c |q_c| max_j sum_c |k_jc|. Added to e.
 """
 
 import numpy as np
@@ -129,7 +129,7 @@ class Attention:
         out, lse, A, S, count, _ = ref
         k, v = self.values()
         e = ((self.D + 8) * 2.0 ** -23 + 2.0 ** -22) * S
-        e = e + 2.0 ** -18 * self.scale * np.abs(f64(self.q)).max(-1) * np.abs(k).sum(-1).max(initial=0.0)
+        e = e + 2.0 ** -17 * self.scale * np.abs(f64(self.q)).max(-1) * np.abs(k).sum(-1).max(initial=0.0)
         sums = ((count + 64) * 2.0 ** -23)[:, None]
         rel = 2.0 ** -11 + 2 * e + 2.0 ** -21 + sums
         small = (count * 2.0 ** -29 * np.abs(v).max(initial=0.0))[:, None, None]
