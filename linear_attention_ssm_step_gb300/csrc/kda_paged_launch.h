@@ -25,15 +25,20 @@ cudaError_t launch_paged_read_fp8(const kda_read_params& p, const kda_paged_scal
 // One side of a paged cache as a tensor map for copies of 64 columns of `box` tokens (kda_tmap.cu).
 cudaError_t pages_tensor_map(const kda_pages& g, const kda_paged_cache& c, int box, CUtensorMap* out);
 
-// One side of a cache in 8 bits for copies of whole heads of `box` tokens: keys with the swizzle of their product (128 bytes
-// for head_dim 128, 64 for 64), values as they are.
-cudaError_t code_pages_tensor_map(const kda_pages& g, const kda_paged_cache& c, int box, bool swizzled, CUtensorMap* out);
+// One side of a cache in 8 bits (head_dim 64 or 128) for copies of whole heads of `box` tokens.
+cudaError_t code_pages_tensor_map(const kda_pages& g, const kda_paged_cache& c, int box, CUtensorMap* out);
 
 // Whether the tensor-core kernel takes this cache (head_dim, page size, alignment), of bf16 or in 8 bits.
 bool paged_attention_on_tensor_cores(const kda_paged_cache& c, bool fp8);
 
 // Workspace bytes of that kernel for parts of items, on `ctas` CTAs, after the zeroed counters.
 size_t paged_attention_parts_bytes(int head_dim, int ctas);
+
+// Rows of an item (4, 8, 16 or 32) in the kernel for few rows over a cache in 8 bits; 0: the requests bring too many. That
+// kernel's launcher; as launch_paged_attention_tc, which calls it.
+int paged_attention_few_rows(const kda_attention_params& p);
+cudaError_t launch_paged_attention_fp8_rows(const kda_attention_params& p, const kda_paged_scales& sc, int rows,
+                                            void* workspace, int ctas, cudaStream_t s);
 
 // Attention on the tensor cores, persistent on `ctas` CTAs (one an SM); cudaErrorNotSupported, with nothing launched,
 // when the cache's strides have no tensor map, a stride of q or out is 2^31 or more, or the work is past 32 bits.

@@ -46,38 +46,37 @@
 // is kept short and in loops that are not unrolled: it is fetched anew each run.
 #include <math.h>
 
-#include "kda_fp8_codec.cuh"
-#include "kda_paged.cuh"
+#include <type_traits>
+
 #include "kda_paged_launch.h"
-#include "kda_tc.cuh"
+#include "kda_paged_line.cuh"
 
 namespace kda {
 
 namespace {
 
-constexpr int UNIT = 128;   // keys a unit
 constexpr int TILE = 128;   // rows a tile
 constexpr int SOFTMAX_THREADS = 256;
 // Which of the SM's four schedulers (warp mod 4) has which of them: with the loads on 1, beside softmax warps 1 and 5,
 // verify and decode steps take 54.6 and 193.6 us, on 0 57.2 and 195.0; chunks 561 against 560.
 constexpr int PRODUCT_WARP = 8, LOAD_WARP = 9, WALK_WARP = 10, AHEAD_WARP = 11;
-constexpr int CONVERT_WARP = 12, CONVERT_WARPS = 3, SCALE_WARP = 15;  // of a cache in 8 bits
+constexpr int CONVERT_WARP = 12, CONVERT_WARPS = 4, CONVERT_REGS = 40;  // of a cache in 8 bits
 constexpr int FIRST = 96;   // keys of a unit whose weights are handed over first, while the others' are formed
 constexpr int RING = 4;  // segments the walking warp may be ahead
 // What an item costs beside its units (its queries, its end), in units: each item takes LEAD + its units of the line. A
 // first chunk of 4096 tokens, whose items have 1 to 32 units: 122 us at 3, 118 at 4, 119.5 at 5 (two tiles); 32 verify
 // requests: 56.7 us at 1, 55.7 at 2, 54.6 at 4, 56.4 at 6 (one tile).
 constexpr int LEAD = 4;
-constexpr int SCALES = 4;                                  // units whose scales are held
+constexpr int SCALES = 2;                                  // pairs of units whose scales are held
 constexpr int BLOCK = KDA_FP8_SCALE_TOKENS, BLOCKS = UNIT / BLOCK;  // keys a scale, scales a unit
 
 // FP8: a cache in 8 bits. A tile of queries is then two of E4M3 numbers, of half the size each.
 template <int D, bool FP8>
 struct Shape {
   // Registers a thread after the split: 256 x 208 + 128 x 88 = 384 x 168, what the block launches with; with the warps of
-  // a cache in 8 bits 256 x 200 + 128 x 72 + 128 x 40 = 512 x 128.
+  // a cache in 8 bits 256 x 208 + 128 x 56 + 128 x 40 = 512 x 128.
   static constexpr int THREADS = FP8 ? 512 : 384;
-  static constexpr int SOFTMAX_REGS = FP8 ? 200 : 208, OTHER_REGS = FP8 ? 72 : 88, CONVERT_REGS = 40;
+  static constexpr int SOFTMAX_REGS = 208, OTHER_REGS = FP8 ? 56 : 88;
   static constexpr int K_STAGES = D == 128 ? 3 : 4;
   static constexpr int V_STAGES = D == 128 ? 2 : 4;
   static constexpr int R_STAGES = !FP8 ? 0 : D == 128 ? 3 : 4;  // units of values as they are in the cache
@@ -91,20 +90,8 @@ struct Shape {
   static constexpr uint32_t END = V0 + V_STAGES * TILE_BYTES;
 };
 
-// A run of units of one item, for one CTA.
-struct Segment {
-  int row0, ntok;        // first row of q, new tokens of the item
-  int head;              // key-value head
-  int pos0;              // position of the first token
-  int request;
-  int lo, hi;            // keys any of its rows sees: [lo, hi)
-  int u0, u1;            // units of this run
-  int dual;              // two row tiles
-  int part, parts, cta0; // this run's place among the item's parts, held by the CTAs from cta0 on
-};
-
 // A unit's scales by blocks: of the keys, and log2 and reciprocal of the values'.
-struct UnitScales {
+struct alignas(16) UnitScales {
   float key[BLOCKS], log_value[BLOCKS], inv_value[BLOCKS];
 };
 
@@ -114,7 +101,7 @@ template <int D>
 struct Shared8<D, true> {
   static constexpr int R_STAGES = Shape<D, true>::R_STAGES;
   uint64_t r_full[R_STAGES], r_empty[R_STAGES], scale_full[SCALES], scale_empty[SCALES];
-  UnitScales scales[SCALES];
+  UnitScales scales[SCALES][2];
 };
 
 template <int D, bool FP8>
@@ -130,56 +117,10 @@ struct Shared : Shared8<D, FP8> {
     int warp_sum[S::THREADS / 32];  // before the first run
   };
   float l1[2][TILE];
-  AttnRequest start;  // the request in which this CTA's share begins, and its first unit
-  int start_prefix;
+  LineStart start;
   uint32_t tmem;
-  int start_request;
   int last_part;
 };
-
-// The keys [lo, hi) that item i (tokens i w .. of n, the first at position pos) sees, and its units.
-struct Span {
-  int lo, hi, u0, u1;
-};
-
-__device__ __forceinline__ Span item_span(int pos, int n, int i, int w, int window) {
-  Span s;
-  s.hi = max(0, pos + min(n, (i + 1) * w));
-  s.lo = first_key(pos + i * w, window);
-  if (s.hi == 0) s.lo = 0;
-  s.u0 = s.lo / UNIT;
-  s.u1 = max(s.u0 + 1, (s.hi + UNIT - 1) / UNIT);  // rows that see no key still need their zeros
-  return s;
-}
-
-// Length on the line of one key-value head of a request: n tokens, w an item. Called by whole warps, one request a lane; a request
-// of many items (a long chunk) is summed by the warp together.
-__device__ __forceinline__ int head_units(int pos, int n, int w, int window) {
-  const int items = (n + w - 1) / w;
-  int units = 0;
-  if (items <= 4)
-    for (int i = 0; i < items; ++i) {
-      const Span s = item_span(pos, n, i, w, window);
-      units += LEAD + s.u1 - s.u0;
-    }
-  unsigned many = __ballot_sync(0xffffffffu, items > 4);
-  const int lane = threadIdx.x & 31;
-  while (many) {
-    const int src = __ffs(many) - 1;
-    many &= many - 1;
-    const int pn = __shfl_sync(0xffffffffu, pos, src), nn = __shfl_sync(0xffffffffu, n, src);
-    const int ni = (nn + w - 1) / w;
-    int part = 0;
-    for (int i = lane; i < ni; i += 32) {
-      const Span s = item_span(pn, nn, i, w, window);
-      part += LEAD + s.u1 - s.u0;
-    }
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
-    if (lane == src) units = part;
-  }
-  return units;
-}
 
 // ---------------------------------------------------------------- tensor memory in 32-column blocks
 
@@ -217,25 +158,6 @@ __device__ __forceinline__ void st16(uint32_t taddr, const uint32_t* v) {
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
       "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// 1 / x and ln x to 2^-22 or better, for sums of weights (from 2^-8 on): bf16 outputs and a log of fp32 terms need no more,
-// and the exact forms are long code for once a run.
-__device__ __forceinline__ float rcp(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float ln(float x) {
-  float y;
-  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y * 0.6931471805599453f;
 }
 
 // Two fp32 at once: x y + z, x + y.
@@ -282,33 +204,6 @@ __device__ __forceinline__ void weights(const uint32_t* s, uint64_t c2, uint64_t
     sum[j & 3] = add2(sum[j & 3], pair(e0, e1));
     w[j] = pack_bf16x2(e0, e1);
   }
-}
-
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
-}
-
-// mbar_wait_bounded with the clock read only every 64th try: reading it takes longer than most of the waits here last.
-__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity) {
-  unsigned long long t0 = 0;
-#pragma unroll 1
-  for (unsigned it = 1; it < WAIT_LIMIT_ITERS; ++it) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((it & 63u) == 0) {
-      const unsigned long long now = global_timer_ns();
-      if (t0 == 0) t0 = now;
-      if (now - t0 > WAIT_LIMIT_NS) return false;
-    }
-  }
-  return false;
-}
-
-// A wait of a whole warp; false for every lane if it gave up for any. The first try, which mostly finds the phase done,
-// is on its own, away from the bounded loop's counting: the warp that issues the products waits four times a pair of
-// units (two chunks of 2048 tokens: 567 us against 584).
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
-  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-  return __all_sync(0xffffffffu, wait_bounded(bar, parity));
 }
 
 // D = A B^T over N / 16 K steps, issued by one elected lane of a converged warp, and then an arrival on `done` (and on
@@ -408,19 +303,11 @@ __device__ __forceinline__ void issue_values_last(uint32_t d, uint32_t a, uint64
       : "memory");
 }
 
-// A value that all lanes hold, for the compiler to keep in a uniform register.
-__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_max_sync(0xffffffffu, x); }
-__device__ __forceinline__ int uniform(int x) { return __reduce_max_sync(0xffffffffu, x); }
-
 // 16 bytes from global to shared memory, asynchronously (both 16-byte aligned); the wait for all of this thread's.
 __device__ __forceinline__ void copy_async16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-
-__device__ __forceinline__ void mbar_init_only(uint64_t* bar, uint32_t count) {  // the fence follows
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(count) : "memory");
-}
 
 __device__ __forceinline__ void prefetch_l2(const void* src) { asm volatile("prefetch.global.L2 [%0];" ::"l"(src)); }
 
@@ -429,18 +316,6 @@ __device__ __forceinline__ uint32_t fresh_tid() {
   uint32_t x;
   asm volatile("mov.u32 %0, %%tid.x;" : "=r"(x));
   return x;
-}
-
-// A barrier of `count` threads that tells all of them whether `x` held for any.
-__device__ __forceinline__ bool bar_any(uint32_t id, uint32_t count, bool x) {
-  uint32_t any;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(any)
-      : "r"((uint32_t)x), "r"(id), "r"(count)
-      : "memory");
-  return any != 0;
 }
 
 __device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
@@ -456,31 +331,6 @@ constexpr uint32_t B_MN_MAJOR = 1u << 16;  // instruction descriptor: B with N c
 // Formats of A and B in it (bits 7-9, 10-12): 0 is fp16 for products of 16-bit numbers, E4M3 for those of 8-bit ones.
 constexpr uint32_t FORMATS = 63u << 7;
 
-// K-major rows of D codes: 128 bytes with the 128-byte swizzle, or 64 bytes with the 64-byte swizzle (mode 4, 8-row groups
-// 512 bytes apart; chunk c of row r sits at chunk c ^ (r / 2 % 4)).
-template <int D>
-__device__ __forceinline__ uint64_t code_desc(uint32_t saddr) {
-  if constexpr (D == 128) return sw128_desc(saddr);
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)1u << 16) | ((uint64_t)(512u >> 4) << 32) |
-         ((uint64_t)1u << 46) | ((uint64_t)4u << 61);
-}
-template <int D>
-__device__ __forceinline__ uint32_t code_chunk(uint32_t row, uint32_t c) {  // byte offset
-  return D == 128 ? row * 128 + ((c ^ (row & 7)) << 4) : row * 64 + ((c ^ (row >> 1 & 3)) << 4);
-}
-
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-__device__ __forceinline__ uint32_t codes_to_f16x2(uint32_t two) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((unsigned short)two));
-  return r;
-}
-
 // Weights exp2(f s + base) of a block of 16 scores as fp16 pairs; their fp32 sum, times inv, is added to `sum`.
 __device__ __forceinline__ void block_weights(const uint32_t* s, float f, float base, float inv, uint64_t& sum, uint32_t* w) {
   const uint64_t f2 = pair(f, f), base2 = pair(base, base);
@@ -495,6 +345,12 @@ __device__ __forceinline__ void block_weights(const uint32_t* s, float f, float 
     w[j] = pack_f16x2(e0, e1);
   }
   sum = fma2(add2(part[0], part[1]), pair(inv, inv), sum);
+}
+
+__device__ __forceinline__ float4 ld_shared4(const float* p) {
+  float4 r;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(r.x), "=f"(r.y), "=f"(r.z), "=f"(r.w) : "r"(smem_addr(p)) : "memory");
+  return r;
 }
 
 __device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
@@ -539,7 +395,7 @@ __global__ void __launch_bounds__(Shape<D, FP8>::THREADS, 1)
   Shared<D, FP8>& sh = *reinterpret_cast<Shared<D, FP8>*>(smem + S::END);
   const kda_attention_params& p = a.p;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int g = a.group, Hkv = p.cache.num_heads;
+  const int g = a.group;
   const int tpt = a.tile_tokens, w = 2 * tpt;  // tokens a tile, an item
   const int window = p.window;
 
@@ -559,13 +415,13 @@ __global__ void __launch_bounds__(Shape<D, FP8>::THREADS, 1)
       }
       if (lane < SCALES) {
         mbar_init_only(&sh.scale_full[lane], 1);
-        mbar_init_only(&sh.scale_empty[lane], SOFTMAX_THREADS / 32);  // an arrival a warp, two where one group takes the unit
+        mbar_init_only(&sh.scale_empty[lane], SOFTMAX_THREADS / 32);  // an arrival a warp
       }
     }
     if (lane < RING) {
       mbar_init_only(&sh.seg_full[lane], 1);
-      // the loading, product and prefetching warps, both softmax groups; the converting and scale warps
-      mbar_init_only(&sh.seg_empty[lane], FP8 ? 6 + CONVERT_WARPS : 5);
+      // the loading, product and prefetching warps, both softmax groups; the converting warps
+      mbar_init_only(&sh.seg_empty[lane], FP8 ? 5 + CONVERT_WARPS : 5);
     }
     if (lane < 2) {
       mbar_init_only(&sh.q_full[lane], TILE);
@@ -585,191 +441,103 @@ __global__ void __launch_bounds__(Shape<D, FP8>::THREADS, 1)
   earlier_work();
 
   // ---- this CTA's share of the line of units
-  int total = 0;
-  unsigned bad = 0;
-  AttnRequest mine_r{0, 0, 0, 0u};
-  int mine = 0, before = 0;  // the units of this thread's request in the latest block, and those before it
-  const int R = p.num_requests;
-  const bool one_block = R <= THREADS;
-  bool summed = false;  // warp_sum holds an earlier block's sums (of this pass or of the one before)
-  auto block_units = [&](int base) {
-    const int r = base + tid;
-    mine_r = AttnRequest{0, 0, 0, 0u};
-    if (r < R) mine_r = attn_request(p, r);
-    bad |= mine_r.bad;
-    mine = head_units(mine_r.kv - mine_r.n, mine_r.n, w, window) * Hkv;
-    int scan = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, scan, o);
-      if (lane >= o) scan += x;
-    }
-    if (summed) __syncthreads();  // every warp has read the sums of the block before
-    summed = true;
-    if (lane == 31) sh.warp_sum[warp] = scan;
-    __syncthreads();
-    before = scan - mine;
-    int all = 0;
-#pragma unroll
-    for (int i = 0; i < THREADS / 32; ++i) {
-      if (i < warp) before += sh.warp_sum[i];
-      all += sh.warp_sum[i];
-    }
-    return all;
-  };
-  // The line is shared evenly: the first `rest` CTAs have share + 1 units. Requests in one block are looked at once; else
-  // once for the sum and once to find where this CTA's share begins.
   const int cta = blockIdx.x;
-  int ctas = 0, share = 0, rest = 0, begin = 0, end = 0;
-  for (int pass = one_block ? 1 : 0; pass < 2; ++pass) {
-    int prefix = 0;
-    for (int base = 0; base < R; base += THREADS) {
-      const int all = block_units(base);
-      if (pass == 0 || one_block) total += all;
-      if (pass == 0 && base + THREADS < R) continue;
-      if (pass == 0 || one_block) {
-        ctas = min(total, (int)gridDim.x);
-        if (cta >= ctas) break;
-        share = total / ctas;
-        rest = total - share * ctas;
-        begin = cta * share + min(cta, rest);
-        end = begin + share + (cta < rest ? 1 : 0);
-      }
-      if (pass == 1 && begin >= prefix + before && begin < prefix + before + mine) {
-        sh.start = mine_r;
-        sh.start_request = base + tid;
-        sh.start_prefix = prefix + before;
-      }
-      prefix += all;
-    }
-    if (cta >= ctas) break;
-  }
-  if (blockIdx.x == 0 && bad && p.error_word) atomicOr(p.error_word, bad);
-  if (cta >= ctas) return;  // the whole CTA: nothing allocated yet
+  const LineShare line = line_share<THREADS, LEAD>(p, w, sh.warp_sum, sh.start);
+  if (blockIdx.x == 0 && line.bad && p.error_word) atomicOr(p.error_word, line.bad);
+  if (cta >= line.ctas) return;  // the whole CTA: nothing allocated yet
   if (warp == PRODUCT_WARP) tmem_alloc(&sh.tmem, 512);
   tc_fence_before();
-  if (__syncthreads_or(bad & KDA_ERR_SEQLENS)) {
-    // Ranges can share rows only where some bounds are out of order. Together they may then hold more rows than there are,
-    // for which the sums above are not made (32 bits): nothing is done.
-    long long rows = 0;
-    for (int r = lane; r < R; r += 32) rows += attn_request(p, r).n;
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) rows += __shfl_xor_sync(0xffffffffu, rows, o);
-    if (rows > p.num_tokens) end = begin;
-  }
+  const int end = line_end(p, line);
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
   const uint32_t S_COL = tmem, O_COL = tmem + 2 * TILE;
 
-  if (warp >= SOFTMAX_THREADS / 32) {
-    if (FP8 && warp >= CONVERT_WARP)
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::CONVERT_REGS));
-    else
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::OTHER_REGS));
+  if (FP8 && warp >= CONVERT_WARP) {
+    if constexpr (FP8) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(CONVERT_REGS));
+      bool alive = true;
+      // ---- values from codes to fp16, which holds them exactly, in the layout of the product: a lane takes 16 codes of a
+      // key, a warp groups of 8 keys. Both layouts are swizzled; the lanes of a quarter warp, which access shared memory
+      // together, take four chunks of a row r and of a row r ^ 5 (head_dim 64: of rows r and r + 1, which lie in 128 bytes),
+      // whose places differ in both. What a lane adds to the group's address never changes.
+      // Keys that are not in use become zeros: their weights are zero, but zero times what lies there need not be.
+      constexpr int HALVES = D / 64;  // of a group's rows
+      const uint32_t c = lane & 3, q = lane >> 3;
+      const uint32_t row = D == 128 ? (lane & 4 ? q ^ 5 : q) : lane >> 2;
+      const uint32_t from = code_chunk<D>(row, c), to = row * 128 + ((2 * c ^ row) & 7) * 16;
+      uint32_t n = 0;
+      for (uint32_t in = 0; alive; ++in) {
+        const uint32_t slot = in % RING;
+        alive = warp_wait(&sh.seg_full[slot], (in / RING) & 1);
+        if (!alive) break;
+        const int ntok = sh.seg[slot].ntok, u0 = sh.seg[slot].u0, u1 = sh.seg[slot].u1, lo = sh.seg[slot].lo, hi = sh.seg[slot].hi;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.seg_empty[slot]);
+        if (ntok < 0) break;
+        for (int u = u0; u < u1; ++u, ++n) {
+          const uint32_t rs = n % S::R_STAGES, vs = n % S::V_STAGES;
+          alive = warp_wait(&sh.r_full[rs], (n / S::R_STAGES) & 1) && warp_wait(&sh.v_empty[vs], (n / S::V_STAGES + 1) & 1);
+          if (!alive) break;
+          constexpr int GROUPS = UNIT / 8 / CONVERT_WARPS;  // of a warp
+          const int key0 = u * UNIT + (warp - CONVERT_WARP) * GROUPS * 8;
+          const uint8_t* const src = smem + S::R0 + rs * S::CODE_BYTES + (warp - CONVERT_WARP) * (GROUPS * 8 * D);
+          uint8_t* const dst = smem + S::V0 + vs * S::TILE_BYTES + (warp - CONVERT_WARP) * (GROUPS * 1024) + to;
+          const bool ragged = lo > u * UNIT || hi < (u + 1) * UNIT;
+          static_assert(GROUPS == 4, "");
+#pragma unroll
+          for (int part = 0; part < 2 * HALVES; ++part) {
+            const int half = part / 2, i0 = part % 2 * 2;
+            uint4 z[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) z[i] = *reinterpret_cast<const uint4*>(src + (i0 + i) * 8 * D + (from ^ (half * 64)));
+            if (__builtin_expect(ragged, 0)) {
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int key = key0 + (i0 + i) * 8 + (int)row;
+                if (key < lo || key >= hi) z[i] = make_uint4(0, 0, 0, 0);
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              uint8_t* const at = dst + half * (TILE * 128) + (i0 + i) * 1024;
+              *reinterpret_cast<uint4*>(at) = make_uint4(codes_to_f16x2(z[i].x), codes_to_f16x2(z[i].x >> 16),
+                                                         codes_to_f16x2(z[i].y), codes_to_f16x2(z[i].y >> 16));
+              uint8_t* const beside = at + (((2 * c ^ row) & 1) ? -16 : 16);  // the place ^ 16
+              *reinterpret_cast<uint4*>(beside) = make_uint4(codes_to_f16x2(z[i].z), codes_to_f16x2(z[i].z >> 16),
+                                                             codes_to_f16x2(z[i].w), codes_to_f16x2(z[i].w >> 16));
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&sh.v_full[vs]);
+            mbar_arrive(&sh.r_empty[rs]);
+          }
+        }
+      }
+      if (!alive && lane == 0 && p.error_word) atomicOr(p.error_word, KDA_ERR_TIMEOUT);
+      __syncwarp();
+    }
+  } else if (warp >= SOFTMAX_THREADS / 32) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::OTHER_REGS));
     bool alive = true;
 
     if (warp == WALK_WARP) {
       // ---- the line of units, cut into segments
-      int r = sh.start_request;
-      int at = begin;
-      int prefix = sh.start_prefix;  // first unit of the current head's first item
       uint32_t out = 0;
-      int head = 0, item = 0;
-      bool fresh = true;  // the place inside request r is still to be found
-      while (alive && at < end && r < R) {
-        const AttnRequest q = fresh ? sh.start : attn_request(p, r);
-        const int pos = q.kv - q.n, items = (q.n + w - 1) / w;
-        if (fresh) {
-          // whole heads first, then 32 items at a time
-          int uh;
-          if (items == 1) {
-            const Span s = item_span(pos, q.n, 0, w, window);
-            uh = LEAD + s.u1 - s.u0;
-          } else {
-            uh = __shfl_sync(0xffffffffu, head_units(pos, lane == 0 ? q.n : 0, w, window), 0);
-          }
-          head = (at - prefix) / uh;
-          prefix += uh * head;
-          item = 0;
-          for (int base = 0; items > 1 && base < items; base += 32) {
-            const int i = base + lane;
-            int u = 0;
-            if (i < items) {
-              const Span s = item_span(pos, q.n, i, w, window);
-              u = LEAD + s.u1 - s.u0;
-            }
-            int scan = u;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-              const int x = __shfl_up_sync(0xffffffffu, scan, o);
-              if (lane >= o) scan += x;
-            }
-            const bool here = i < items && prefix + scan > at;
-            const unsigned found = __ballot_sync(0xffffffffu, here);
-            if (found) {
-              const int src = __ffs(found) - 1;
-              item = base + src;
-              prefix += __shfl_sync(0xffffffffu, scan - u, src);
-              break;
-            }
-            prefix += __shfl_sync(0xffffffffu, scan, 31);
-          }
-          fresh = false;
-        }
-        // `prefix` is the first unit of item `item` of head `head`
-        while (alive && at < end && head < Hkv && items > 0) {
-          const Span s = item_span(pos, q.n, item, w, window);
-          const int units0 = prefix + LEAD, item_end = units0 + (s.u1 - s.u0);
-          const int from = max(at, units0), stop = min(end, item_end);
-          at = stop;
-          prefix = item_end;
-          const int i = item;
-          if (++item == items) {
-            item = 0;
-            ++head;
-          }
-          if (from >= stop) continue;  // the share ends before the item's first unit
-          Segment g2;
-          g2.row0 = q.row0 + i * w;
-          g2.ntok = min(q.n - i * w, w);
-          g2.head = item == 0 ? head - 1 : head;
-          g2.pos0 = pos + i * w;
-          g2.request = r;
-          g2.lo = s.lo;
-          g2.hi = s.hi;
-          g2.u0 = s.u0 + (from - units0);
-          g2.u1 = s.u0 + (stop - units0);
-          g2.dual = g2.ntok > tpt;
-          // the CTA that holds unit x of the line
-          auto holder = [&](int x) {
-            if (x >= begin && x < end) return cta;
-            const int longer = rest * (share + 1);
-            return x < longer ? x / (share + 1) : rest + (x - longer) / share;
-          };
-          g2.cta0 = holder(units0);
-          g2.parts = holder(item_end - 1) - g2.cta0 + 1;
-          g2.part = cta - g2.cta0;
-          const uint32_t slot = out % RING;
-          alive = warp_wait(&sh.seg_empty[slot], (out / RING + 1) & 1);
-          if (!alive) break;
-          if (lane == 0) {
-            sh.seg[slot] = g2;
-            mbar_arrive(&sh.seg_full[slot]);
-          }
-          __syncwarp();
-          ++out;
-        }
-        ++r;
-        head = item = 0;
-      }
-      if (alive) {
+      auto put = [&](Segment g2) {
+        g2.dual = g2.ntok > tpt;
         const uint32_t slot = out % RING;
-        alive = warp_wait(&sh.seg_empty[slot], (out / RING + 1) & 1);
-        if (alive && lane == 0) {
-          sh.seg[slot].ntok = -1;
+        if (!warp_wait(&sh.seg_empty[slot], (out / RING + 1) & 1)) return false;
+        if (lane == 0) {
+          sh.seg[slot] = g2;
           mbar_arrive(&sh.seg_full[slot]);
         }
-      }
+        __syncwarp();
+        ++out;
+        return true;
+      };
+      alive = line_walk<LEAD>(p, w, line, end, sh.start, put);
     } else if (warp == LOAD_WARP) {
       // ---- keys and values of the CTA's units, a lane per copy; keys one unit ahead
       const int P = p.cache.page_size, box = a.box;
@@ -869,20 +637,56 @@ __global__ void __launch_bounds__(Shape<D, FP8>::THREADS, 1)
         }
       }
     } else if (warp == AHEAD_WARP) {
-      // ---- the queries of the runs to come into L2: from memory they take 2400 cycles, in which a run could not start
+      // ---- the queries of the runs to come into L2: from memory they take 2400 cycles, in which a run could not start.
+      // FP8: and the scales of the runs' units, a pair of units at a time (16 lanes each: keys' blocks, then values'), the
+      // next pair on its way meanwhile. The queries then come ahead by the units whose scales are held.
+      uint32_t pairs = 0;
       for (uint32_t in = 0; alive; ++in) {
         const uint32_t slot = in % RING;
         alive = warp_wait(&sh.seg_full[slot], (in / RING) & 1);
         if (!alive) break;
-        const int ntok = sh.seg[slot].ntok, row0 = sh.seg[slot].row0, head = sh.seg[slot].head;
+        const Segment sg = sh.seg[slot];
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.seg_empty[slot]);
-        if (ntok < 0) break;
-        if (in == 0) continue;  // being fetched
-        const uint16_t* const q = static_cast<const uint16_t*>(p.q.ptr) + (int64_t)row0 * p.q.b_stride + (int64_t)(head * g) * p.q.h_stride;
-        for (int r = lane; r < ntok * g; r += 32) {
-          const uint16_t* const src = q + (int64_t)(r / g) * p.q.b_stride + (int64_t)(r % g) * p.q.h_stride;
-          for (int ch = 0; ch < D; ch += 64) prefetch_l2(src + ch);
+        if (sg.ntok < 0) break;
+        const int P = p.cache.page_size, b = lane & (BLOCKS - 1);
+        const bool of_values = (lane & BLOCKS) != 0;
+        const int32_t* const table = p.table + (int64_t)sg.request * p.table_stride;
+        auto fetch = [&](int u0) {
+          const int u = u0 + (lane >> 4);
+          if (u >= sg.u1) return 1.f;
+          const int key = u * UNIT + b * BLOCK;
+          if (key >= sg.hi || key + BLOCK <= sg.lo) return 1.f;  // no key of it is seen
+          const int page = table[key / P];
+          return page < 0 || page >= p.cache.num_pages ? 1.f : block_scale(of_values ? a.sc.v : a.sc.k, page, key % P, sg.head);
+        };
+        float next = 1.f;
+        if constexpr (FP8) next = fetch(sg.u0);
+        if (in > 0) {  // the first are being fetched
+          const uint16_t* const q =
+              static_cast<const uint16_t*>(p.q.ptr) + (int64_t)sg.row0 * p.q.b_stride + (int64_t)(sg.head * g) * p.q.h_stride;
+          for (int r = lane; r < sg.ntok * g; r += 32) {
+            const uint16_t* const src = q + (int64_t)(r / g) * p.q.b_stride + (int64_t)(r % g) * p.q.h_stride;
+            for (int ch = 0; ch < D; ch += 64) prefetch_l2(src + ch);
+          }
+        }
+        if constexpr (FP8) {
+          for (int u = sg.u0; u < sg.u1; u += 2, ++pairs) {
+            const float x = next;
+            next = fetch(u + 2);
+            const uint32_t st = pairs % SCALES;
+            alive = warp_wait(&sh.scale_empty[st], (pairs / SCALES + 1) & 1);
+            if (!alive) break;
+            UnitScales& us = sh.scales[st][lane >> 4];
+            if (of_values) {
+              us.log_value[b] = log2f(x);
+              us.inv_value[b] = 1.f / x;
+            } else {
+              us.key[b] = x;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.scale_full[st]);
+          }
         }
       }
     } else if (warp == PRODUCT_WARP) {
@@ -963,111 +767,6 @@ __global__ void __launch_bounds__(Shape<D, FP8>::THREADS, 1)
         tc_commit_w(&sh.drain);
         mbar_drain_bounded(&sh.drain, 0);
       }
-    } else if constexpr (FP8) {
-      if (warp == SCALE_WARP) {
-        // ---- the scales of the CTA's units, two units at a time (16 lanes each: keys' blocks, then values'), and the
-        // next two on their way meanwhile
-        uint32_t n = 0;
-        const int P = p.cache.page_size, b = lane & (BLOCKS - 1);
-        const bool values = (lane & BLOCKS) != 0;
-        const kda_page_scales& from = values ? a.sc.v : a.sc.k;
-        for (uint32_t in = 0; alive; ++in) {
-          const uint32_t slot = in % RING;
-          alive = warp_wait(&sh.seg_full[slot], (in / RING) & 1);
-          if (!alive) break;
-          const Segment sg = sh.seg[slot];
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.seg_empty[slot]);
-          if (sg.ntok < 0) break;
-          const int32_t* const table = p.table + (int64_t)sg.request * p.table_stride;
-          auto fetch = [&](int u0) {
-            const int u = u0 + (lane >> 4);
-            if (u >= sg.u1) return 1.f;
-            const int key = u * UNIT + b * BLOCK;
-            if (key >= sg.hi || key + BLOCK <= sg.lo) return 1.f;  // no key of it is seen
-            const int page = table[key / P];
-            return page < 0 || page >= p.cache.num_pages ? 1.f : block_scale(from, page, key % P, sg.head);
-          };
-          float next = fetch(sg.u0);
-          for (int u = sg.u0; alive && u < sg.u1; u += 2) {
-            const float x = next;
-            next = fetch(u + 2);
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              if (!alive || u + half >= sg.u1) break;
-              const uint32_t st = n % SCALES;
-              alive = warp_wait(&sh.scale_empty[st], (n / SCALES + 1) & 1);
-              if (!alive) break;
-              if (lane >> 4 == half) {
-                if (!values) {
-                  sh.scales[st].key[b] = x;
-                } else {
-                  sh.scales[st].log_value[b] = log2f(x);
-                  sh.scales[st].inv_value[b] = 1.f / x;
-                }
-              }
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&sh.scale_full[st]);
-              ++n;
-            }
-          }
-        }
-      } else {
-        // ---- values from codes to fp16, which holds them exactly, in the layout of the product: 16 codes of a key a lane.
-        // Keys that are not in use become zeros: their weights are zero, but zero times what lies there need not be.
-        uint32_t n = 0;
-        for (uint32_t in = 0; alive; ++in) {
-          const uint32_t slot = in % RING;
-          alive = warp_wait(&sh.seg_full[slot], (in / RING) & 1);
-          if (!alive) break;
-          const int ntok = sh.seg[slot].ntok, u0 = sh.seg[slot].u0, u1 = sh.seg[slot].u1, lo = sh.seg[slot].lo, hi = sh.seg[slot].hi;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.seg_empty[slot]);
-          if (ntok < 0) break;
-          for (int u = u0; u < u1; ++u, ++n) {
-            const uint32_t rs = n % S::R_STAGES, vs = n % S::V_STAGES;
-            alive = warp_wait(&sh.r_full[rs], (n / S::R_STAGES) & 1) && warp_wait(&sh.v_empty[vs], (n / S::V_STAGES + 1) & 1);
-            if (!alive) break;
-            const uint8_t* const src = smem + S::R0 + rs * S::CODE_BYTES;
-            uint8_t* const dst = smem + S::V0 + vs * S::TILE_BYTES;
-            const int first = lo - u * UNIT, last = hi - u * UNIT;
-            constexpr int CHUNKS = D / 16, ROUNDS8 = UNIT * CHUNKS / 32, GROUP = 4;
-#pragma unroll 1
-            for (int k = warp - CONVERT_WARP; k < ROUNDS8; k += GROUP * CONVERT_WARPS) {
-              uint4 z[GROUP];
-#pragma unroll
-              for (int i = 0; i < GROUP; ++i) {
-                const int x = (k + i * CONVERT_WARPS) * 32 + lane;
-                z[i] = make_uint4(0, 0, 0, 0);
-                if (x < UNIT * CHUNKS && x / CHUNKS >= first && x / CHUNKS < last)
-                  z[i] = *reinterpret_cast<const uint4*>(src + x * 16);
-              }
-#pragma unroll
-              for (int i = 0; i < GROUP; ++i) {
-                const int x = (k + i * CONVERT_WARPS) * 32 + lane;
-                if (x >= UNIT * CHUNKS) continue;
-                const uint32_t row = x / CHUNKS, c = x % CHUNKS;
-                const uint4 h0 = make_uint4(codes_to_f16x2(z[i].x), codes_to_f16x2(z[i].x >> 16), codes_to_f16x2(z[i].y),
-                                            codes_to_f16x2(z[i].y >> 16));
-                const uint4 h1 = make_uint4(codes_to_f16x2(z[i].z), codes_to_f16x2(z[i].z >> 16), codes_to_f16x2(z[i].w),
-                                            codes_to_f16x2(z[i].w >> 16));
-                // the second half of a row's lanes store their second chunk first, so that eight neighbours meet eight banks
-                const uint32_t flip = c >> 2;
-                uint8_t* const at = dst + (c >> 2) * (TILE * 128) + row * 128;
-                const uint32_t ch = (2 * c) & 7;
-                *reinterpret_cast<uint4*>(at + (((ch + flip) ^ (row & 7)) << 4)) = flip ? h1 : h0;
-                *reinterpret_cast<uint4*>(at + (((ch + 1 - flip) ^ (row & 7)) << 4)) = flip ? h0 : h1;
-              }
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(&sh.v_full[vs]);
-              mbar_arrive(&sh.r_empty[rs]);
-            }
-          }
-        }
-      }
     }
     if (!alive && lane == 0 && p.error_word) atomicOr(p.error_word, KDA_ERR_TIMEOUT);
     __syncwarp();
@@ -1079,7 +778,7 @@ __global__ void __launch_bounds__(Shape<D, FP8>::THREADS, 1)
     // A reference m is in units of the scores, or (FP8) their log2: times to_log2 it is log2, times to_ln ln.
     const float to_log2 = FP8 ? 1.f : c, to_ln = FP8 ? 0.6931471805599453f : p.scale;
     uint32_t seen_s = 0, runs = 0;  // scores waited for; ends of runs
-    uint32_t units_before = 0;      // FP8: the CTA's units before this run
+    uint32_t pairs_before = 0;      // FP8: pairs of units before this run
     bool alive = true;
     auto div_g = [&](int row) { return (int)((uint32_t)row * a.inv_group >> 16); };
     // Where a thread stands is worked out anew for each part of a run: kept over the units, it would cost them registers.
@@ -1102,40 +801,6 @@ __global__ void __launch_bounds__(Shape<D, FP8>::THREADS, 1)
       const int tk = div_g(r);
       return (int64_t)tk * (int)b_stride + (int64_t)(r - tk * g) * (int)h_stride;
     };
-    // FP8: a query x becomes hi + lo, two E4M3 numbers of x 2^-e with the head's largest in (224, 448]. bf16's eight bits
-    // are four in each, exact down to 2^-2 (2^-9 of the largest or more); below, lo is off by half the subnormals' step,
-    // 2^-10, less than 2^-17 of the largest.
-    auto put_codes = [&](uint4 z, bool there, int r, int ch, uint8_t* tile, bool both) {
-      const uint32_t words[4] = {z.x, z.y, z.z, z.w};
-      float x[8], top = 0.f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) unpack_bf16x2(words[j], x[2 * j], x[2 * j + 1]);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[j]));
-#pragma unroll
-      for (int o = D / 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const int e = top > 0.f ? max(row_exponent(top), -100) : 0;
-      const float down = top < INFINITY ? pow2f(-e) : __uint_as_float(0x7fc00000u);  // an infinite query: NaN
-      uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float u = x[2 * j] * down, w = x[2 * j + 1] * down;
-        const uint32_t h = f32x2_to_e4m3x2(pk2(u, w));
-        float hu, hw;
-        upk2(e4m3x2_to_f32x2(h), hu, hw);
-        hi[j >> 1] |= h << (16 * (j & 1));
-        lo[j >> 1] |= f32x2_to_e4m3x2(pk2(u - hu, w - hw)) << (16 * (j & 1));
-      }
-      if (!there) return;
-      uint8_t* const at = tile + code_chunk<D>(r, ch >> 1) + (ch & 1) * 8;
-      *reinterpret_cast<uint2*>(at) = make_uint2(hi[0], hi[1]);
-      *reinterpret_cast<uint2*>(at + S::CODE_BYTES) = make_uint2(lo[0], lo[1]);
-      if (ch == 0) {
-        const float up = pow2f(e);
-        sh.m1[t][r] = up;
-        if (both) sh.m1[1 - t][r] = up;
-      }
-    };
     // The queries of a run: a group's tile, or its half of the tile that both share.
     auto fetch_q = [&](const Segment& n) {
       const Place me = place();
@@ -1146,11 +811,14 @@ __global__ void __launch_bounds__(Shape<D, FP8>::THREADS, 1)
                                  (int64_t)(n.head * g) * p.q.h_stride + me.ch * 8;
       uint8_t* const qs = smem + (n.dual && t ? S::Q1 : S::Q0) + me.at + from * 128;
       if constexpr (FP8) {
-#pragma unroll 1
-        for (int k0 = 0; from + k0 * ROWS_A_ROUND < to; k0 += 4) {  // the same for the whole warp
-          uint4 z[4];
+        uint8_t* const codes = smem + (n.dual && t ? S::Q1 : S::Q0);
+        // N rounds at a time; the same for the whole warp
+        auto rounds = [&](auto count, int k0) {
+          constexpr int N = decltype(count)::value;
+          uint4 z[N];
+          int e[N];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < N; ++k) {
             const int r = from + me.row + (k0 + k) * ROWS_A_ROUND;
             z[k] = make_uint4(0, 0, 0, 0);
             if (r >= to) continue;
@@ -1158,18 +826,34 @@ __global__ void __launch_bounds__(Shape<D, FP8>::THREADS, 1)
             if (a.q_wide) {
               z[k] = *reinterpret_cast<const uint4*>(src);
             } else {
-              uint32_t e[4];
+              uint32_t x[4];
 #pragma unroll
-              for (int j = 0; j < 4; ++j) e[j] = (uint32_t)src[2 * j] | ((uint32_t)src[2 * j + 1] << 16);
-              z[k] = make_uint4(e[0], e[1], e[2], e[3]);
+              for (int j = 0; j < 4; ++j) x[j] = (uint32_t)src[2 * j] | ((uint32_t)src[2 * j + 1] << 16);
+              z[k] = make_uint4(x[0], x[1], x[2], x[3]);
             }
           }
+          query_exponents<N, D / 8>(z, e);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < N; ++k) {
             const int r = from + me.row + (k0 + k) * ROWS_A_ROUND;
-            put_codes(z[k], r < to, r, me.ch, smem + (n.dual && t ? S::Q1 : S::Q0), !n.dual);
+            uint2 hi, lo;
+            query_codes(z[k], e[k], hi, lo);
+            if (r >= to) continue;
+            uint8_t* const at = codes + code_chunk<D>(r, me.ch >> 1) + (me.ch & 1) * 8;
+            *reinterpret_cast<uint2*>(at) = hi;
+            *reinterpret_cast<uint2*>(at + S::CODE_BYTES) = lo;
+            if (me.ch == 0) {
+              const float up = query_up(e[k]);
+              sh.m1[t][r] = up;
+              if (!n.dual) sh.m1[1 - t][r] = up;
+            }
           }
-        }
+        };
+        int k0 = 0;
+#pragma unroll 1
+        for (; from + (k0 + 4) * ROWS_A_ROUND < to; k0 += 8) rounds(std::integral_constant<int, 8>(), k0);
+#pragma unroll 1
+        for (; from + k0 * ROWS_A_ROUND < to; ++k0) rounds(std::integral_constant<int, 1>(), k0);
       } else if (a.q_wide) {  // asynchronously, all rounds in flight
 #pragma unroll 4
         for (int k = 0; k < ROUNDS; ++k) {
@@ -1239,9 +923,27 @@ __global__ void __launch_bounds__(Shape<D, FP8>::THREADS, 1)
       const int step = dual ? 1 : 2;
       int units = 0;
       for (int u = sg.u0 + (dual ? 0 : t); u < sg.u1; u += step) {
+        // FP8: what the unit's scales give is made ready while its scores are still being formed
+        const uint32_t of_run = (uint32_t)(u - sg.u0), pair_of = pairs_before + of_run / 2;
+        float f[FP8 ? BLOCKS : 1], log_value[FP8 ? BLOCKS : 1];
+        if constexpr (FP8) {
+          if (!dual || of_run % 2 == 0) alive = alive && warp_wait(&sh.scale_full[pair_of % SCALES], (pair_of / SCALES) & 1);
+          if (!alive) break;
+          const UnitScales& us = sh.scales[pair_of % SCALES][of_run % 2];
+#pragma unroll
+          for (int b = 0; b < BLOCKS; b += 4) {
+            const float4 key = ld_shared4(us.key + b), lv = ld_shared4(us.log_value + b);
+            f[b] = query_scale * key.x;
+            f[b + 1] = query_scale * key.y;
+            f[b + 2] = query_scale * key.z;
+            f[b + 3] = query_scale * key.w;
+            log_value[b] = lv.x;
+            log_value[b + 1] = lv.y;
+            log_value[b + 2] = lv.z;
+            log_value[b + 3] = lv.w;
+          }
+        }
         alive = alive && warp_wait(&sh.s_full[t], seen_s & 1);
-        const uint32_t unit = units_before + (uint32_t)(u - sg.u0);
-        if constexpr (FP8) alive = alive && warp_wait(&sh.scale_full[unit % SCALES], (unit / SCALES) & 1);
         if (!alive) break;
         if (warp_valid) {
           tc_fence_after();
@@ -1284,17 +986,17 @@ __global__ void __launch_bounds__(Shape<D, FP8>::THREADS, 1)
           uint32_t wa[16];
           if constexpr (FP8) {
             // y = f s is a score in log2 units, f its block's factor; weights times value scales are exp2(y + log2 vs - m)
-            const UnitScales& us = sh.scales[unit % SCALES];
             float top = -INFINITY;
 #pragma unroll
             for (int b = 0; b < BLOCKS; ++b) {
-              float t0 = __uint_as_float(s[b * BLOCK]), t1 = __uint_as_float(s[b * BLOCK + 1]);
+              const uint32_t* const x = s + b * BLOCK;
+              float t0 = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1])), t1 = fmaxf(__uint_as_float(x[2]), __uint_as_float(x[3]));
 #pragma unroll
-              for (int j = 2; j < BLOCK; j += 4) {
-                t0 = max3(t0, __uint_as_float(s[b * BLOCK + j]), __uint_as_float(s[b * BLOCK + j + 1]));
-                if (j + 2 < BLOCK) t1 = max3(t1, __uint_as_float(s[b * BLOCK + j + 2]), __uint_as_float(s[b * BLOCK + j + 3]));
+              for (int j = 4; j < BLOCK; j += 4) {
+                t0 = max3(t0, __uint_as_float(x[j]), __uint_as_float(x[j + 1]));
+                t1 = max3(t1, __uint_as_float(x[j + 2]), __uint_as_float(x[j + 3]));
               }
-              top = fmaxf(top, fmaf(fmaxf(t0, t1), query_scale * us.key[b], us.log_value[b]));
+              top = fmaxf(top, fmaf(fmaxf(t0, t1), f[b], log_value[b]));
             }
             const bool grown = valid && top - m > LIFT + SLACK;  // m = -inf: any key (-inf less itself is no number)
             if (__builtin_expect(__any_sync(0xffffffffu, grown), 0)) {
@@ -1305,15 +1007,18 @@ __global__ void __launch_bounds__(Shape<D, FP8>::THREADS, 1)
             }
             const float base = m == -INFINITY ? 0.f : -m;
             uint64_t sum = 0;
+            const UnitScales& us = sh.scales[pair_of % SCALES][of_run % 2];
 #pragma unroll
-            for (int i = 0; i < UNIT; i += 32) {
+            for (int b0 = 0; b0 < BLOCKS; b0 += 4) {
+              const float4 lv = ld_shared4(us.log_value + b0), iv = ld_shared4(us.inv_value + b0);  // again: registers are short
+              const float logs[4] = {lv.x, lv.y, lv.z, lv.w}, invs[4] = {iv.x, iv.y, iv.z, iv.w};
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const int b = i / BLOCK + h;
-                block_weights(s + b * BLOCK, query_scale * us.key[b], base + us.log_value[b], us.inv_value[b], sum, wa + 8 * h);
+              for (int i = 0; i < 4; ++i) {
+                const int b = b0 + i;
+                block_weights(s + b * BLOCK, f[b], base + logs[i], invs[i], sum, wa + 8 * (b & 1));
+                if (b & 1) st16(s_addr + (b - 1) * (BLOCK / 2), wa);
+                if ((b + 1) * BLOCK == FIRST) give(0);
               }
-              st16(s_addr + i / 2, wa);
-              if (i + 32 == FIRST) give(0);
             }
             give(1);
             float l0, l1;
@@ -1357,13 +1062,16 @@ __global__ void __launch_bounds__(Shape<D, FP8>::THREADS, 1)
         }
         if constexpr (FP8) {
           __syncwarp();
-          if (lane == 0) mbar_arrive_n(&sh.scale_empty[unit % SCALES], dual ? 1 : 2);
+          const bool last = u + 1 == sg.u1;
+          // the pair's second unit, or its only one: where one group takes that, it arrives for both
+          if (lane == 0 && (!dual || last || of_run % 2 == 1))
+            mbar_arrive_n(&sh.scale_empty[pair_of % SCALES], !dual && last && of_run % 2 == 0 ? 2 : 1);
         }
         ++seen_s;
         ++units;
       }
 
-      units_before += (uint32_t)(sg.u1 - sg.u0);
+      pairs_before += (uint32_t)(sg.u1 - sg.u0 + 1) / 2;
 
       // ---- the end of the run
       const Place me = place();
@@ -1684,8 +1392,10 @@ cudaError_t launch_paged_attention_tc(const kda_attention_params& p, const kda_p
   CUtensorMap km, vm;
   const bool wide = p.cache.head_dim == 128;
   if (scales != nullptr) {
-    cudaError_t e = code_pages_tensor_map(p.cache.k, p.cache, a.box, true, &km);
-    if (e == cudaSuccess) e = code_pages_tensor_map(p.cache.v, p.cache, a.box, false, &vm);
+    const int rows = paged_attention_few_rows(p);
+    if (rows > 0) return launch_paged_attention_fp8_rows(p, *scales, rows, workspace, ctas, s);
+    cudaError_t e = code_pages_tensor_map(p.cache.k, p.cache, a.box, &km);
+    if (e == cudaSuccess) e = code_pages_tensor_map(p.cache.v, p.cache, a.box, &vm);
     if (e != cudaSuccess) return e;
     return wide ? launch_tc<128, true>(km, vm, a, ctas, s) : launch_tc<64, true>(km, vm, a, ctas, s);
   }

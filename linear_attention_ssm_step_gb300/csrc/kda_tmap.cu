@@ -171,8 +171,9 @@ cudaError_t pages_tensor_map(const kda_pages& g, const kda_paged_cache& c, int b
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorNotSupported;
 }
 
-// The same for codes of 8 bits, read in {head_dim, box, 1, 1} boxes: whole heads of `box` tokens.
-cudaError_t code_pages_tensor_map(const kda_pages& g, const kda_paged_cache& c, int box, bool swizzled, CUtensorMap* out) {
+// The same for codes of 8 bits, read in {head_dim, box, 1, 1} boxes: whole heads of `box` tokens, with the swizzle of their
+// rows' bytes.
+cudaError_t code_pages_tensor_map(const kda_pages& g, const kda_paged_cache& c, int box, CUtensorMap* out) {
   const EncodeTiledFn fn = encode_tiled();
   if (fn == nullptr) return cudaErrorNotSupported;
   const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.page_size, (cuuint64_t)c.num_heads,
@@ -181,10 +182,9 @@ cudaError_t code_pages_tensor_map(const kda_pages& g, const kda_paged_cache& c, 
   const cuuint64_t strides[3] = {(cuuint64_t)g.token_stride, (cuuint64_t)head, (cuuint64_t)page};
   const cuuint32_t boxes[4] = {(cuuint32_t)c.head_dim, (cuuint32_t)box, 1, 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
-  const CUtensorMapSwizzle swizzle = !swizzled ? CU_TENSOR_MAP_SWIZZLE_NONE
-                                     : c.head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+  const CUtensorMapSwizzle swizzle = c.head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
   const CUresult r = fn(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, g.ptr, dims, strides, boxes, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorNotSupported;
 }

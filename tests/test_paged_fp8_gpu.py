@@ -284,3 +284,33 @@ def test_attention_equals_oracle(dev, case):
     assert int(err.item()) == 0
     without, _ = a.run(dev, kda)
     assert torch.equal(out, without)
+
+
+FEW = [
+    # decode and verify steps: new, kv, heads that share a key (times Hkv), Hkv, page, window, order
+    ([1], [77], 4, 2, 16, 0, "thd"),
+    ([1] * 5, [1, 128, 129, 1000, 0], 1, 3, 64, 0, "thd"),
+    ([1] * 3, [3000, 5, 640], 2, 1, 128, 0, "htd"),
+    ([1] * 40, [17 * i % 700 for i in range(40)], 4, 2, 32, 0, "thd"),
+    ([1, 0, 1, 1], [9000, 0, 400, 4096], 8, 1, 64, 0, "thd"),      # cut between many CTAs
+    ([8, 8, 8], [1200, 8, 130], 3, 2, 32, 0, "htd"),
+    ([4, 4], [2, 300], 3, 2, 16, 0, "thd"),                        # rows that see no key
+    ([2, 2, 2], [500, 900, 40], 16, 1, 64, 100, "padded"),         # a window
+    ([1, 1], [700, 300], 32, 1, 64, 1, "thd"),                     # a row sees itself alone
+    ([1, 30, 1, 1, 2, 1, 1, 1], [200, 700, 64, 1, 333, 90, 128, 127], 6, 2, 64, 0, "thd"),  # ragged
+    ([1] * 200, [5 + i for i in range(200)], 7, 1, 16, 0, "thd"),
+]
+
+
+@pytest.mark.parametrize("D", [128, 64])
+@pytest.mark.parametrize("case", range(len(FEW)))
+def test_attention_of_few_rows_equals_oracle(dev, case, D):
+    new, kv, g, Hkv, page, window, order = FEW[case]
+    a = Attention(new, kv, g * Hkv, Hkv, D, page, window, order, seed=100 + case, q_spread=0.5).poison()
+    err = err_word(dev)
+    work = kda.paged_attention_workspace(D, dev)
+    out, lse = a.run(dev, kda, workspace=work, error_word=err)
+    a.check(out, lse)
+    assert int(err.item()) == 0
+    again, lse2 = a.run(dev, kda, workspace=work)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
