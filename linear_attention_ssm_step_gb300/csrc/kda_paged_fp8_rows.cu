@@ -39,8 +39,10 @@ constexpr int RING = 4;    // segments the walking warp may be ahead
 constexpr int LEAD = 2;    // what an item costs beside its units, in units
 constexpr int SCALES = 4;  // pairs of units whose scales are held
 constexpr int BLOCK = KDA_FP8_SCALE_TOKENS, BLOCKS = UNIT / BLOCK;
-constexpr float LIFT = 6.f, SLACK = 2.f;  // log2 of the largest weight when the reference is set; its growth until the next
+constexpr float LIFT = 4.f, SLACK = 4.f;  // log2 of the largest weight when the reference is set; its growth until the next
 constexpr float LOG2E = 1.4426950408889634f;
+constexpr float NOTHING = -1e30f;  // the reference of a row that has seen no key: below any score, and no infinity, so that
+                                   // differences to it are numbers
 
 template <int D, int R>
 struct Shape {
@@ -51,7 +53,8 @@ struct Shape {
   static constexpr uint32_t Q_BYTES = NS * D, P_BYTES = NP * UNIT;
   static constexpr uint32_t K0 = 0, V0 = K0 + STAGES * UNIT_BYTES;
   static constexpr uint32_t Q0 = V0 + STAGES * UNIT_BYTES, P0 = Q0 + 2 * Q_BYTES;
-  static constexpr uint32_t END = P0 + 2 * P_BYTES;
+  static constexpr uint32_t RAW0 = P0 + 2 * P_BYTES;            // queries as they come (head_dim 64)
+  static constexpr uint32_t END = RAW0 + (D == 64 ? R * 128 : 0);
   static constexpr uint32_t S_COLS = NS, COLS = 2 * NS + NP;
   static constexpr uint32_t TMEM = COLS <= 64 ? 64 : COLS <= 128 ? 128 : 256;
 };
@@ -70,6 +73,7 @@ struct Shared {
   Segment seg[RING];
   alignas(16) float q_scale[2][R];  // scale log2e times the power of two by which a row's query was brought down
   alignas(16) float top[4][R];      // a warp's maxima, or sums
+  alignas(16) float m[R];           // a run's references at its end
   int warp_sum[THREADS / 32];
   LineStart start;
   uint32_t tmem;
@@ -110,29 +114,90 @@ __device__ __forceinline__ void issue(uint32_t d, uint64_t a, uint64_t b, uint32
       : "memory");
 }
 
+// The weights' operand: 16 columns of O^T (bytes) of a key side by side, key after key, the next 16 columns 128 keys on. N is
+// contiguous, without a swizzle: leading byte offset, the next 8 keys; stride byte offset, the next 16 columns. A K step of
+// 32 keys adds 512 bytes. So a thread stores what it has of its key in whole 16 bytes (a byte a column and key, in rows of
+// keys, took 3 R stores: 32 verify requests of 24 rows 87.6 us).
+__device__ __forceinline__ uint64_t weight_desc(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(128u >> 4) << 16) | ((uint64_t)(UNIT * 16u >> 4) << 32) |
+         ((uint64_t)1u << 46);
+}
+
+__device__ __forceinline__ f32x2 add2(f32x2 x, f32x2 y) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
+
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t x, uint32_t y) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
   return r;
 }
 
-// N consecutive columns of this thread's lane, with the wait (N: 8, 16 or a multiple of 32).
+// N consecutive columns of this thread's lane, with the wait (N: 4, 8, 16, 32 or 64).
 template <int N>
 __device__ __forceinline__ void load_columns(uint32_t taddr, float (&out)[N]) {
-  if constexpr (N == 8) {
+  if constexpr (N == 4) {
+    uint32_t z[4];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];\n\ttcgen05.wait::ld.sync.aligned;"
+                 : "=r"(z[0]), "=r"(z[1]), "=r"(z[2]), "=r"(z[3])
+                 : "r"(taddr)
+                 : "memory");
+#pragma unroll
+    for (int j = 0; j < 4; ++j) out[j] = __uint_as_float(z[j]);
+  } else if constexpr (N == 8) {
     tmem_ld8(taddr, out);
   } else if constexpr (N == 16) {
     tmem_ld16(taddr, out);
   } else {
-    static_assert(N % 32 == 0, "");
+    static_assert(N == 32 || N == 64, "");
+    float lo[32], hi[32];
+    if constexpr (N == 64)
+      tmem_ld32x2(taddr, lo, hi);
+    else
+      tmem_ld32(taddr, lo);
 #pragma unroll
-    for (int i = 0; i < N; i += 32) {
-      float f[32];
-      tmem_ld32(taddr + i, f);
-#pragma unroll
-      for (int j = 0; j < 32; ++j) out[i + j] = f[j];
+    for (int j = 0; j < 32; ++j) {
+      out[j] = lo[j];
+      if constexpr (N == 64) out[32 + j] = hi[j];
     }
   }
+}
+
+template <int N>
+__device__ __forceinline__ void store_columns(uint32_t taddr, const float (&v)[N]) {
+  if constexpr (N == 32) {
+    tmem_st32(taddr, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      uint32_t z[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) z[j] = __float_as_uint(v[i + j]);
+      tmem_st4(taddr + i, z);
+    }
+  }
+}
+
+// Four columns at taddr, taddr + step and taddr + 2 step, with the wait.
+__device__ __forceinline__ void load_parts(uint32_t taddr, int step, float (&out)[3][4]) {
+  uint32_t z[3][4];
+#pragma unroll
+  for (int i = 0; i < 3; ++i)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(z[i][0]), "=r"(z[i][1]), "=r"(z[i][2]), "=r"(z[i][3])
+                 : "r"(taddr + i * step)
+                 : "memory");
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(z[0][0]), "+r"(z[0][1]), "+r"(z[0][2]), "+r"(z[0][3]), "+r"(z[1][0]), "+r"(z[1][1]), "+r"(z[1][2]),
+                 "+r"(z[1][3]), "+r"(z[2][0]), "+r"(z[2][1]), "+r"(z[2][2]), "+r"(z[2][3])
+               :
+               : "memory");
+#pragma unroll
+  for (int i = 0; i < 3; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) out[i][j] = __uint_as_float(z[i][j]);
 }
 
 // The sums (or maxima) over a warp's lanes of R values a lane: lane l is left with that of value l % R. Each step sends half
@@ -330,42 +395,41 @@ __global__ void __launch_bounds__(THREADS, 1)
       alive = warp_wait(&sh.q_empty[qb], (in / 2 + 1) & 1);
       if (!alive) break;
       {
+        // brought asynchronously, then turned into codes row by row in a loop that is not unrolled: once-a-run code is
+        // fetched anew each run. For head_dim 128 a row's codes go where its numbers lie.
         constexpr int LANES = D / 8, ROWS = 32 / LANES;  // lanes a row, rows a round
-        constexpr int AT_ONCE = R / ROWS < 8 ? R / ROWS : 8;
         const int rows = sg.ntok * g, ch = lane % LANES;
         const uint16_t* const qg =
             static_cast<const uint16_t*>(p.q.ptr) + (int64_t)sg.row0 * p.q.b_stride + (int64_t)(sg.head * g) * p.q.h_stride + ch * 8;
         uint8_t* const tile = smem + S::Q0 + qb * S::Q_BYTES;
+        auto raw = [&](int r) {
+          return D == 128 ? tile + (ch >> 3) * (R * 128) + r * 128 + (ch & 7) * 16 : smem + S::RAW0 + r * 128 + ch * 16;
+        };
+        for (int r = lane / LANES; r < rows; r += ROWS) {
+          const int tk = (int)((uint32_t)r * a.inv_group >> 16);
+          const uint16_t* const src = qg + (int64_t)tk * p.q.b_stride + (int64_t)(r - tk * g) * p.q.h_stride;
+          if (a.q_wide) {
+            copy_async16(raw(r), src);
+          } else {
+            uint32_t x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[k] = (uint32_t)src[2 * k] | ((uint32_t)src[2 * k + 1] << 16);
+            *reinterpret_cast<uint4*>(raw(r)) = make_uint4(x[0], x[1], x[2], x[3]);
+          }
+        }
+        copy_async_wait();
 #pragma unroll 1
-        for (int r0 = 0; r0 < R; r0 += ROWS * AT_ONCE) {
-          uint4 z[AT_ONCE];
-          int e[AT_ONCE];
-#pragma unroll
-          for (int i = 0; i < AT_ONCE; ++i) {
-            const int r = r0 + i * ROWS + lane / LANES;
-            z[i] = make_uint4(0, 0, 0, 0);
-            if (r >= rows) continue;
-            const int tk = (int)((uint32_t)r * a.inv_group >> 16);
-            const uint16_t* const src = qg + (int64_t)tk * p.q.b_stride + (int64_t)(r - tk * g) * p.q.h_stride;
-            if (a.q_wide) {
-              z[i] = *reinterpret_cast<const uint4*>(src);
-            } else {
-              uint32_t x[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) x[k] = (uint32_t)src[2 * k] | ((uint32_t)src[2 * k + 1] << 16);
-              z[i] = make_uint4(x[0], x[1], x[2], x[3]);
-            }
-          }
-          query_exponents<AT_ONCE, LANES>(z, e);
-#pragma unroll
-          for (int i = 0; i < AT_ONCE; ++i) {
-            const int r = r0 + i * ROWS + lane / LANES;
-            uint2 hi, lo;
-            query_codes(z[i], e[i], hi, lo);
-            *reinterpret_cast<uint2*>(tile + code_chunk<D>(r, ch >> 1) + (ch & 1) * 8) = hi;
-            *reinterpret_cast<uint2*>(tile + code_chunk<D>(R + r, ch >> 1) + (ch & 1) * 8) = lo;
-            if (ch == 0) sh.q_scale[qb][r] = p.scale * LOG2E * query_up(e[i]);
-          }
+        for (int r = lane / LANES; r < R; r += ROWS) {
+          uint4 z[1] = {make_uint4(0, 0, 0, 0)};
+          int e[1];
+          if (r < rows) z[0] = *reinterpret_cast<const uint4*>(raw(r));
+          query_exponents<1, LANES>(z, e);
+          uint2 hi, lo;
+          query_codes(z[0], e[0], hi, lo);
+          __syncwarp();  // the row's numbers are read
+          *reinterpret_cast<uint2*>(tile + code_chunk<D>(r, ch >> 1) + (ch & 1) * 8) = hi;
+          *reinterpret_cast<uint2*>(tile + code_chunk<D>(R + r, ch >> 1) + (ch & 1) * 8) = lo;
+          if (ch == 0) sh.q_scale[qb][r] = p.scale * LOG2E * query_up(e[0]);
         }
       }
       fence_proxy_async_smem();
@@ -392,18 +456,18 @@ __global__ void __launch_bounds__(THREADS, 1)
   } else if (warp == PRODUCT_WARP) {
     // ---- the products: a unit's scores one unit ahead of its values, over the ends of runs
     const uint32_t base = smem_addr(smem), tm = uniform(tmem);
-    constexpr uint32_t M128 = 128u >> 4, F32 = 1u << 4, A_MN_MAJOR = 1u << 15;
+    constexpr uint32_t M128 = 128u >> 4, F32 = 1u << 4, MN_MAJOR = 3u << 15;  // of A and B
     constexpr uint32_t IDESC_S = F32 | ((uint32_t)S::NS >> 3 << 17) | (M128 << 24);
-    constexpr uint32_t IDESC_O = F32 | A_MN_MAJOR | ((uint32_t)S::NP >> 3 << 17) | ((uint32_t)D >> 4 << 24);
+    constexpr uint32_t IDESC_O = F32 | MN_MAJOR | ((uint32_t)S::NP >> 3 << 17) | ((uint32_t)D >> 4 << 24);
     uint32_t n = 0;          // units whose scores have been issued
     uint32_t fresh = 0;      // the last of them begins a run
     auto values = [&](uint32_t m) {
       const uint32_t st = m % S::STAGES, buf = m & 1;
       if (!warp_wait(&sh.v_full[st], (m / S::STAGES) & 1) || !warp_wait(&sh.p_full[buf], (m / 2) & 1)) return false;
       tc_fence_after();
-      issue<UNIT / 32, 32 * D / 16, 2>(tm + 2 * S::S_COLS, code_desc<D>(base + S::V0 + st * S::UNIT_BYTES),
-                                       sw128_desc(base + S::P0 + buf * S::P_BYTES), IDESC_O, fresh, smem_addr(&sh.p_done[buf]),
-                                       smem_addr(&sh.v_empty[st]), 0u);
+      issue<UNIT / 32, 32 * D / 16, 32>(tm + 2 * S::S_COLS, code_desc<D>(base + S::V0 + st * S::UNIT_BYTES),
+                                        weight_desc(base + S::P0 + buf * S::P_BYTES), IDESC_O, fresh, smem_addr(&sh.p_done[buf]),
+                                        smem_addr(&sh.v_empty[st]), 0u);
       return true;
     };
     for (uint32_t in = 0; alive; ++in) {
@@ -455,70 +519,83 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int u0 = sg.u0, u1 = sg.u1, ntok = sg.ntok, pos0 = sg.pos0, rows = ntok * g;
       // every row sees the keys [all_lo, all_hi)
       const int all_lo = first_key(pos0 + ntok - 1, window), all_hi = pos0 + 1;
-      float m[R], l[R];
+      f32x2 down[R / 2], l[R / 2];  // -m and l of two rows each
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        m[r] = -INFINITY;
-        l[r] = 0.f;
+      for (int r = 0; r < R; r += 2) {
+        down[r / 2] = pk2(-NOTHING, -NOTHING);
+        l[r / 2] = pk2(0.f, 0.f);
       }
       for (int u = u0; u < u1; ++u, ++n) {
         const uint32_t buf = n & 1, of_run = (uint32_t)(u - u0), pair_of = pairs_before + of_run / 2;
         if (of_run % 2 == 0) alive = alive && warp_wait(&sh.scale_full[pair_of % SCALES], (pair_of / SCALES) & 1);
         alive = alive && warp_wait(&sh.s_full[buf], (n / 2) & 1);
-        float y[R];
+        f32x2 y[R / 2];  // two rows each
         if (alive) {  // a warp whose wait gave up stays with the group to its next vote
           tc_fence_after();
           const UnitScales& us = sh.scales[pair_of % SCALES][of_run % 2];
           const float f = us.key[x / BLOCK], lv = us.log_value[x / BLOCK];
-          float s[R == 4 ? 8 : S::NS];
+          float s[2 * R];
           load_columns(tmem + buf * S::S_COLS + lane_base, s);
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh.s_empty[buf]);
+          const f32x2 f2 = pk2(f, f), lv2 = pk2(lv, lv);
 #pragma unroll
           for (int r = 0; r < R; r += 4) {
             const float4 q = *reinterpret_cast<const float4*>(&sh.q_scale[qb][r]);
-            const float qs[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) y[r + i] = fmaf(s[r + i] + s[R + r + i], qs[i] * f, lv);
+            y[r / 2] = fma2(add2(pk2(s[r], s[r + 1]), pk2(s[R + r], s[R + r + 1])), mul2(pk2(q.x, q.y), f2), lv2);
+            y[r / 2 + 1] = fma2(add2(pk2(s[r + 2], s[r + 3]), pk2(s[R + r + 2], s[R + r + 3])), mul2(pk2(q.z, q.w), f2), lv2);
           }
         }
         bool grown = !alive;
         const int key = u * UNIT + x;
         if (__builtin_expect((u + 1) * UNIT > all_hi || u * UNIT < all_lo, 0)) {
 #pragma unroll
-          for (int r = 0; r < R; ++r) {
-            const int pos = pos0 + (int)((uint32_t)r * a.inv_group >> 16);
-            if (r < rows && (key > pos || key < first_key(pos, window))) y[r] = -INFINITY;
+          for (int r = 0; r < R; r += 2) {
+            float two[2];
+            upk2(y[r / 2], two[0], two[1]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int pos = pos0 + (int)((uint32_t)(r + i) * a.inv_group >> 16);
+              if (r + i < rows && (key > pos || key < first_key(pos, window))) two[i] = -INFINITY;
+            }
+            y[r / 2] = pk2(two[0], two[1]);
           }
         }
+        float over = -INFINITY;  // the largest log2 of a weight
 #pragma unroll
-        for (int r = 0; r < R; ++r) grown |= y[r] - m[r] > LIFT + SLACK;  // m = -inf: any key (-inf less itself is no number)
+        for (int r = 0; r < R; r += 2) {
+          float d0, d1;
+          upk2(add2(y[r / 2], down[r / 2]), d0, d1);
+          over = max3(over, d0, d1);
+        }
+        grown |= over > LIFT + SLACK;
         if (bar_any(1, SOFTMAX_THREADS, grown)) {
           float v[R];
 #pragma unroll
-          for (int r = 0; r < R; ++r) v[r] = y[r];
+          for (int r = 0; r < R; r += 2) upk2(y[r / 2], v[r], v[r + 1]);
           const float mine = fold<R, true>(v);
           if (lane < R) sh.top[warp][lane] = mine;
           if (bar_any(2, SOFTMAX_THREADS, !alive)) {
             alive = false;
             break;
           }
-          float fade[R];
+          f32x2 fade[R / 2];
 #pragma unroll
-          for (int r = 0; r < R; r += 4) {
-            const float4 t0 = *reinterpret_cast<const float4*>(&sh.top[0][r]), t1 = *reinterpret_cast<const float4*>(&sh.top[1][r]);
-            const float4 t2 = *reinterpret_cast<const float4*>(&sh.top[2][r]), t3 = *reinterpret_cast<const float4*>(&sh.top[3][r]);
-            const float tops[4] = {fmaxf(fmaxf(t0.x, t1.x), fmaxf(t2.x, t3.x)), fmaxf(fmaxf(t0.y, t1.y), fmaxf(t2.y, t3.y)),
-                                   fmaxf(fmaxf(t0.z, t1.z), fmaxf(t2.z, t3.z)), fmaxf(fmaxf(t0.w, t1.w), fmaxf(t2.w, t3.w))};
+          for (int r = 0; r < R; r += 2) {
+            float down0[2], fade0[2];
+            upk2(down[r / 2], down0[0], down0[1]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const bool moves = tops[i] - m[r + i] > LIFT + SLACK;
-              const float to = moves ? tops[i] - LIFT : m[r + i];
-              fade[r + i] = moves ? ex2(m[r + i] - to) : 1.f;
-              m[r + i] = to;
-              l[r + i] *= fade[r + i];
+            for (int i = 0; i < 2; ++i) {
+              const float top = fmaxf(fmaxf(sh.top[0][r + i], sh.top[1][r + i]), fmaxf(sh.top[2][r + i], sh.top[3][r + i]));
+              const bool moves = top + down0[i] > LIFT + SLACK;
+              const float to = moves ? LIFT - top : down0[i];
+              fade0[i] = moves ? ex2(to - down0[i]) : 1.f;
+              down0[i] = to;
             }
+            down[r / 2] = pk2(down0[0], down0[1]);
+            fade[r / 2] = pk2(fade0[0], fade0[1]);
+            l[r / 2] = mul2(l[r / 2], fade[r / 2]);
           }
           if (of_run > 0) {  // O^T, once the product before is done
             alive = warp_wait(&sh.p_done[1 - buf], ((n - 1) / 2) & 1);
@@ -526,29 +603,11 @@ __global__ void __launch_bounds__(THREADS, 1)
               tc_fence_after();
 #pragma unroll 1
               for (int part = 0; part < 3; ++part) {
-                if constexpr (R == 4) {
-                  uint32_t o[4];
-                  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];\n\ttcgen05.wait::ld.sync.aligned;"
-                               : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
-                               : "r"(o_addr + part * 4)
-                               : "memory");
+                float o[R];
+                load_columns(o_addr + part * R, o);
 #pragma unroll
-                  for (int r = 0; r < 4; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * fade[r]);
-                  tmem_st4(o_addr + part * 4, o);
-                } else {
-#pragma unroll
-                  for (int r = 0; r < R; r += 8) {
-                    float o[8];
-                    tmem_ld8(o_addr + part * R + r, o);
-                    uint32_t z[4];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                      for (int i = 0; i < 4; ++i) z[i] = __float_as_uint(o[4 * h + i] * fade[r + 4 * h + i]);
-                      tmem_st4(o_addr + part * R + r + 4 * h, z);
-                    }
-                  }
-                }
+                for (int r = 0; r < R; r += 2) upk2(mul2(pk2(o[r], o[r + 1]), fade[r / 2]), o[r], o[r + 1]);
+                store_columns(o_addr + part * R, o);
               }
               tmem_st_wait();
             }
@@ -558,23 +617,26 @@ __global__ void __launch_bounds__(THREADS, 1)
         alive = alive && warp_wait(&sh.p_done[buf], (n / 2 + 1) & 1);
         if (!alive) continue;
         const float iv = sh.scales[pair_of % SCALES][of_run % 2].inv_value[x / BLOCK];
-        uint8_t* const pt = smem + S::P0 + buf * S::P_BYTES + (x & 15);
-        const uint32_t chunk = (uint32_t)x >> 4;
+        uint32_t words[S::NP / 4] = {};  // the columns of this key, four a word
 #pragma unroll
         for (int r = 0; r < R; r += 2) {
-          const float p0 = ex2(y[r] - (m[r] == -INFINITY ? 0.f : m[r])), p1 = ex2(y[r + 1] - (m[r + 1] == -INFINITY ? 0.f : m[r + 1]));
-          l[r] = fmaf(p0, iv, l[r]);
-          l[r + 1] = fmaf(p1, iv, l[r + 1]);
+          float p0, p1;
+          upk2(add2(y[r / 2], down[r / 2]), p0, p1);
+          p0 = ex2(p0);
+          p1 = ex2(p1);
+          l[r / 2] = fma2(pk2(p0, p1), pk2(iv, iv), l[r / 2]);
           uint32_t rest = pack_f16x2(p0, p1);
 #pragma unroll
           for (int part = 0; part < 3; ++part) {
             const uint32_t c = f16x2_to_codes(rest);
-            const int row = part * R + r;
-            pt[row * UNIT + ((chunk ^ (row & 7)) << 4)] = (uint8_t)c;
-            pt[(row + 1) * UNIT + ((chunk ^ ((row + 1) & 7)) << 4)] = (uint8_t)(c >> 8);
+            words[(part * R + r) / 4] |= r % 4 ? c << 16 : c;
             if (part < 2) rest = mul_f16x2(sub_f16x2(rest, codes_to_f16x2(c)), 0x50005000u);  // 32
           }
         }
+        uint8_t* const pt = smem + S::P0 + buf * S::P_BYTES + x * 16;
+#pragma unroll
+        for (int i = 0; i < S::NP / 16; ++i)
+          *reinterpret_cast<uint4*>(pt + i * UNIT * 16) = make_uint4(words[4 * i], words[4 * i + 1], words[4 * i + 2], words[4 * i + 3]);
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
@@ -591,9 +653,15 @@ __global__ void __launch_bounds__(THREADS, 1)
       {
         float v[R];
 #pragma unroll
-        for (int r = 0; r < R; ++r) v[r] = l[r];
+        for (int r = 0; r < R; r += 2) upk2(l[r / 2], v[r], v[r + 1]);
         const float mine = fold<R, false>(v);
         if (lane < R) sh.top[warp][lane] = mine;
+#pragma unroll
+        for (int r = 0; r < R; r += 2) {  // the same in all threads
+          float d0, d1;
+          upk2(down[r / 2], d0, d1);
+          if (x == 0) *reinterpret_cast<float2*>(&sh.m[r]) = make_float2(-d0, -d1);
+        }
       }
       if (bar_any(2, SOFTMAX_THREADS, !alive)) {
         alive = false;
@@ -616,34 +684,22 @@ __global__ void __launch_bounds__(THREADS, 1)
       auto part_o = [&](int id) { return a.parts + (size_t)id * a.slot_floats; };
       auto part_ml = [&](int id) { return reinterpret_cast<float2*>(part_o(id) + R * D); };
       const int my_slot = sg.part == 0 ? 2 * cta + 1 : 2 * cta;
-      // m is the same in all threads: thread r stores that of row r
-#pragma unroll
-      for (int r0 = 0; r0 < R; r0 += 4) {
-        if (r0 >= rows) break;
+#pragma unroll 1
+      for (int r0 = 0; r0 < rows; r0 += 4) {
         float o[3][4];
-#pragma unroll
-        for (int part = 0; part < 3; ++part) {
-          uint32_t z[4];
-          asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(z[0]), "=r"(z[1]), "=r"(z[2]), "=r"(z[3])
-                       : "r"(o_addr + part * R + r0)
-                       : "memory");
-          asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(z[0]), "+r"(z[1]), "+r"(z[2]), "+r"(z[3]) : : "memory");
-#pragma unroll
-          for (int i = 0; i < 4; ++i) o[part][i] = __uint_as_float(z[i]);
-        }
+        load_parts(o_addr + r0, R, o);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = r0 + i;
+          if (r >= rows) break;
           const float sum = (sh.top[0][r] + sh.top[1][r]) + (sh.top[2][r] + sh.top[3][r]);
           const float value = fmaf(fmaf(o[2][i], 0.03125f, o[1][i]), 0.03125f, o[0][i]);
-          if (r >= rows) continue;
           if (direct) {
             if (has_d) *out_at(r) = float_to_bf16_bits(sees_none(r) ? 0.f : value * rcp(sum));
-            if (x == r && p.lse != nullptr) put_lse(r, m[r], sum);
+            if (x == r && p.lse != nullptr) put_lse(r, sh.m[r], sum);
           } else {
             if (has_d) part_o(my_slot)[r * D + d] = value;
-            if (x == r) part_ml(my_slot)[r] = make_float2(m[r], sum);
+            if (x == r) part_ml(my_slot)[r] = make_float2(sh.m[r], sum);
           }
         }
       }
@@ -658,53 +714,46 @@ __global__ void __launch_bounds__(THREADS, 1)
           __threadfence();
         }
         bar_sync(2, SOFTMAX_THREADS);
-        if (sh.last_part) {  // the last to arrive joins the parts, in their order, four rows of four parts at a time
+        if (sh.last_part) {  // the last to arrive joins the parts, in their order: four dimensions of a row a thread
           __threadfence();
+          constexpr int LANES = D / 4;
+          const int d4 = x % LANES * 4;
 #pragma unroll 1
-          for (int r0 = 0; r0 < rows; r0 += 4) {
-            float mm[4], ll[4], acc[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              mm[i] = -INFINITY;
-              ll[i] = acc[i] = 0.f;
-            }
+          for (int r = x / LANES; r < rows; r += SOFTMAX_THREADS / LANES) {
+            float mm = -INFINITY, ll = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
             for (int q = 0; q < sg.parts; q += 4) {
-              float2 z[4][4];
-              float v[4][4];
+              float2 z[4];
+              float4 v[4];
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 const bool on = q + k < sg.parts;
                 const int id = slot_of(on ? q + k : q);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const bool there = on && r0 + i < rows;
-                  z[k][i] = there ? __ldcg(part_ml(id) + r0 + i) : make_float2(-INFINITY, 0.f);
-                  v[k][i] = there && has_d ? __ldcg(part_o(id) + (r0 + i) * D + d) : 0.f;
-                }
+                z[k] = __ldcg(part_ml(id) + r);
+                v[k] = __ldcg(reinterpret_cast<const float4*>(part_o(id) + r * D + d4));
+                if (!on) z[k].x = -INFINITY;
               }
+              const float top = fmaxf(fmaxf(mm, fmaxf(z[0].x, z[1].x)), fmaxf(z[2].x, z[3].x));
+              const float f = ex2(mm - top);  // a reference is a number: NOTHING, or of scores that are no infinity
+              ll *= f;
+              acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float top = fmaxf(fmaxf(mm[i], fmaxf(z[0][i].x, z[1][i].x)), fmaxf(z[2][i].x, z[3][i].x));
-                const float mb = top == -INFINITY ? 0.f : top, f = ex2(mm[i] - mb);
-                ll[i] *= f;
-                acc[i] *= f;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const float weight = ex2(z[k][i].x - mb);
-                  ll[i] = fmaf(z[k][i].y, weight, ll[i]);
-                  acc[i] = fmaf(v[k][i], weight, acc[i]);
-                }
-                mm[i] = top;
+              for (int k = 0; k < 4; ++k) {
+                const float weight = ex2(z[k].x - top);
+                if (q + k >= sg.parts) break;
+                ll = fmaf(z[k].y, weight, ll);
+                acc = make_float4(fmaf(v[k].x, weight, acc.x), fmaf(v[k].y, weight, acc.y), fmaf(v[k].z, weight, acc.z),
+                                  fmaf(v[k].w, weight, acc.w));
               }
+              mm = top;
             }
+            const float iv = sees_none(r) ? 0.f : rcp(ll);
+            uint16_t* const dst = out_at(r) - d + d4;
+            const float f4[4] = {acc.x, acc.y, acc.z, acc.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int r = r0 + i;
-              if (r >= rows) continue;
-              if (has_d) *out_at(r) = float_to_bf16_bits(sees_none(r) ? 0.f : acc[i] * rcp(ll[i]));
-              if (x == 0 && p.lse != nullptr) put_lse(r, mm[i], ll[i]);
-            }
+            for (int i = 0; i < 4; ++i) dst[i] = float_to_bf16_bits(sees_none(r) ? 0.f : f4[i] * iv);
+            if (d4 == 0 && p.lse != nullptr) put_lse(r, mm, ll);
           }
         }
       }

@@ -123,7 +123,20 @@ __device__ __forceinline__ bool bar_any(uint32_t id, uint32_t count, bool x) {
   return any != 0;
 }
 
+// 16 bytes from global to shared memory, asynchronously (both 16-byte aligned); the wait for all of this thread's.
+__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // ---------------------------------------------------------------- numbers
+
+// The largest of three (a NaN among them is passed over).
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
 
 __device__ __forceinline__ float ex2(float x) {
   float y;

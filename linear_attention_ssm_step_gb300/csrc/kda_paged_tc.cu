@@ -60,7 +60,7 @@ constexpr int SOFTMAX_THREADS = 256;
 // Which of the SM's four schedulers (warp mod 4) has which of them: with the loads on 1, beside softmax warps 1 and 5,
 // verify and decode steps take 54.6 and 193.6 us, on 0 57.2 and 195.0; chunks 561 against 560.
 constexpr int PRODUCT_WARP = 8, LOAD_WARP = 9, WALK_WARP = 10, AHEAD_WARP = 11;
-constexpr int CONVERT_WARP = 12, CONVERT_WARPS = 4, CONVERT_REGS = 40;  // of a cache in 8 bits
+constexpr int CONVERT_WARP = 12, CONVERT_WARPS = 4, CONVERT_REGS = 32;  // of a cache in 8 bits
 constexpr int FIRST = 96;   // keys of a unit whose weights are handed over first, while the others' are formed
 constexpr int RING = 4;  // segments the walking warp may be ahead
 // What an item costs beside its units (its queries, its end), in units: each item takes LEAD + its units of the line. A
@@ -74,9 +74,9 @@ constexpr int BLOCK = KDA_FP8_SCALE_TOKENS, BLOCKS = UNIT / BLOCK;  // keys a sc
 template <int D, bool FP8>
 struct Shape {
   // Registers a thread after the split: 256 x 208 + 128 x 88 = 384 x 168, what the block launches with; with the warps of
-  // a cache in 8 bits 256 x 208 + 128 x 56 + 128 x 40 = 512 x 128.
+  // a cache in 8 bits 256 x 216 + 128 x 48 + 128 x 32 = 512 x 128.
   static constexpr int THREADS = FP8 ? 512 : 384;
-  static constexpr int SOFTMAX_REGS = 208, OTHER_REGS = FP8 ? 56 : 88;
+  static constexpr int SOFTMAX_REGS = FP8 ? 216 : 208, OTHER_REGS = FP8 ? 48 : 88;
   static constexpr int K_STAGES = D == 128 ? 3 : 4;
   static constexpr int V_STAGES = D == 128 ? 2 : 4;
   static constexpr int R_STAGES = !FP8 ? 0 : D == 128 ? 3 : 4;  // units of values as they are in the cache
@@ -87,7 +87,10 @@ struct Shape {
   static constexpr uint32_t K0 = 2 * TILE_BYTES;
   static constexpr uint32_t R0 = K0 + K_STAGES * KEY_BYTES;
   static constexpr uint32_t V0 = R0 + R_STAGES * CODE_BYTES;
-  static constexpr uint32_t END = V0 + V_STAGES * TILE_BYTES;
+  // Where queries are brought in 16 bits: into their own place, but for codes of head_dim 64, whose rows lie otherwise.
+  static constexpr bool OWN_RAW = FP8 && D == 64;
+  static constexpr uint32_t RAW0 = OWN_RAW ? V0 + V_STAGES * TILE_BYTES : Q0, RAW1 = RAW0 + TILE_BYTES;
+  static constexpr uint32_t END = V0 + V_STAGES * TILE_BYTES + (OWN_RAW ? 2 * TILE_BYTES : 0);
 };
 
 // A unit's scales by blocks: of the keys, and log2 and reciprocal of the values'.
@@ -179,13 +182,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
   return r;
 }
-// The largest of three (a NaN among them is passed over).
-__device__ __forceinline__ float max3(float x, float y, float z) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
-  return r;
-}
-
 // -m c twice; 0 for a row that has seen no key.
 __device__ __forceinline__ uint64_t reference(float m, float c) {
   const float base = m == -INFINITY ? 0.f : -m * c;
@@ -302,12 +298,6 @@ __device__ __forceinline__ void issue_values_last(uint32_t d, uint32_t a, uint64
       "r"(a), "l"(b), "r"(idesc), "r"(done), "r"(free)
       : "memory");
 }
-
-// 16 bytes from global to shared memory, asynchronously (both 16-byte aligned); the wait for all of this thread's.
-__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 __device__ __forceinline__ void prefetch_l2(const void* src) { asm volatile("prefetch.global.L2 [%0];" ::"l"(src)); }
 
@@ -809,52 +799,8 @@ __global__ void __launch_bounds__(Shape<D, FP8>::THREADS, 1)
       const int to = min(min(n.ntok - tile0, tpt) * g, n.dual ? TILE : from + TILE / 2);
       const uint16_t* const qg = static_cast<const uint16_t*>(p.q.ptr) + (int64_t)(n.row0 + tile0) * p.q.b_stride +
                                  (int64_t)(n.head * g) * p.q.h_stride + me.ch * 8;
-      uint8_t* const qs = smem + (n.dual && t ? S::Q1 : S::Q0) + me.at + from * 128;
-      if constexpr (FP8) {
-        uint8_t* const codes = smem + (n.dual && t ? S::Q1 : S::Q0);
-        // N rounds at a time; the same for the whole warp
-        auto rounds = [&](auto count, int k0) {
-          constexpr int N = decltype(count)::value;
-          uint4 z[N];
-          int e[N];
-#pragma unroll
-          for (int k = 0; k < N; ++k) {
-            const int r = from + me.row + (k0 + k) * ROWS_A_ROUND;
-            z[k] = make_uint4(0, 0, 0, 0);
-            if (r >= to) continue;
-            const uint16_t* const src = qg + row_offset(r, p.q.b_stride, p.q.h_stride);
-            if (a.q_wide) {
-              z[k] = *reinterpret_cast<const uint4*>(src);
-            } else {
-              uint32_t x[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j) x[j] = (uint32_t)src[2 * j] | ((uint32_t)src[2 * j + 1] << 16);
-              z[k] = make_uint4(x[0], x[1], x[2], x[3]);
-            }
-          }
-          query_exponents<N, D / 8>(z, e);
-#pragma unroll
-          for (int k = 0; k < N; ++k) {
-            const int r = from + me.row + (k0 + k) * ROWS_A_ROUND;
-            uint2 hi, lo;
-            query_codes(z[k], e[k], hi, lo);
-            if (r >= to) continue;
-            uint8_t* const at = codes + code_chunk<D>(r, me.ch >> 1) + (me.ch & 1) * 8;
-            *reinterpret_cast<uint2*>(at) = hi;
-            *reinterpret_cast<uint2*>(at + S::CODE_BYTES) = lo;
-            if (me.ch == 0) {
-              const float up = query_up(e[k]);
-              sh.m1[t][r] = up;
-              if (!n.dual) sh.m1[1 - t][r] = up;
-            }
-          }
-        };
-        int k0 = 0;
-#pragma unroll 1
-        for (; from + (k0 + 4) * ROWS_A_ROUND < to; k0 += 8) rounds(std::integral_constant<int, 8>(), k0);
-#pragma unroll 1
-        for (; from + k0 * ROWS_A_ROUND < to; ++k0) rounds(std::integral_constant<int, 1>(), k0);
-      } else if (a.q_wide) {  // asynchronously, all rounds in flight
+      uint8_t* const qs = smem + (n.dual && t ? S::RAW1 : S::RAW0) + me.at + from * 128;
+      if (a.q_wide) {  // asynchronously, all rounds in flight
 #pragma unroll 4
         for (int k = 0; k < ROUNDS; ++k) {
           const int r = from + me.row + k * ROWS_A_ROUND;
@@ -871,6 +817,30 @@ __global__ void __launch_bounds__(Shape<D, FP8>::THREADS, 1)
 #pragma unroll
           for (int j = 0; j < 4; ++j) e[j] = (uint32_t)src[2 * j] | ((uint32_t)src[2 * j + 1] << 16);
           *reinterpret_cast<uint4*>(qs + k * (ROWS_A_ROUND * 128)) = make_uint4(e[0], e[1], e[2], e[3]);
+        }
+      }
+      if constexpr (FP8) {  // to codes, each thread the chunks that it has brought
+        uint8_t* const codes = smem + (n.dual && t ? S::Q1 : S::Q0) + (me.ch & 1) * 8;
+#pragma unroll 1
+        for (int k = 0; from + k * ROWS_A_ROUND < to; ++k) {  // the same for the whole warp
+          const int r = from + me.row + k * ROWS_A_ROUND;
+          uint4 z[1] = {make_uint4(0, 0, 0, 0)};
+          int e[1];
+          if (r < to) z[0] = *reinterpret_cast<const uint4*>(qs + k * (ROWS_A_ROUND * 128));
+          query_exponents<1, D / 8>(z, e);
+          uint2 hi, lo;
+          query_codes(z[0], e[0], hi, lo);
+          __syncwarp();  // the row's chunks are read: for head_dim 128 its codes go where they lie
+          if (r < to) {
+            uint8_t* const at = codes + code_chunk<D>(r, me.ch >> 1);
+            *reinterpret_cast<uint2*>(at) = hi;
+            *reinterpret_cast<uint2*>(at + S::CODE_BYTES) = lo;
+            if (me.ch == 0) {
+              const float up = query_up(e[0]);
+              sh.m1[t][r] = up;
+              if (!n.dual) sh.m1[1 - t][r] = up;
+            }
+          }
         }
       }
       fence_proxy_async_smem();

@@ -13,7 +13,9 @@ Bounds (derived, element-wise):
       - a weight times its key's value scale is rounded to fp16, not bf16, before it meets v: 2^-11 A. They are kept so
         that the largest of a row is 2^6 or more, and fp16's subnormals round by 2^-25: 2^-31 of that largest for each
         key seen, times |code| <= 448, and a scale s has a code of 224 or more in its block, so |v| >= 224 s in it:
-        2^-30 max |v| each, 2^-29 with room;
+        2^-30 max |v| each, 2^-29 with room. For few rows the fp16 number goes on as three E4M3 numbers, each 2^5 below
+        the one before, the last off by half its subnormals' step: 2^-20 where the largest of a row is 2^4 or more, so
+        2^-24 instead of 2^-31, 2^-22 max |v| each with room;
       - on the tensor cores a query number below 2^-9 of its head's largest is off by 2^-17 of that: a score by
         2^-17 scale max_c |q_c| max_j sum_c |k_jc|. Added to e.
 """
@@ -132,7 +134,8 @@ class Attention:
         e = e + 2.0 ** -17 * self.scale * np.abs(f64(self.q)).max(-1) * np.abs(k).sum(-1).max(initial=0.0)
         sums = ((count + 64) * 2.0 ** -23)[:, None]
         rel = 2.0 ** -11 + 2 * e + 2.0 ** -21 + sums
-        small = (count * 2.0 ** -29 * np.abs(v).max(initial=0.0))[:, None, None]
+        few = -(-self.q.shape[0] // len(self.kv)) * (self.Hq // self.Hkv) <= 32
+        small = (count * 2.0 ** (-22 if few else -29) * np.abs(v).max(initial=0.0))[:, None, None]
         tol = rel[:, :, None] * A + 2.0 ** -8 * np.abs(out) + small + 1e-30
         safe = np.where(np.isfinite(lse), np.abs(lse), 0.0)
         return tol, e + sums + 2.0 ** -20 + 2.0 ** -22 * safe
