@@ -36,7 +36,7 @@ namespace {
 constexpr int THREADS = 256, SOFTMAX_THREADS = 128;
 constexpr int PRODUCT_WARP = 4, LOAD_WARP = 5, WALK_WARP = 6, AHEAD_WARP = 7;
 constexpr int RING = 4;    // segments the walking warp may be ahead
-constexpr int LEAD = 2;    // what an item costs beside its units, in units
+constexpr int LEAD = 3;    // what an item costs beside its units, in units
 constexpr int SCALES = 4;  // pairs of units whose scales are held
 constexpr int BLOCK = KDA_FP8_SCALE_TOKENS, BLOCKS = UNIT / BLOCK;
 constexpr float LIFT = 4.f, SLACK = 4.f;  // log2 of the largest weight when the reference is set; its growth until the next
@@ -368,7 +368,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   } else if (warp == AHEAD_WARP) {
     // ---- queries of the runs to come, as codes, and their units' scales, a pair of units at a time (16 lanes each: keys'
-    // blocks, then values'), the next pair on its way meanwhile
+    // blocks, then values'). Two pairs are on their way meanwhile, and the page numbers of a third: under a full load of
+    // memory the two trips of a scale take longer than a pair of units
     uint32_t pairs = 0;
     for (uint32_t in = 0; alive; ++in) {
       const uint32_t slot = in % RING;
@@ -381,15 +382,19 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int P = p.cache.page_size, b = lane & (BLOCKS - 1);
       const bool of_values = (lane & BLOCKS) != 0;
       const int32_t* const table = p.table + (int64_t)sg.request * p.table_stride;
-      auto fetch = [&](int u0) {
+      const kda_page_scales& of = of_values ? a.sc.v : a.sc.k;
+      auto page_of = [&](int u0) {  // -1: no key of this lane's block is seen, or the page is none
         const int u = u0 + (lane >> 4);
-        if (u >= sg.u1) return 1.f;
+        if (u >= sg.u1) return -1;
         const int key = u * UNIT + b * BLOCK;
-        if (key >= sg.hi || key + BLOCK <= sg.lo) return 1.f;  // no key of it is seen
-        const int page = table[key / P];
-        return page < 0 || page >= p.cache.num_pages ? 1.f : block_scale(of_values ? a.sc.v : a.sc.k, page, key % P, sg.head);
+        return key >= sg.hi || key + BLOCK <= sg.lo ? -1 : table[key / P];
       };
-      float next = fetch(sg.u0);
+      auto scale_of = [&](int u0, int page) {
+        return page < 0 || page >= p.cache.num_pages ? 1.f : block_scale(of, page, ((u0 + (lane >> 4)) * UNIT + b * BLOCK) % P, sg.head);
+      };
+      const int p0 = page_of(sg.u0), p1 = page_of(sg.u0 + 2);
+      int page = page_of(sg.u0 + 4);
+      float x0 = 1.f, x1 = 1.f;
 
       const uint32_t qb = in & 1;
       alive = warp_wait(&sh.q_empty[qb], (in / 2 + 1) & 1);
@@ -417,19 +422,28 @@ __global__ void __launch_bounds__(THREADS, 1)
             *reinterpret_cast<uint4*>(raw(r)) = make_uint4(x[0], x[1], x[2], x[3]);
           }
         }
+        x0 = scale_of(sg.u0, p0);
+        x1 = scale_of(sg.u0 + 2, p1);
         copy_async_wait();
+        constexpr int N = R / ROWS < 4 ? R / ROWS : 4;  // rounds at a time
 #pragma unroll 1
-        for (int r = lane / LANES; r < R; r += ROWS) {
-          uint4 z[1] = {make_uint4(0, 0, 0, 0)};
-          int e[1];
-          if (r < rows) z[0] = *reinterpret_cast<const uint4*>(raw(r));
-          query_exponents<1, LANES>(z, e);
-          uint2 hi, lo;
-          query_codes(z[0], e[0], hi, lo);
-          __syncwarp();  // the row's numbers are read
-          *reinterpret_cast<uint2*>(tile + code_chunk<D>(r, ch >> 1) + (ch & 1) * 8) = hi;
-          *reinterpret_cast<uint2*>(tile + code_chunk<D>(R + r, ch >> 1) + (ch & 1) * 8) = lo;
-          if (ch == 0) sh.q_scale[qb][r] = p.scale * LOG2E * query_up(e[0]);
+        for (int r0 = lane / LANES; r0 < R; r0 += N * ROWS) {
+          uint4 z[N];
+          int e[N];
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            z[i] = r0 + i * ROWS < rows ? *reinterpret_cast<const uint4*>(raw(r0 + i * ROWS)) : make_uint4(0, 0, 0, 0);
+          query_exponents<N, LANES>(z, e);
+          __syncwarp();  // the rows' numbers are read
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            const int r = r0 + i * ROWS;
+            uint2 hi, lo;
+            query_codes(z[i], e[i], hi, lo);
+            *reinterpret_cast<uint2*>(tile + code_chunk<D>(r, ch >> 1) + (ch & 1) * 8) = hi;
+            *reinterpret_cast<uint2*>(tile + code_chunk<D>(R + r, ch >> 1) + (ch & 1) * 8) = lo;
+            if (ch == 0) sh.q_scale[qb][r] = p.scale * LOG2E * query_up(e[i]);
+          }
         }
       }
       fence_proxy_async_smem();
@@ -437,8 +451,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (lane == 0) mbar_arrive(&sh.q_full[qb]);
 
       for (int u = sg.u0; u < sg.u1; u += 2, ++pairs) {
-        const float x = next;
-        next = fetch(u + 2);
+        const float x = x0;
+        x0 = x1;
+        x1 = scale_of(u + 4, page);
+        page = page_of(u + 6);
         const uint32_t st = pairs % SCALES;
         alive = warp_wait(&sh.scale_empty[st], (pairs / SCALES + 1) & 1);
         if (!alive) break;
@@ -705,9 +721,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       tc_fence_before();
       if (!direct) {
-        __threadfence();
         bar_sync(1, SOFTMAX_THREADS);
         if (tid == 0) {
+          __threadfence();  // of what the barrier has gathered
           const unsigned done = atomicAdd(&a.counters[sg.cta0], 1u);
           sh.last_part = done + 1 == (unsigned)sg.parts;
           if (sh.last_part) a.counters[sg.cta0] = 0;
@@ -715,33 +731,35 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         bar_sync(2, SOFTMAX_THREADS);
         if (sh.last_part) {  // the last to arrive joins the parts, in their order: four dimensions of a row a thread
-          __threadfence();
-          constexpr int LANES = D / 4;
+          constexpr int LANES = D / 4, AT_ONCE = 8;  // parts: a trip to memory takes 2000 cycles and more
           const int d4 = x % LANES * 4;
 #pragma unroll 1
           for (int r = x / LANES; r < rows; r += SOFTMAX_THREADS / LANES) {
             float mm = -INFINITY, ll = 0.f;
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-            for (int q = 0; q < sg.parts; q += 4) {
-              float2 z[4];
-              float4 v[4];
+            for (int q = 0; q < sg.parts; q += AT_ONCE) {
+              float2 z[AT_ONCE];
+              float4 v[AT_ONCE];
+              float top = mm;
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const bool on = q + k < sg.parts;
-                const int id = slot_of(on ? q + k : q);
-                z[k] = __ldcg(part_ml(id) + r);
-                v[k] = __ldcg(reinterpret_cast<const float4*>(part_o(id) + r * D + d4));
-                if (!on) z[k].x = -INFINITY;
+              for (int k = 0; k < AT_ONCE; ++k) {
+                z[k] = make_float2(-INFINITY, 0.f);
+                v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (q + k < sg.parts) {
+                  const int id = slot_of(q + k);
+                  z[k] = __ldcg(part_ml(id) + r);
+                  v[k] = __ldcg(reinterpret_cast<const float4*>(part_o(id) + r * D + d4));
+                }
               }
-              const float top = fmaxf(fmaxf(mm, fmaxf(z[0].x, z[1].x)), fmaxf(z[2].x, z[3].x));
+#pragma unroll
+              for (int k = 0; k < AT_ONCE; ++k) top = fmaxf(top, z[k].x);
               const float f = ex2(mm - top);  // a reference is a number: NOTHING, or of scores that are no infinity
               ll *= f;
               acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
+              for (int k = 0; k < AT_ONCE; ++k) {
                 const float weight = ex2(z[k].x - top);
-                if (q + k >= sg.parts) break;
                 ll = fmaf(z[k].y, weight, ll);
                 acc = make_float4(fmaf(v[k].x, weight, acc.x), fmaf(v[k].y, weight, acc.y), fmaf(v[k].z, weight, acc.z),
                                   fmaf(v[k].w, weight, acc.w));
