@@ -63,7 +63,7 @@ typedef struct {
  * Rows of one block must follow one another in the call, row t + 1 at
  * slots[t] + 1 (kda_paged_plan's rows of a request do); where rows of a block
  * come in any other order, or a slot twice, that block's codes and scales are
- * undefined. k is turned with sines and cosines good to 2^-20, far below the
+ * undefined. At most 2^30 rows a call. k is turned with sines and cosines good to 2^-20, far below the
  * rounding of a code; q as in kda_rope_append.
  */
 kda_status kda_rope_append_fp8(const kda_rope_params* p, const kda_paged_scales* s, void* stream);

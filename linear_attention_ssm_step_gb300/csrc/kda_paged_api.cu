@@ -189,6 +189,7 @@ kda_status rope_append(const char* call, const kda_rope_params* p, bool fp8, con
   if (fp8 && (s = check_scales(sc, p->cache)) != KDA_OK) return s;
   const int D = p->cache.head_dim, Hkv = p->cache.num_heads;
   if (p->num_tokens < 0) return fail(KDA_EINVAL, "num_tokens = %d is negative", p->num_tokens);
+  if (fp8 && p->num_tokens > 1 << 30) return fail(KDA_EUNSUPPORTED, "num_tokens = %d is above 2^30", p->num_tokens);
   if (p->num_q_heads < 1) return fail(KDA_EINVAL, "num_q_heads = %d is below 1", p->num_q_heads);
   if (p->num_q_heads > 16384) return fail(KDA_EUNSUPPORTED, "num_q_heads = %d is above 16384", p->num_q_heads);
   if (p->rotary_dim < 0 || p->rotary_dim > D || p->rotary_dim % 2)

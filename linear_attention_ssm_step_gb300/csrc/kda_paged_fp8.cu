@@ -15,48 +15,23 @@ constexpr int SCALE_LOW = -40, SCALE_HIGH = 40;  // exponents of the scales
 
 // ---------------------------------------------------------------- append
 //
-// One CTA per row turns the row's queries as kda_rope_append_kernel does. Keys
-// and values go by the block: a scale needs the largest magnitude of all the
-// rows that fall into one block (a run: at most 16 rows that follow one
-// another), so a warp takes one side and head of a whole run. The run's CTAs
-// share its 2 x heads such tasks evenly, CTA i of n taking every n-th: a chunk
-// has as much to do in each CTA as a decode step, whose runs are single rows.
-// Every CTA finds its run itself, from the slots of the 15 rows on either side.
-//
-// A task reads its rows once, into registers as bf16 (two a lane and row for
-// head_dim 128), goes over them for the largest magnitude, and again to encode.
-// Keys are turned in both passes, by sines and cosines of all the run's rows
-// that the CTA's threads leave in shared memory; these are the fast ones (off
-// by 2^-20, where a code rounds by 2^-4), since each of up to 16 CTAs forms
-// them. Other head sizes, and rows off their alignment, read the rows twice.
+// A CTA per row turns its queries, as kda_rope_append_kernel does. Keys and
+// values, in CTAs beside those, go by the block: a scale needs the largest
+// magnitude of all the rows that fall into one block (a run: at most 16 rows that
+// follow one another). A CTA has the runs that begin among its `span` rows, found
+// from the positions and slots of these and the 15 behind; a task is one side and
+// head of a run, and a warp takes it whole, reads its rows once, into registers as
+// bf16 (two a lane and row for head_dim 128), goes over them for the largest
+// magnitude, and again to encode. Keys are turned in both passes, by sines and
+// cosines that the CTA forms once for all heads, in shared memory, by the fast
+// functions (off by 2^-20, where a code rounds by 2^-4). Other head sizes, and
+// rows off their alignment, read the rows twice.
 
-constexpr int APPEND_THREADS = 128, APPEND_WARPS = APPEND_THREADS / 32;
-
-// A run: rows t0 .. t0 + n - 1, at tokens first .. of a block; i: this CTA's row of it.
+// A run: rows t0 .. t0 + n - 1, at tokens first .. of a block.
 struct BlockRun {
-  int t0, n, i;
+  int t0, n;
   int page, block, first;
 };
-
-// The run of row t, whose slot is in the cache. Called by whole warps.
-__device__ __forceinline__ BlockRun block_run(const kda_rope_params& p, int t, int slot) {
-  const int lane = threadIdx.x & 31, P = p.cache.page_size;
-  BlockRun r;
-  r.page = slot / P;
-  const int place = slot - r.page * P;
-  r.block = place / SCALE_TOKENS;
-  const int off = place - r.block * SCALE_TOKENS, size = min(SCALE_TOKENS, P - r.block * SCALE_TOKENS);
-  const int d = lane - 15;  // -15 .. 16; 16 is never in the block
-  bool in = false;
-  if (off + d >= 0 && off + d < size && (long long)t + d >= 0 && (long long)t + d < p.num_tokens)
-    in = p.positions[t + d] >= 0 && p.slots[t + d] == slot + d;
-  const uint32_t rows = __ballot_sync(0xffffffffu, in);  // bit 15 (row t) is set
-  r.i = __clz(~(rows << 17));                            // rows right before t
-  r.n = r.i + __ffs(~(rows >> 15)) - 1;
-  r.t0 = t - r.i;
-  r.first = off - r.i;
-  return r;
-}
 
 __device__ __forceinline__ float warp_max(float x) {
 #pragma unroll
@@ -76,8 +51,10 @@ __device__ __forceinline__ BlockScale new_scale(float top, bool earlier, float o
   const float need = pow2f(e);
   BlockScale b;
   b.scale = earlier ? fmaxf(old, need) : need;
-  b.inverse = 1.f / b.scale;  // exact for a power of two
-  b.again = earlier && need > old ? old / need : 0.f;
+  // 2^-e of a power of two 2^e, |e| < 127, by its exponent field (a division is a long subroutine)
+  auto inverse = [](float x) { return __uint_as_float((254u << 23) - (__float_as_uint(x) & 0x7f800000u)); };
+  b.inverse = inverse(b.scale);
+  b.again = earlier && need > old ? old * inverse(need) : 0.f;
   return b;
 }
 
@@ -86,51 +63,71 @@ __device__ __forceinline__ uint32_t encode4(const float* x, float inverse) {
          (f32x2_to_e4m3x2(pk2(x[2] * inverse, x[3] * inverse)) << 16);
 }
 
-// One side and head of a run, E consecutive elements a lane and row (32 E = head_dim).
+// One side and head of a run: where it lies.
+struct BlockTask {
+  const uint16_t* src;  // its first row
+  int64_t row_stride, token_stride;
+  uint8_t* block;       // codes of the block's first token
+  float* scale;
+  bool turned;
+};
+
+// The rows of a task, E consecutive elements a lane and row (32 E = head_dim), two a word.
 template <int E>
-__device__ __forceinline__ void append_wide(const kda_rope_params& p, const BlockRun& run, const uint16_t* src,
-                                            int64_t row_stride, uint8_t* block, int64_t token_stride, float* scale,
-                                            const float2 (*turn)[128], bool turned) {
-  const int lane = threadIdx.x & 31, half = p.rotary_dim >> 1;
-  constexpr int W = E / 2;  // words a row
-  using Codes = std::conditional_t<E == 4, uint32_t, uint16_t>;
-  const float old = run.first > 0 ? *scale : 0.f;
-  uint32_t raw[SCALE_TOKENS][W];
+struct RunRows {
+  uint32_t raw[SCALE_TOKENS][E / 2];
+  float old;  // the block's scale, where it has earlier tokens
+};
+
+template <int E>
+__device__ __forceinline__ void load_rows(const BlockRun& run, const BlockTask& k, RunRows<E>& z) {
+  const int lane = threadIdx.x & 31;
+  z.old = run.first > 0 ? *k.scale : 0.f;
 #pragma unroll
   for (int i = 0; i < SCALE_TOKENS; ++i) {
-    const uint16_t* const row = src + i * row_stride + lane * E;
-#pragma unroll
-    for (int w = 0; w < W; ++w) raw[i][w] = 0;
+    const uint16_t* const row = k.src + i * k.row_stride + lane * E;
+    uint2 x = make_uint2(0, 0);
     if (i < run.n) {
       if constexpr (E == 4)
-        *reinterpret_cast<uint2*>(raw[i]) = *reinterpret_cast<const uint2*>(row);
+        x = *reinterpret_cast<const uint2*>(row);
       else
-        raw[i][0] = *reinterpret_cast<const uint32_t*>(row);
+        x.x = *reinterpret_cast<const uint32_t*>(row);
     }
+    z.raw[i][0] = x.x;
+    if constexpr (E == 4) z.raw[i][1] = x.y;
   }
-  const bool mine = turned && lane * E < p.rotary_dim, lower = lane * E < half;
+}
+
+// table: sines and cosines of the run's rows, rotary_dim / 2 a row.
+template <int E>
+__device__ __forceinline__ void append_rows(const kda_rope_params& p, const BlockRun& run, const BlockTask& k,
+                                            const RunRows<E>& z, const float2* table) {
+  const int lane = threadIdx.x & 31, half = p.rotary_dim >> 1;
+  constexpr int W = E / 2;
+  using Codes = std::conditional_t<E == 4, uint32_t, uint16_t>;
+  const bool mine = k.turned && lane * E < p.rotary_dim, lower = lane * E < half;
   const int partner = !mine || p.interleaved ? lane : lower ? lane + half / E : lane - half / E;
   const int pair = p.interleaved ? lane * W : lower ? lane * E : lane * E - half;
   auto row_values = [&](int i, float (&x)[E]) {
 #pragma unroll
-    for (int w = 0; w < W; ++w) unpack_bf16x2(raw[i][w], x[2 * w], x[2 * w + 1]);
-    if (!turned) return;
-    const float2* const u = turn[i] + pair;
+    for (int w = 0; w < W; ++w) unpack_bf16x2(z.raw[i][w], x[2 * w], x[2 * w + 1]);
+    if (!k.turned) return;
+    const float2* const u = table + i * half + pair;
     if (p.interleaved) {
       if (!mine) return;
 #pragma unroll
       for (int w = 0; w < W; ++w) {
         const float a = x[2 * w], b = x[2 * w + 1];
-        x[2 * w] = a * u[w].x - b * u[w].y;
-        x[2 * w + 1] = b * u[w].x + a * u[w].y;
+        x[2 * w] = fmaf(a, u[w].x, -b * u[w].y);
+        x[2 * w + 1] = fmaf(b, u[w].x, a * u[w].y);
       }
     } else {
       float y[E];
 #pragma unroll
-      for (int w = 0; w < W; ++w) unpack_bf16x2(__shfl_sync(0xffffffffu, raw[i][w], partner), y[2 * w], y[2 * w + 1]);
+      for (int w = 0; w < W; ++w) unpack_bf16x2(__shfl_sync(0xffffffffu, z.raw[i][w], partner), y[2 * w], y[2 * w + 1]);
       if (!mine) return;
 #pragma unroll
-      for (int e = 0; e < E; ++e) x[e] = lower ? x[e] * u[e].x - y[e] * u[e].y : x[e] * u[e].x + y[e] * u[e].y;
+      for (int e = 0; e < E; ++e) x[e] = fmaf(x[e], u[e].x, lower ? -y[e] * u[e].y : y[e] * u[e].y);
     }
   };
   float top = 0.f;
@@ -142,44 +139,49 @@ __device__ __forceinline__ void append_wide(const kda_rope_params& p, const Bloc
 #pragma unroll
     for (int e = 0; e < E; ++e) top = fmaxf(top, fabsf(x[e]));
   }
-  const BlockScale b = new_scale(warp_max(top), run.first > 0, old);
-  uint8_t* const at = block + lane * E;
+  const BlockScale b = new_scale(warp_max(top), run.first > 0, z.old);
+  uint8_t* const at = k.block + lane * E;
   if (b.again > 0.f) {
-#pragma unroll 1
-    for (int j = 0; j < run.first; ++j) {
-      Codes* const c = reinterpret_cast<Codes*>(at + j * token_stride);
-      float x[4] = {};
-      e4m3x4_to_floats(*c, x);
-      *c = (Codes)encode4(x, b.again);
+    constexpr int AT_ONCE = 5;  // tokens a trip to memory: all 15 in three
+    for (int j0 = 0; j0 < run.first; j0 += AT_ONCE) {
+      Codes c[AT_ONCE];
+#pragma unroll
+      for (int j = 0; j < AT_ONCE; ++j)
+        if (j0 + j < run.first) c[j] = *reinterpret_cast<const Codes*>(at + (j0 + j) * k.token_stride);
+#pragma unroll
+      for (int j = 0; j < AT_ONCE; ++j) {
+        if (j0 + j >= run.first) break;
+        float four[4] = {};
+        e4m3x4_to_floats(c[j], four);
+        *reinterpret_cast<Codes*>(at + (j0 + j) * k.token_stride) = (Codes)encode4(four, b.again);
+      }
     }
   }
 #pragma unroll
   for (int i = 0; i < SCALE_TOKENS; ++i) {
     if (i >= run.n) break;
-    float x[E], z[4] = {};
+    float x[E], four[4] = {};
     row_values(i, x);
 #pragma unroll
-    for (int e = 0; e < E; ++e) z[e] = x[e];
-    *reinterpret_cast<Codes*>(at + (run.first + i) * token_stride) = (Codes)encode4(z, b.inverse);
+    for (int e = 0; e < E; ++e) four[e] = x[e];
+    *reinterpret_cast<Codes*>(at + (run.first + i) * k.token_stride) = (Codes)encode4(four, b.inverse);
   }
-  if (lane == 0) *scale = b.scale;
+  if (lane == 0) *k.scale = b.scale;
 }
 
-// The same for any head_dim and alignment, an element at a time.
-__device__ __forceinline__ void append_any(const kda_rope_params& p, const BlockRun& run, const uint16_t* src,
-                                           int64_t row_stride, uint8_t* block, int64_t token_stride, float* scale,
-                                           const float2 (*turn)[128], bool turned) {
+// A task for any head_dim and alignment, an element at a time.
+__device__ __forceinline__ void append_any(const kda_rope_params& p, const BlockRun& run, const BlockTask& k, const float2* table) {
   const int lane = threadIdx.x & 31, half = p.rotary_dim >> 1, D = p.cache.head_dim;
-  const float old = run.first > 0 ? *scale : 0.f;
+  const float old = run.first > 0 ? *k.scale : 0.f;
   auto value = [&](int i, int c) {
-    const uint16_t* const row = src + i * row_stride;
+    const uint16_t* const row = k.src + i * k.row_stride;
     const float x = bf16_bits_to_float(row[c]);
-    if (!turned || c >= p.rotary_dim) return x;
+    if (!k.turned || c >= p.rotary_dim) return x;
     const bool lower = p.interleaved ? c % 2 == 0 : c < half;
     const int step = p.interleaved ? 1 : half;
     const float y = bf16_bits_to_float(row[lower ? c + step : c - step]);
-    const float2 u = turn[i][p.interleaved ? c >> 1 : lower ? c : c - half];
-    return lower ? x * u.x - y * u.y : x * u.x + y * u.y;
+    const float2 u = table[i * half + (p.interleaved ? c >> 1 : lower ? c : c - half)];
+    return fmaf(x, u.x, lower ? -y * u.y : y * u.y);
   };
   float top = 0.f;
   for (int i = 0; i < run.n; ++i)
@@ -188,13 +190,13 @@ __device__ __forceinline__ void append_any(const kda_rope_params& p, const Block
   if (b.again > 0.f)
     for (int j = 0; j < run.first; ++j)
       for (int c = lane; c < D; c += 32) {
-        uint8_t* const code = block + j * token_stride + c;
+        uint8_t* const code = k.block + j * k.token_stride + c;
         *code = (uint8_t)f32x2_to_e4m3x2(pk2(e4m3_to_float(*code) * b.again, 0.f));
       }
   for (int i = 0; i < run.n; ++i)
     for (int c = lane; c < D; c += 32)
-      block[(run.first + i) * token_stride + c] = (uint8_t)f32x2_to_e4m3x2(pk2(value(i, c) * b.inverse, 0.f));
-  if (lane == 0) *scale = b.scale;
+      k.block[(run.first + i) * k.token_stride + c] = (uint8_t)f32x2_to_e4m3x2(pk2(value(i, c) * b.inverse, 0.f));
+  if (lane == 0) *k.scale = b.scale;
 }
 
 // Sine and cosine of a phase in 2^-64 turns, off by 2^-20 at most.
@@ -203,22 +205,23 @@ __device__ __forceinline__ float2 fast_turn(uint64_t phase, float mscale) {
   return make_float2(mscale * __cosf(angle), mscale * __sinf(angle));
 }
 
-template <int VEC, int E>
-__global__ void __launch_bounds__(APPEND_THREADS) kda_rope_append_fp8_kernel(kda_rope_params p, kda_paged_scales sc) {
-  __shared__ float2 turn[128];                                     // mscale (cos, sin) of this row's pairs
-  __shared__ __align__(16) float2 run_turn[SCALE_TOKENS][128];     // and of the run's rows
-  const int t = blockIdx.x, tid = threadIdx.x, warp = tid >> 5;
-  const int half = p.rotary_dim >> 1, D = p.cache.head_dim;
-  const int Hq = p.num_q_heads, Hkv = p.cache.num_heads;
-  const int per_head = (D + 2 * VEC - 1) / (2 * VEC), tasks = Hq * per_head;
-  earlier_work();
-  const int pos = p.positions[t], slot = p.slots[t];
-  const uint64_t freq = tid < half ? p.freqs[tid] : 0u;
+constexpr int APPEND_WARPS = 8;  // a CTA
+
+// The queries of row t.
+template <int VEC>
+__device__ __forceinline__ void turn_queries(const kda_rope_params& p, int t) {
+  __shared__ float2 turn[128];  // mscale (cos, sin) of pair i
+  const int tid = threadIdx.x, half = p.rotary_dim >> 1, D = p.cache.head_dim;
+  const int per_head = (D + 2 * VEC - 1) / (2 * VEC), tasks = p.num_q_heads * per_head;
+  const int pos = p.positions[t];
+  const uint64_t freq = tid < half ? p.freqs[tid] : 0u;  // half <= 128, the fewest threads
   const uint16_t* const qi = static_cast<const uint16_t*>(p.q.ptr) + (int64_t)t * p.q.b_stride;
+  uint16_t* const qo = static_cast<uint16_t*>(p.q_out) + (int64_t)t * p.q_out_b_stride;
   RopeTask<VEC> j;
   auto load = [&](int i) {
     const int h = i / per_head, c = i - h * per_head;
     j.src = qi + (int64_t)h * p.q.h_stride;
+    j.dst = qo + (int64_t)h * p.q_out_h_stride;
     j.c = c * VEC < half ? c * VEC : -1;
     j.a = 2 * c * VEC;
     j.b = j.a + VEC;
@@ -232,61 +235,129 @@ __global__ void __launch_bounds__(APPEND_THREADS) kda_rope_append_fp8_kernel(kda
     if (j.two) j.rb = load_run<VEC>(j.src + j.b);
   };
   if (tid < tasks) load(tid);  // asked for before the position is known
-
   if (pos < 0) return;
-  if (tid < half) {  // half <= 128 = APPEND_THREADS
+  if (tid < half) {
     const uint64_t phase = (uint64_t)(uint32_t)pos * freq;
     float sn, cs;
     sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &sn, &cs);
     turn[tid] = make_float2(p.mscale * cs, p.mscale * sn);
   }
-  const long long slots = (long long)p.cache.num_pages * p.cache.page_size;
-  const bool append = slot >= 0 && slot < slots;
-  if (!append && slot != -1 && tid == 0 && p.error_word) atomicOr(p.error_word, KDA_ERR_PAGES);
-  BlockRun run{};
-  if (append) {
-    run = block_run(p, t, slot);
-    if (run.i < Hkv)  // its first task is one of keys
-      for (int x = tid; x < run.n * half; x += APPEND_THREADS) {
-        const int i = x / half, c = x - i * half;
-        run_turn[i][c] = fast_turn((uint64_t)(uint32_t)p.positions[run.t0 + i] * p.freqs[c], p.mscale);
-      }
-  }
   __syncthreads();
-
-  uint16_t* const qo = static_cast<uint16_t*>(p.q_out) + (int64_t)t * p.q_out_b_stride;
   for (int i = tid; i < tasks;) {
     if (j.c >= 0) turn_task<VEC>(j, turn, p.interleaved);
-    j.dst = qo + (int64_t)(i / per_head) * p.q_out_h_stride;
     store_run<VEC>(j.dst + j.a, j.ra);
     if (j.two) store_run<VEC>(j.dst + j.b, j.rb);
-    i += APPEND_THREADS;
+    i += blockDim.x;
     if (i < tasks) load(i);
   }
-  if (!append) return;
-  for (int x = run.i + run.n * warp; x < 2 * Hkv; x += run.n * APPEND_WARPS) {
-    const bool keys = x < Hkv;
-    const int h = keys ? x : x - Hkv;
-    const kda_view& v = keys ? p.k : p.v;
-    const kda_pages& g = keys ? p.cache.k : p.cache.v;
-    const kda_page_scales& f = keys ? sc.k : sc.v;
-    const uint16_t* const src =
-        static_cast<const uint16_t*>(v.ptr) + (int64_t)run.t0 * v.b_stride + (int64_t)h * v.h_stride;
-    uint8_t* const block = static_cast<uint8_t*>(g.ptr) + (int64_t)run.page * g.page_stride +
-                           (int64_t)run.block * SCALE_TOKENS * g.token_stride + (int64_t)h * g.head_stride;
-    float* const scale = f.ptr + (int64_t)run.page * f.page_stride + (int64_t)run.block * f.block_stride +
-                         (int64_t)h * f.head_stride;
-    if constexpr (E > 0)
-      append_wide<E>(p, run, src, v.b_stride, block, g.token_stride, scale, run_turn, keys && half > 0);
-    else
-      append_any(p, run, src, v.b_stride, block, g.token_stride, scale, run_turn, keys && half > 0);
+}
+
+// E: elements of a key or value row a lane takes at a time, 0 for any row; VEC: of a query's. The first `blocks` x `splits`
+// CTAs have keys and values, `splits` of them the tasks of the same runs in turn; those behind (if any) a row of queries each.
+template <int VEC, int E>
+__global__ void __launch_bounds__(APPEND_WARPS * 32, 2)
+    kda_rope_append_fp8_kernel(kda_rope_params p, kda_paged_scales sc, int span, int blocks, int splits) {
+  extern __shared__ __align__(16) float2 table[];  // [16][rotary_dim / 2]
+  __shared__ int positions[32];
+  earlier_work();
+  if ((int)blockIdx.x >= blocks * splits) {
+    turn_queries<VEC>(p, (int)blockIdx.x - blocks * splits);
+    return;
+  }
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int split = (int)blockIdx.x % splits;
+  const int half = p.rotary_dim >> 1, Hkv = p.cache.num_heads, P = p.cache.page_size;
+  // lane l has row t0 + l - 1: the row before this CTA's, its own, and those that their runs may reach to
+  const int t0 = (int)blockIdx.x / splits * span;
+  const long long near = (long long)t0 + lane - 1, slots = (long long)p.cache.num_pages * P;
+  int pos = -1, slot = -1;
+  if (near >= 0 && near < p.num_tokens) {
+    pos = p.positions[near];
+    slot = p.slots[near];
+  }
+  const bool own = lane >= 1 && lane <= span && near < p.num_tokens;
+  const bool bad = pos >= 0 && slot != -1 && (slot < 0 || slot >= slots);
+  if (bad && own && warp == 0 && split == 0 && p.error_word) atomicOr(p.error_word, KDA_ERR_PAGES);
+  if (pos < 0 || bad) slot = -1;
+  const int page = slot >= 0 ? slot / P : 0, off = slot >= 0 ? (slot - page * P) % SCALE_TOKENS : 0;
+  const int before = __shfl_up_sync(0xffffffffu, slot, 1);  // by all lanes
+  const bool follows = lane > 0 && slot > 0 && off > 0 && before == slot - 1;
+  const uint32_t follow = __ballot_sync(0xffffffffu, follows);
+  uint32_t starts = __ballot_sync(0xffffffffu, own && slot >= 0 && !follows);
+  if (warp == 0) positions[lane] = pos;
+  while (starts) {  // the same for the whole CTA
+    const int at = __ffs(starts) - 1;
+    starts &= starts - 1;
+    BlockRun run;
+    run.t0 = t0 + at - 1;
+    run.n = at == 31 ? 1 : __ffs(~(follow >> (at + 1)));  // `at` is at most 16, and a run at most 16 rows
+    run.page = __shfl_sync(0xffffffffu, page, at);
+    run.first = __shfl_sync(0xffffffffu, off, at);
+    run.block = (__shfl_sync(0xffffffffu, slot, at) - run.page * P) / SCALE_TOKENS;
+    auto task = [&](int x) {
+      const bool keys = x < Hkv;
+      const int h = keys ? x : x - Hkv;
+      const kda_view& v = keys ? p.k : p.v;
+      const kda_pages& g = keys ? p.cache.k : p.cache.v;
+      const kda_page_scales& f = keys ? sc.k : sc.v;
+      BlockTask k;
+      k.src = static_cast<const uint16_t*>(v.ptr) + (int64_t)run.t0 * v.b_stride + (int64_t)h * v.h_stride;
+      k.row_stride = v.b_stride;
+      k.block = static_cast<uint8_t*>(g.ptr) + (int64_t)run.page * g.page_stride +
+                (int64_t)run.block * SCALE_TOKENS * g.token_stride + (int64_t)h * g.head_stride;
+      k.token_stride = g.token_stride;
+      k.scale = f.ptr + (int64_t)run.page * f.page_stride + (int64_t)run.block * f.block_stride + (int64_t)h * f.head_stride;
+      k.turned = keys && half > 0;
+      return k;
+    };
+    int x = split * APPEND_WARPS + warp;
+    RunRows<E == 0 ? 2 : E> rows;
+    BlockTask k{};
+    if (x < 2 * Hkv) {
+      k = task(x);
+      if constexpr (E > 0) load_rows<E>(run, k, rows);  // on their way while the table is formed
+    }
+    __syncthreads();  // positions are there; the table of the run before is read
+    for (int y = tid; y < run.n * half; y += blockDim.x) {
+      const int i = y / half, c = y - i * half;
+      table[y] = fast_turn((uint64_t)(uint32_t)positions[at + i] * p.freqs[c], p.mscale);
+    }
+    __syncthreads();
+    while (x < 2 * Hkv) {
+      if constexpr (E > 0)
+        append_rows<E>(p, run, k, rows, table);
+      else
+        append_any(p, run, k, table);
+      x += APPEND_WARPS * splits;
+      if (x < 2 * Hkv) {
+        k = task(x);
+        if constexpr (E > 0) load_rows<E>(run, k, rows);
+      }
+    }
   }
 }
 
 cudaError_t launch_rope_append_fp8(const kda_rope_params& p, const kda_paged_scales& sc, bool q_wide, int lane_elems,
                                    cudaStream_t s) {
-  const dim3 grid((unsigned)p.num_tokens);
-  auto go = [&](auto kernel) { return launch_early(kernel, grid, APPEND_THREADS, 0, s, p, sc); };
+  // Up to 512 rows are mostly decode steps, whose rows may each be a run: a CTA per row, and the queries in the same launch
+  // (8192 rows so: 47.3 us). More are chunks, or so many rows that it does not matter: a CTA looks for runs in up to 16 rows,
+  // and the queries go ahead in a launch of kda_rope_append_kernel without keys and values, which needs half the registers:
+  // it runs at twice the occupancy, and this kernel is brought in while it ends.
+  const bool fused = p.num_tokens <= 512;
+  const int span = fused ? 1 : p.num_tokens < 16 * 512 ? (p.num_tokens + 511) / 512 : SCALE_TOKENS;
+  const int blocks = p.num_tokens / span + (p.num_tokens % span != 0), tasks = 2 * p.cache.num_heads;
+  // few runs: a task a warp
+  const int splits = p.num_tokens < 4096 && tasks > APPEND_WARPS ? (tasks + APPEND_WARPS - 1) / APPEND_WARPS : 1;
+  if (!fused) {
+    kda_rope_params q = p;
+    q.cache.num_heads = q.cache.num_pages = 0;
+    q.error_word = nullptr;
+    const cudaError_t e = launch_rope_append(q, q_wide, s);
+    if (e != cudaSuccess) return e;
+  }
+  const size_t smem = (size_t)SCALE_TOKENS * (p.rotary_dim / 2) * sizeof(float2);  // at most 16 KB
+  const dim3 grid((unsigned)(blocks * splits + (fused ? p.num_tokens : 0)));
+  auto go = [&](auto kernel) { return launch_early(kernel, grid, 32 * APPEND_WARPS, smem, s, p, sc, span, blocks, splits); };
   if (lane_elems == 4) return q_wide ? go(kda_rope_append_fp8_kernel<8, 4>) : go(kda_rope_append_fp8_kernel<1, 4>);
   if (lane_elems == 2) return q_wide ? go(kda_rope_append_fp8_kernel<8, 2>) : go(kda_rope_append_fp8_kernel<1, 2>);
   return q_wide ? go(kda_rope_append_fp8_kernel<8, 0>) : go(kda_rope_append_fp8_kernel<1, 0>);
