@@ -5,7 +5,8 @@ tokens in a step (chunks of prompts, decode tokens, or none).
 One step is: the page plan (kda_paged_plan), then layer by layer, on the packed
 rows of all requests,
   a KDA layer         projections, kda_prefill on the request's state slot
-  an attention layer  projections, kda_rope_append, kda_paged_attention
+  an attention layer  projections, kda_rope_append, kda_paged_attention, or on a
+                      cache in 8 bits kda_rope_append_fp8, kda_paged_attention_fp8
 each with an RMS norm before and a residual around it. Projections are plain
 torch matrix products with random weights: this module shows how the calls are
 used together, and is not a model.
@@ -22,9 +23,13 @@ HEAD_DIM = 128  # of KDA layers (the library's) and, here, of attention layers t
 
 class HybridLayers:
     def __init__(self, hidden=1024, layers="kkka", heads=8, kv_heads=2, requests=4, pages=256, page_size=64,
-                 max_tokens=4096, rope_base=10000.0, device="cuda", seed=0):
+                 max_tokens=4096, rope_base=10000.0, device="cuda", seed=0, cache_bits=16):
         """layers: one letter each, "k" KDA, "a" attention. requests: rows of the
-        block table and slots of the KDA state; max_tokens: longest request."""
+        block table and slots of the KDA state; max_tokens: longest request;
+        cache_bits: 16 (bf16) or 8 (E4M3 codes and scales) for keys and values."""
+        if cache_bits not in (8, 16):
+            raise ValueError(f"cache_bits must be 8 or 16, got {cache_bits}")
+        self.cache_bits = cache_bits
         self.hidden, self.layers, self.heads, self.kv_heads = hidden, layers, heads, kv_heads
         self.page_size, self.pages, self.device = page_size, pages, torch.device(device)
         gen = torch.Generator(device=self.device).manual_seed(seed)
@@ -46,9 +51,11 @@ class HybridLayers:
             else:
                 self.weights.append({"in": weight(hidden, (heads + 2 * kv_heads) * HEAD_DIM),
                                      "out": weight(heads * HEAD_DIM, hidden)})
-                # keys and values of a page side by side
-                self.memory.append(torch.zeros((pages, 2, page_size, kv_heads, HEAD_DIM), dtype=torch.bfloat16,
-                                               device=self.device))
+                if cache_bits == 8:  # k_codes, v_codes, k_scales, v_scales
+                    self.memory.append(kda.paged_fp8_cache(pages, page_size, kv_heads, HEAD_DIM, self.device))
+                else:  # keys and values of a page side by side
+                    self.memory.append(torch.zeros((pages, 2, page_size, kv_heads, HEAD_DIM), dtype=torch.bfloat16,
+                                                   device=self.device))
         int32 = {"dtype": torch.int32, "device": self.device}
         self.slots = torch.arange(requests, **int32)
         self.cached = torch.zeros(requests, **int32)
@@ -83,14 +90,32 @@ class HybridLayers:
                                       w["dt_bias"], error_word=self.error_word)
             else:
                 q, k, v = y.view(T, -1, D).split((H, self.kv_heads, self.kv_heads), dim=1)
-                k_cache, v_cache = memory[:, 0], memory[:, 1]
-                kda.kda_rope_append(q, k, v, plan.positions, plan.slots, self.freqs, k_cache, v_cache, q_out=q,
-                                    error_word=self.error_word)
-                out = kda.kda_paged_attention(q, k_cache, v_cache, self.block_table, plan.cu_new, plan.kv_len,
-                                              workspace=self.workspace, error_word=self.error_word)
+                if self.cache_bits == 8:
+                    append, attention, cache = kda.kda_rope_append_fp8, kda.kda_paged_attention_fp8, memory
+                else:
+                    append, attention, cache = kda.kda_rope_append, kda.kda_paged_attention, (memory[:, 0], memory[:, 1])
+                append(q, k, v, plan.positions, plan.slots, self.freqs, *cache, q_out=q, error_word=self.error_word)
+                out = attention(q, *cache, self.block_table, plan.cu_new, plan.kv_len, workspace=self.workspace,
+                                error_word=self.error_word)
             x = x + out.reshape(T, H * D) @ w["out"]
         self.cached, self.free_count = torch.where(admitted, plan.kv_len, self.cached), plan.free_count
         return x
+
+    def cached_rows(self, layer):
+        """Keys and values that an attention layer has cached, request after request: bf16 [sum of cached, kv_heads,
+        128] each, to be moved elsewhere or looked at."""
+        memory = self.memory[layer]
+        if self.layers[layer] != "a":
+            raise ValueError(f"layer {layer} is no attention layer")
+        lengths = self.cached.tolist()
+        total = sum(lengths)
+        if self.cache_bits == 8:
+            starts = torch.zeros(len(lengths) + 1, dtype=torch.int32, device=self.device)
+            starts[1:] = self.cached.cumsum(0)
+            return kda.kda_paged_read_fp8(*memory, self.block_table, starts, self.cached, total, error_word=self.error_word)
+        rows = [memory[self.block_table[r, :-(-n // self.page_size)].long()].transpose(0, 1).flatten(1, 2)[:, :n]
+                for r, n in enumerate(lengths)]
+        return kda.PagedRead(*torch.cat(rows, dim=1))
 
 
 def main():
