@@ -67,6 +67,8 @@ constexpr int RING = 4;  // segments the walking warp may be ahead
 // first chunk of 4096 tokens, whose items have 1 to 32 units: 122 us at 3, 118 at 4, 119.5 at 5 (two tiles); 32 verify
 // requests: 56.7 us at 1, 55.7 at 2, 54.6 at 4, 56.4 at 6 (one tile).
 constexpr int LEAD = 4;
+// A cache in 8 bits, whose queries become codes: a first chunk of 4096 tokens 179 us at 4, 171 at 7, 174 at 10.
+constexpr int LEAD8 = 7;
 constexpr int SCALES = 2;                                  // pairs of units whose scales are held
 constexpr int BLOCK = KDA_FP8_SCALE_TOKENS, BLOCKS = UNIT / BLOCK;  // keys a scale, scales a unit
 
@@ -432,7 +434,7 @@ __global__ void __launch_bounds__(Shape<D, FP8>::THREADS, 1)
 
   // ---- this CTA's share of the line of units
   const int cta = blockIdx.x;
-  const LineShare line = line_share<THREADS, LEAD>(p, w, sh.warp_sum, sh.start);
+  const LineShare line = line_share<THREADS, FP8 ? LEAD8 : LEAD>(p, w, sh.warp_sum, sh.start);
   if (blockIdx.x == 0 && line.bad && p.error_word) atomicOr(p.error_word, line.bad);
   if (cta >= line.ctas) return;  // the whole CTA: nothing allocated yet
   if (warp == PRODUCT_WARP) tmem_alloc(&sh.tmem, 512);
@@ -527,7 +529,7 @@ __global__ void __launch_bounds__(Shape<D, FP8>::THREADS, 1)
         ++out;
         return true;
       };
-      alive = line_walk<LEAD>(p, w, line, end, sh.start, put);
+      alive = line_walk<FP8 ? LEAD8 : LEAD>(p, w, line, end, sh.start, put);
     } else if (warp == LOAD_WARP) {
       // ---- keys and values of the CTA's units, a lane per copy; keys one unit ahead
       const int P = p.cache.page_size, box = a.box;
@@ -1344,7 +1346,7 @@ cudaError_t launch_paged_attention_tc(const kda_attention_params& p, const kda_p
   long long keys = (long long)p.table_width * p.cache.page_size;
   if (p.window > 0 && p.window + tokens < keys) keys = p.window + tokens;
   const long long items = p.num_tokens / tokens + p.num_requests;
-  if (items * (keys / UNIT + 2 + LEAD) > 0x7fffffffLL / p.cache.num_heads) return cudaErrorNotSupported;
+  if (items * (keys / UNIT + 2 + (scales ? LEAD8 : LEAD)) > 0x7fffffffLL / p.cache.num_heads) return cudaErrorNotSupported;
   AttnArgs a;
   a.p = p;
   a.sc = scales ? *scales : kda_paged_scales{};
