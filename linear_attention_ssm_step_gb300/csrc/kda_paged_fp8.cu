@@ -26,6 +26,13 @@ constexpr int SCALE_LOW = -40, SCALE_HIGH = 40;  // exponents of the scales
 // cosines that the CTA forms once for all heads, in shared memory, by the fast
 // functions (off by 2^-20, where a code rounds by 2^-4). Other head sizes, and
 // rows off their alignment, read the rows twice.
+//
+// Measured: 8192 rows of 32 + 8 + 8 heads of 128, 43 us, of which the queries 20
+// and keys and values 23 to 30, bound by latency: 1400 instructions a task, issued
+// in a third of the cycles. A CTA per row with its share of the run's tasks (each
+// forming the run's sines and cosines again): 58 us; one with four warps a task
+// and the turn in registers, 52 to 69. 256 decode rows 7.3 us: a launch, the slots,
+// the rows and scales, the codes.
 
 // A run: rows t0 .. t0 + n - 1, at tokens first .. of a block.
 struct BlockRun {
@@ -368,7 +375,8 @@ cudaError_t launch_rope_append_fp8(const kda_rope_params& p, const kda_paged_sca
 // A CTA per 16 packed rows: its threads go through the requests, and each
 // request marks the rows of the tile that it covers; 16 threads then find their
 // rows' pages; then all copy, 16 codes and 32 bytes of output a thread at a time
-// where the rows allow it. Bound by memory: a byte in and two out an element.
+// where the rows allow it. Bound by memory: a byte in and two out an element (32
+// requests of 1500..6000 tokens, 8 heads of 128: 120 us, 6.3 TB/s, 94 % of a copy).
 
 constexpr int READ_THREADS = 256, READ_ROWS = 16;
 

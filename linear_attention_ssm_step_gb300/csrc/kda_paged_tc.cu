@@ -1,5 +1,7 @@
 // kda_paged_tc.cu - paged attention on the fifth-generation tensor cores
-// (include/kda_paged.h), head_dim 64 or 128.
+// (include/kda_paged.h), head_dim 64 or 128; FP8, over a cache in 8 bits
+// (include/kda_paged_fp8.h), requests of more than 32 rows a key-value head (for
+// fewer: kda_paged_fp8_rows.cu).
 //
 // Mathematics. For one key-value head and the rows that read it, over units of
 // 128 keys: S = Q K^T, P = exp2(c (S - m)) with c = scale log2 e and m a running
@@ -44,6 +46,27 @@
 // 530 us alone, 1.66 PFLOP/s, and 560..585 us in a loop, under the power cap).
 // Small calls: latency (one decode request of 1000 tokens 10.1 us). Once-a-run code
 // is kept short and in loops that are not unrolled: it is fetched anew each run.
+//
+// FP8. The codes of the keys go into the first product as they are, with the
+// queries as two E4M3 numbers each (query_codes in kda_paged_line.cuh): two
+// products at twice the rate of one of bf16, without a conversion of the keys,
+// which read half the shared memory. Values become fp16, which holds them exactly,
+// on the way from one buffer in shared memory to another, by four more warps: a
+// product takes operands of one width, and weights in 8 bits would be too coarse.
+// A block's scale of 16 keys is a factor of its scores, in the multiply-add that
+// forms the exponent (y = f s + log2 vs), and the value scale an addend there: the
+// weights that meet the values are exp2(y - m), their reference m of fp32 y, so
+// that the sum l takes them times 1 / vs. fp16 weights of up to 2^14 (a reference
+// set at 2^6, and 8 of growth) hold 11 bits down to 2^-14, so that keys of 2^-20
+// of the largest weight still count.
+// Two chunks of 2048 tokens over 4096..16384 cached, 32 query heads: 787 us, 1.28
+// PFLOP/s. The conversion costs 35 us of that (with its arithmetic left out: 733), its
+// reads and writes of shared memory beside the products'; the block scales in
+// the weights 30 (with one factor: 757), the queries to codes 13000 cycles a run
+// against 6600. The rest of the difference to the 16-bit cache's rate is the
+// supply of instructions: twice as many warps run code of their own. Scores taken
+// twice from tensor memory to save registers were slower (1054), as were 8 and 16
+// rows of queries at a time (850, 793).
 #include <math.h>
 
 #include <type_traits>
