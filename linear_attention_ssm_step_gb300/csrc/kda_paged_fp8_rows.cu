@@ -82,7 +82,7 @@ struct Shared {
   Segment seg[RING];
   alignas(16) float q_scale[2][R];  // scale log2e times the power of two by which a row's query was brought down
   alignas(16) float top[4][R];      // a warp's maxima, or sums
-  alignas(16) float m[R];           // a run's references at its end
+  alignas(16) float down[R], fade[R];  // -m, the same for all keys, and by how much it last moved
   int warp_sum[THREADS / 32];
   LineStart start;
   uint32_t tmem;
@@ -189,24 +189,26 @@ __device__ __forceinline__ void store_columns(uint32_t taddr, const float (&v)[N
   }
 }
 
-// Four columns at taddr, taddr + step and taddr + 2 step, with the wait.
-__device__ __forceinline__ void load_parts(uint32_t taddr, int step, float (&out)[3][4]) {
-  uint32_t z[3][4];
-#pragma unroll
-  for (int i = 0; i < 3; ++i)
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(z[i][0]), "=r"(z[i][1]), "=r"(z[i][2]), "=r"(z[i][3])
-                 : "r"(taddr + i * step)
-                 : "memory");
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(z[0][0]), "+r"(z[0][1]), "+r"(z[0][2]), "+r"(z[0][3]), "+r"(z[1][0]), "+r"(z[1][1]), "+r"(z[1][2]),
-                 "+r"(z[1][3]), "+r"(z[2][0]), "+r"(z[2][1]), "+r"(z[2][2]), "+r"(z[2][3])
-               :
-               : "memory");
+// N (4 or 8) columns at taddr, taddr + step and taddr + 2 step, with one wait.
+template <int N>
+__device__ __forceinline__ void load_parts(uint32_t taddr, int step, float (&out)[3][N]) {
+  uint32_t z[3][N];
 #pragma unroll
   for (int i = 0; i < 3; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) out[i][j] = __uint_as_float(z[i][j]);
+    for (int j = 0; j < N; j += 4)
+      asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(z[i][j]), "=r"(z[i][j + 1]), "=r"(z[i][j + 2]), "=r"(z[i][j + 3])
+                   : "r"(taddr + i * step + j)
+                   : "memory");
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 3; ++i)
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      asm volatile("" : "+r"(z[i][j]));  // no use of it above the wait
+      out[i][j] = __uint_as_float(z[i][j]);
+    }
 }
 
 // The sums (or maxima) over a warp's lanes of R values a lane: lane l is left with that of value l % R. Each step sends half
@@ -544,7 +546,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int u0 = sg.u0, u1 = sg.u1, ntok = sg.ntok, pos0 = sg.pos0, rows = ntok * g;
       // every row sees the keys [all_lo, all_hi)
       const int all_lo = first_key(pos0 + ntok - 1, window), all_hi = pos0 + 1;
-      f32x2 down[R / 2], l[R / 2];  // -m and l of two rows each
+      if (x < R) sh.down[x] = -NOTHING;  // first read behind the votes of the first unit
+      f32x2 down[R / 2], l[R / 2];       // -m and l of two rows each
 #pragma unroll
       for (int r = 0; r < R; r += 2) {
         down[r / 2] = pk2(-NOTHING, -NOTHING);
@@ -605,22 +608,25 @@ __global__ void __launch_bounds__(THREADS, 1)
             alive = false;
             break;
           }
+          // a thread a row finds its new reference, and all read them
+          if (x < R) {
+            const float top = fmaxf(fmaxf(sh.top[0][x], sh.top[1][x]), fmaxf(sh.top[2][x], sh.top[3][x])), was = sh.down[x];
+            const bool moves = top + was > LIFT + SLACK;
+            const float to = moves ? LIFT - top : was;
+            sh.down[x] = to;
+            sh.fade[x] = moves ? ex2(to - was) : 1.f;
+          }
+          bar_sync(2, SOFTMAX_THREADS);
           f32x2 fade[R / 2];
 #pragma unroll
-          for (int r = 0; r < R; r += 2) {
-            float down0[2], fade0[2];
-            upk2(down[r / 2], down0[0], down0[1]);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float top = fmaxf(fmaxf(sh.top[0][r + i], sh.top[1][r + i]), fmaxf(sh.top[2][r + i], sh.top[3][r + i]));
-              const bool moves = top + down0[i] > LIFT + SLACK;
-              const float to = moves ? LIFT - top : down0[i];
-              fade0[i] = moves ? ex2(to - down0[i]) : 1.f;
-              down0[i] = to;
-            }
-            down[r / 2] = pk2(down0[0], down0[1]);
-            fade[r / 2] = pk2(fade0[0], fade0[1]);
+          for (int r = 0; r < R; r += 4) {
+            const float4 d = *reinterpret_cast<const float4*>(&sh.down[r]), f = *reinterpret_cast<const float4*>(&sh.fade[r]);
+            down[r / 2] = pk2(d.x, d.y);
+            down[r / 2 + 1] = pk2(d.z, d.w);
+            fade[r / 2] = pk2(f.x, f.y);
+            fade[r / 2 + 1] = pk2(f.z, f.w);
             l[r / 2] = mul2(l[r / 2], fade[r / 2]);
+            l[r / 2 + 1] = mul2(l[r / 2 + 1], fade[r / 2 + 1]);
           }
           if (of_run > 0) {  // O^T, once the product before is done
             alive = warp_wait(&sh.p_done[1 - buf], ((n - 1) / 2) & 1);
@@ -681,12 +687,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int r = 0; r < R; r += 2) upk2(l[r / 2], v[r], v[r + 1]);
         const float mine = fold<R, false>(v);
         if (lane < R) sh.top[warp][lane] = mine;
-#pragma unroll
-        for (int r = 0; r < R; r += 2) {  // the same in all threads
-          float d0, d1;
-          upk2(down[r / 2], d0, d1);
-          if (x == 0) *reinterpret_cast<float2*>(&sh.m[r]) = make_float2(-d0, -d1);
-        }
       }
       if (bar_any(2, SOFTMAX_THREADS, !alive)) {
         alive = false;
@@ -709,22 +709,23 @@ __global__ void __launch_bounds__(THREADS, 1)
       auto part_o = [&](int id) { return a.parts + (size_t)id * a.slot_floats; };
       auto part_ml = [&](int id) { return reinterpret_cast<float2*>(part_o(id) + R * D); };
       const int my_slot = sg.part == 0 ? 2 * cta + 1 : 2 * cta;
+      constexpr int STEP = R < 8 ? 4 : 8;
 #pragma unroll 1
-      for (int r0 = 0; r0 < rows; r0 += 4) {
-        float o[3][4];
+      for (int r0 = 0; r0 < rows; r0 += STEP) {
+        float o[3][STEP];
         load_parts(o_addr + r0, R, o);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < STEP; ++i) {
           const int r = r0 + i;
           if (r >= rows) break;
           const float sum = (sh.top[0][r] + sh.top[1][r]) + (sh.top[2][r] + sh.top[3][r]);
           const float value = fmaf(fmaf(o[2][i], 0.03125f, o[1][i]), 0.03125f, o[0][i]);
           if (direct) {
             if (has_d) *out_at(r) = float_to_bf16_bits(sees_none(r) ? 0.f : value * rcp(sum));
-            if (x == r && p.lse != nullptr) put_lse(r, sh.m[r], sum);
+            if (x == r && p.lse != nullptr) put_lse(r, -sh.down[r], sum);
           } else {
             if (has_d) part_o(my_slot)[r * D + d] = value;
-            if (x == r) part_ml(my_slot)[r] = make_float2(sh.m[r], sum);
+            if (x == r) part_ml(my_slot)[r] = make_float2(-sh.down[r], sum);
           }
         }
       }
