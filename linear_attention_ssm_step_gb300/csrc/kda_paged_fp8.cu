@@ -93,15 +93,14 @@ __device__ __forceinline__ void load_rows(const BlockRun& run, const BlockTask& 
 #pragma unroll
   for (int i = 0; i < SCALE_TOKENS; ++i) {
     const uint16_t* const row = k.src + i * k.row_stride + lane * E;
-    uint2 x = make_uint2(0, 0);
-    if (i < run.n) {
-      if constexpr (E == 4)
-        x = *reinterpret_cast<const uint2*>(row);
-      else
-        x.x = *reinterpret_cast<const uint32_t*>(row);
+    if (i >= run.n) break;  // the same for the whole warp
+    if constexpr (E == 4) {
+      const uint2 x = *reinterpret_cast<const uint2*>(row);
+      z.raw[i][0] = x.x;
+      z.raw[i][1] = x.y;
+    } else {
+      z.raw[i][0] = *reinterpret_cast<const uint32_t*>(row);
     }
-    z.raw[i][0] = x.x;
-    if constexpr (E == 4) z.raw[i][1] = x.y;
   }
 }
 
@@ -346,12 +345,13 @@ __global__ void __launch_bounds__(APPEND_WARPS * 32, 2)
 
 cudaError_t launch_rope_append_fp8(const kda_rope_params& p, const kda_paged_scales& sc, bool q_wide, int lane_elems,
                                    cudaStream_t s) {
-  // Up to 512 rows are mostly decode steps, whose rows may each be a run: a CTA per row, and the queries in the same launch
-  // (8192 rows so: 47.3 us). More are chunks, or so many rows that it does not matter: a CTA looks for runs in up to 16 rows,
-  // and the queries go ahead in a launch of kda_rope_append_kernel without keys and values, which needs half the registers:
-  // it runs at twice the occupancy, and this kernel is brought in while it ends.
-  const bool fused = p.num_tokens <= 512;
-  const int span = fused ? 1 : p.num_tokens < 16 * 512 ? (p.num_tokens + 511) / 512 : SCALE_TOKENS;
+  // Up to 512 rows are mostly decode steps, whose rows may each be a run: a CTA per row. More are chunks, or so many rows that
+  // it does not matter: a CTA looks for runs in up to 16 rows, 512 CTAs. Up to 2048 rows the queries are in the same launch
+  // (1037 rows: 10.3 us, 11.9 in two launches). With more they go ahead in a launch of kda_rope_append_kernel without keys and
+  // values, which needs half the registers and runs at twice the occupancy, and this kernel is brought in while it ends (8192
+  // rows: 43 us, 47 in one launch).
+  const bool fused = p.num_tokens <= 2048;
+  const int span = p.num_tokens <= 512 ? 1 : p.num_tokens < 16 * 512 ? (p.num_tokens + 511) / 512 : SCALE_TOKENS;
   const int blocks = p.num_tokens / span + (p.num_tokens % span != 0), tasks = 2 * p.cache.num_heads;
   // few runs: a task a warp
   const int splits = p.num_tokens < 4096 && tasks > APPEND_WARPS ? (tasks + APPEND_WARPS - 1) / APPEND_WARPS : 1;
