@@ -59,14 +59,14 @@
 // that the sum l takes them times 1 / vs. fp16 weights of up to 2^14 (a reference
 // set at 2^6, and 8 of growth) hold 11 bits down to 2^-14, so that keys of 2^-20
 // of the largest weight still count.
-// Two chunks of 2048 tokens over 4096..16384 cached, 32 query heads: 787 us, 1.28
-// PFLOP/s. The conversion costs 35 us of that (with its arithmetic left out: 733), its
-// reads and writes of shared memory beside the products'; the block scales in
-// the weights 30 (with one factor: 757), the queries to codes 13000 cycles a run
-// against 6600. The rest of the difference to the 16-bit cache's rate is the
-// supply of instructions: twice as many warps run code of their own. Scores taken
-// twice from tensor memory to save registers were slower (1054), as were 8 and 16
-// rows of queries at a time (850, 793).
+// Two chunks of 2048 tokens over 4096..16384 cached, 32 query heads: 754 us, 1.34
+// PFLOP/s. What that costs beside the 16-bit cache's chain was taken from a state
+// of 771 us: the conversion of the values 38 (733 with it left out), its reads and
+// writes of shared memory beside the products'; the block scales in the weights 13
+// (758 with one factor). The queries to codes take 6000 cycles a run. What is left
+// follows how the loop over the units is compiled, by up to 10 %, with a third
+// more instructions than the 16-bit one's. Scores taken twice from tensor memory to
+// save registers: 1054.
 #include <math.h>
 
 #include <type_traits>
