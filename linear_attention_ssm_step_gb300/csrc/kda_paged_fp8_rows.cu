@@ -10,10 +10,10 @@
 //   O^T += V^T P^T    P as three E4M3 numbers each, 3 R columns
 // A weight p <= 2^8 is p1 + 2^-5 p2 + 2^-10 p3: each part takes four bits and
 // what it leaves is at most 2^-5 of it, so that three hold fp16's eleven bits;
-// small weights are off by 2^-20 at most, 2^-26 of the row's largest: the parts
+// small weights are off by 2^-20 at most, 2^-24 of the row's largest: the parts
 // have columns of their own in O^T and are added up at the end, in fp32. l sums
 // the fp32 weights. The reference m of a row follows its maximum when that has
-// grown by more than 2 (log2), for all keys together: m is the same in all
+// grown by more than 4 (log2), for all keys together: m is the same in all
 // threads, which agree on it by a vote a unit.
 //
 // A CTA is eight warps: four of softmax (a thread per key), and one warp each
@@ -24,13 +24,14 @@
 // and parts are written as whole rows.
 //
 // What bounds it: memory, and what is not hidden behind it. 64 decode requests of
-// 2048..8192 tokens, 8 key-value heads: 113 us, 5.6 TB/s; a unit takes 1360 cycles
-// at the copy's rate and the softmax group about 1000 of these. A call begins with
-// 5000 cycles until the first scores, and ends with an item's parts: 2000 to 3500
-// a trip to memory under load, hence eight parts a trip (four: 47 us against 43
+// 2048..8192 tokens, 8 key-value heads: 113 to 115 us, 5.5 TB/s; a unit takes 1360
+// cycles at the copy's rate. In a build with clocks read on the way (126 us) a call
+// began with 7800 cycles until the first scores and ended with an item's parts,
+// 2300 to 2700 a trip to memory under load, hence eight parts a trip (four: 47 us against 43
 // for 4 requests of 16384..65536 tokens). With rows as the rows of the products (the
 // kernel for chunks) the same 64 requests took 220 us, bound by the padding to 128
-// rows and by the conversion of the values.
+// rows and by the conversion of the values. 32 verify requests of 24 rows: 48 us,
+// 17 of memory.
 // Scales: with one pair of units on its way a step waited for them under load
 // (600 cycles a unit in the slowest CTAs); with two it does not.
 #include <math.h>

@@ -59,14 +59,14 @@
 // that the sum l takes them times 1 / vs. fp16 weights of up to 2^14 (a reference
 // set at 2^6, and 8 of growth) hold 11 bits down to 2^-14, so that keys of 2^-20
 // of the largest weight still count.
-// Two chunks of 2048 tokens over 4096..16384 cached, 32 query heads: 754 us, 1.34
-// PFLOP/s. What that costs beside the 16-bit cache's chain was taken from a state
-// of 771 us: the conversion of the values 38 (733 with it left out), its reads and
-// writes of shared memory beside the products'; the block scales in the weights 13
-// (758 with one factor). The queries to codes take 6000 cycles a run. What is left
-// follows how the loop over the units is compiled, by up to 10 %, with a third
-// more instructions than the 16-bit one's. Scores taken twice from tensor memory to
-// save registers: 1054.
+// Two chunks of 2048 tokens over 4096..16384 cached, 32 query heads: 755 to 758 us,
+// 1.33 PFLOP/s. What that costs beside the 16-bit cache's chain was measured on an
+// earlier build of 767 to 772 us: 733 with the conversion of the values left out,
+// 758 with one factor for all keys in place of the block scales, 698 with neither.
+// Another build spent 13700 cycles a run until its queries were codes (the 16-bit
+// kernel has them after 6600). How the loop over the units is compiled depends on
+// code that runs once a run: builds that differ in that alone took 756 to 853.
+// Scores taken twice from tensor memory to save registers: 1054.
 #include <math.h>
 
 #include <type_traits>
@@ -403,7 +403,7 @@ __device__ __forceinline__ float2* part_ml(const AttnArgs& a, int slot) {
 // Rows [from, to) of a tile of queries in 16 bits to codes, by the 128 threads of a group, each the chunks (8 numbers, D / 8 a
 // row) that it has brought, from `raw` on. up, also: where the powers of two go by which rows were brought down. A function of
 // its own, not inlined: inside the kernel it changed how the loop over the units was compiled (two chunks of 2048 tokens over
-// 4096..16384 cached 788 us, against 754; with two rows a thread at a time 852).
+// 4096..16384 cached 788 us, against 756; with two rows a thread at a time 852).
 template <int D>
 __device__ __noinline__ void queries_to_codes(const uint8_t* raw, uint8_t* codes, float* up, float* also, int from, int to) {
   constexpr int CHUNKS = D / 8, ROUND = TILE / CHUNKS, N = 2;
