@@ -86,6 +86,10 @@ kda_status kda_rope_append_fp8(const kda_rope_params* p, const kda_paged_scales*
  * cache rows on 16 bytes (pointers, and strides that are multiples of 16) runs
  * on the tensor cores, any other cache on the CUDA cores. The workspace is
  * kda_paged_attention's, and the two calls may take turns with one.
+ *
+ * Calls with up to 32 rows (new tokens times query heads of a key-value head) a
+ * request on average run in a kernel for few rows, others in one for chunks. A
+ * step that mixes decode tokens and chunks is faster as two calls, one for each.
  */
 kda_status kda_paged_attention_fp8(const kda_attention_params* p, const kda_paged_scales* s, void* workspace,
                                    size_t workspace_bytes, void* stream);

@@ -813,6 +813,11 @@ static cudaError_t launch_rows(const RowsArgs& a, int ctas, cudaStream_t s) {
   return launch_early(kda_paged_attention_fp8_rows_kernel<D, R>, dim3((unsigned)ctas), THREADS, bytes, s, km, vm, a);
 }
 
+// By the mean rows a request, which is all that the host knows. On 64 requests of 2048..8192 tokens, 32 heads over 8, single
+// calls from a cold cache, this kernel and the one for chunks: 1 new token each 138 and 224 us, 4 each 142 and 226, 1..8 each
+// 162 and 228. Decode tokens and a chunk in one call, 200 and 1000: 794 and 939 where the decodes have such contexts and the
+// chunk 8192 tokens; but 1873 and 541 where they have 64..256 and the chunk 32768, whose keys are read once every 8 tokens.
+// As two calls these take 522 and 451.
 int paged_attention_few_rows(const kda_attention_params& p) {
   const long long group = p.num_q_heads / p.cache.num_heads;
   const long long tokens = ((long long)p.num_tokens + p.num_requests - 1) / p.num_requests;
