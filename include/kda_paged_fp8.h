@@ -76,9 +76,9 @@ kda_status kda_rope_append_fp8(const kda_rope_params* p, const kda_paged_scales*
  *     head, exact within 2^9 of the largest magnitude of its head and off by
  *     less than 2^-17 of that below;
  *   - a weight, times its key's value scale, enters as fp16, by a power of two
- *     for the row that follows its largest; its sum does not. For few rows that
- *     number goes on as three E4M3 numbers, off by at most 2^-24 of the row's
- *     largest beside fp16's rounding.
+ *     for the row that follows its largest; its sum does not. So it is off by up
+ *     to 2^-11 of itself, and at the least by 2^-31 of the row's largest (2^-35
+ *     for few rows): n small ones beside a large one by up to n times that.
  * A query with an infinite or NaN number gives NaN in out and lse. NaN codes
  * that a row sees act as NaN does in kda_paged_attention.
  *

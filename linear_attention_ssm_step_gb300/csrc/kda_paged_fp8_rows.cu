@@ -7,14 +7,17 @@
 // of the cache enter both products as they lie in the pages:
 //   S^T = K Q^T       Q as two E4M3 numbers each (put_query), 2 R columns
 //   P^T = exp2(y - m), y = scale log2e ks S + log2 vs: weights times value scales
-//   O^T += V^T P^T    P as three E4M3 numbers each, 3 R columns
-// A weight p <= 2^8 is p1 + 2^-5 p2 + 2^-10 p3: each part takes four bits and
-// what it leaves is at most 2^-5 of it, so that three hold fp16's eleven bits;
-// small weights are off by 2^-20 at most, 2^-24 of the row's largest: the parts
-// have columns of their own in O^T and are added up at the end, in fp32. l sums
-// the fp32 weights. The reference m of a row follows its maximum when that has
-// grown by more than 4 (log2), for all keys together: m is the same in all
-// threads, which agree on it by a vote a unit.
+//   O^T += V^T P^T    P as three E5M2 numbers each, 3 R columns
+// A weight p <= 2^14, as fp16, is p1 + 2^-4 p2 + 2^-8 p3, exactly, subnormals
+// included: in the binade of 2^E a part takes three bits and leaves at most
+// 2^(E - 3), the next 2^(E - 7), the third nothing of fp16's eleven bits. So a
+// weight is rounded by 2^-11 of itself, and below 2^-24 of the row's largest
+// (which is kept at 2^10 or more) by 2^-35 of that: many small weights beside a
+// large one still add up. (E4M3 parts hold as many bits, but of a weight at 2^-23
+// of the largest one bit.) The parts have columns of their own in O^T and are
+// added up at the end, in fp32. l sums the fp32 weights. The reference m of a row
+// follows its maximum when that has grown by more than 4 (log2), for all keys
+// together: m is the same in all threads, which agree on it by a vote a unit.
 //
 // A CTA is eight warps: four of softmax (a thread per key), and one warp each
 // that issues the products, that loads (a tensor-map copy a page and side), that
@@ -49,7 +52,8 @@ constexpr int RING = 4;    // segments the walking warp may be ahead
 constexpr int LEAD = 3;    // what an item costs beside its units, in units
 constexpr int SCALES = 4;  // pairs of units whose scales are held
 constexpr int BLOCK = KDA_FP8_SCALE_TOKENS, BLOCKS = UNIT / BLOCK;
-constexpr float LIFT = 4.f, SLACK = 4.f;  // log2 of the largest weight when the reference is set; its growth until the next
+constexpr float LIFT = 10.f, SLACK = 4.f;  // log2 of the largest weight when the reference is set; its growth until the next
+static_assert(LIFT + SLACK <= 14.f, "16 times what the first part of a weight leaves is a number of E5M2");
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float NOTHING = -1e30f;  // the reference of a row that has seen no key: below any score, and no infinity, so that
                                    // differences to it are numbers
@@ -144,6 +148,14 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t x, uint32_t y) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
   return r;
 }
+
+// Two fp16 numbers to E5M2, and back: an E5M2 number is the upper byte of an fp16 one.
+__device__ __forceinline__ uint32_t f16x2_to_e5m2x2(uint32_t x) {
+  unsigned short r;
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t e5m2x2_to_f16x2(uint32_t two) { return __byte_perm(two, 0u, 0x1404); }
 
 // N consecutive columns of this thread's lane, with the wait (N: 4, 8, 16, 32 or 64).
 template <int N>
@@ -485,8 +497,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     // ---- the products: a unit's scores one unit ahead of its values, over the ends of runs
     const uint32_t base = smem_addr(smem), tm = uniform(tmem);
     constexpr uint32_t M128 = 128u >> 4, F32 = 1u << 4, MN_MAJOR = 3u << 15;  // of A and B
+    constexpr uint32_t B_E5M2 = 1u << 10;                                     // the weights; all others are E4M3 (0)
     constexpr uint32_t IDESC_S = F32 | ((uint32_t)S::NS >> 3 << 17) | (M128 << 24);
-    constexpr uint32_t IDESC_O = F32 | MN_MAJOR | ((uint32_t)S::NP >> 3 << 17) | ((uint32_t)D >> 4 << 24);
+    constexpr uint32_t IDESC_O = F32 | B_E5M2 | MN_MAJOR | ((uint32_t)S::NP >> 3 << 17) | ((uint32_t)D >> 4 << 24);
     uint32_t n = 0;          // units whose scores have been issued
     uint32_t fresh = 0;      // the last of them begins a run
     auto values = [&](uint32_t m) {
@@ -660,9 +673,9 @@ __global__ void __launch_bounds__(THREADS, 1)
           uint32_t rest = pack_f16x2(p0, p1);
 #pragma unroll
           for (int part = 0; part < 3; ++part) {
-            const uint32_t c = f16x2_to_codes(rest);
+            const uint32_t c = f16x2_to_e5m2x2(rest);
             words[(part * R + r) / 4] |= r % 4 ? c << 16 : c;
-            if (part < 2) rest = mul_f16x2(sub_f16x2(rest, codes_to_f16x2(c)), 0x50005000u);  // 32
+            if (part < 2) rest = mul_f16x2(sub_f16x2(rest, e5m2x2_to_f16x2(c)), 0x4c004c00u);  // 16
           }
         }
         uint8_t* const pt = smem + S::P0 + buf * S::P_BYTES + x * 16;
@@ -720,7 +733,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           const int r = r0 + i;
           if (r >= rows) break;
           const float sum = (sh.top[0][r] + sh.top[1][r]) + (sh.top[2][r] + sh.top[3][r]);
-          const float value = fmaf(fmaf(o[2][i], 0.03125f, o[1][i]), 0.03125f, o[0][i]);
+          const float value = fmaf(fmaf(o[2][i], 0.0625f, o[1][i]), 0.0625f, o[0][i]);
           if (direct) {
             if (has_d) *out_at(r) = float_to_bf16_bits(sees_none(r) ? 0.f : value * rcp(sum));
             if (x == r && p.lse != nullptr) put_lse(r, -sh.down[r], sum);
