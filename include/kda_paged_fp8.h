@@ -61,9 +61,11 @@ typedef struct {
  * ones too; NaN becomes a NaN code and does not count in m.
  *
  * Rows of one block must follow one another in the call, row t + 1 at
- * slots[t] + 1 (kda_paged_plan's rows of a request do); where rows of a block
- * come in any other order, or a slot twice, that block's codes and scales are
- * undefined. At most 2^30 rows a call. k is turned with sines and cosines good to 2^-20, far below the
+ * slots[t] + 1 (kda_paged_plan's rows of a request do). Rows among them that
+ * are not stored (a negative position, slot -1 or outside the cache) stand for
+ * the tokens in between, whose codes are left as they are and count with the
+ * new scale. Where rows of a block come in any other order, or a slot twice,
+ * that block's codes and scales are undefined. At most 2^30 rows a call. k is turned with sines and cosines good to 2^-20, far below the
  * rounding of a code; q as in kda_rope_append.
  */
 kda_status kda_rope_append_fp8(const kda_rope_params* p, const kda_paged_scales* s, void* stream);

@@ -17,15 +17,17 @@ constexpr int SCALE_LOW = -40, SCALE_HIGH = 40;  // exponents of the scales
 //
 // A CTA per row turns its queries, as kda_rope_append_kernel does. Keys and
 // values, in CTAs beside those, go by the block: a scale needs the largest
-// magnitude of all the rows that fall into one block (a run: at most 16 rows that
-// follow one another). A CTA has the runs that begin among its `span` rows, found
-// from the positions and slots of these and the 15 behind; a task is one side and
-// head of a run, and a warp takes it whole, reads its rows once, into registers as
-// bf16 (two a lane and row for head_dim 128), goes over them for the largest
-// magnitude, and again to encode. Keys are turned in both passes, by sines and
-// cosines that the CTA forms once for all heads, in shared memory, by the fast
-// functions (off by 2^-20, where a code rounds by 2^-4). Other head sizes, and
-// rows off their alignment, read the rows twice.
+// magnitude of all the rows that fall into one block (a run: at most 16 rows,
+// consecutive but for some that are not stored). A CTA has the runs that begin
+// among its `span` rows, found from the positions and slots of these and of the 15
+// before and behind; a task is one side and head of a run, and a warp takes it
+// whole, reads its rows once, into registers as bf16 (two a lane and row for
+// head_dim 128), goes over them for the largest magnitude, and again to encode.
+// Keys are turned in both passes, by sines and cosines that the CTA forms once for
+// all heads, in shared memory, by the fast functions (off by 2^-20, where a code
+// rounds by 2^-4). Other head sizes, rows off their alignment and runs with rows
+// left out read the rows twice (asking for every row of a run whether it is stored
+// cost the chunk below 1.3 us more).
 //
 // Measured: 8192 rows of 32 + 8 + 8 heads of 128, 43 us, of which the queries 20
 // and keys and values 23 to 30, bound by latency: 1400 instructions a task, issued
@@ -34,9 +36,11 @@ constexpr int SCALE_LOW = -40, SCALE_HIGH = 40;  // exponents of the scales
 // and the turn in registers, 52 to 69. 256 decode rows 7.3 us: a launch, the slots,
 // the rows and scales, the codes.
 
-// A run: rows t0 .. t0 + n - 1, at tokens first .. of a block.
+// A run: rows t0 .. t0 + n - 1, at tokens first .. of a block; those that are stored as bits, of which the first and the last
+// are set.
 struct BlockRun {
   int t0, n;
+  uint32_t rows;
   int page, block, first;
 };
 
@@ -191,7 +195,7 @@ __device__ __forceinline__ void append_any(const kda_rope_params& p, const Block
   };
   float top = 0.f;
   for (int i = 0; i < run.n; ++i)
-    for (int c = lane; c < D; c += 32) top = fmaxf(top, fabsf(value(i, c)));
+    for (int c = lane; run.rows >> i & 1u && c < D; c += 32) top = fmaxf(top, fabsf(value(i, c)));
   const BlockScale b = new_scale(warp_max(top), run.first > 0, old);
   if (b.again > 0.f)
     for (int j = 0; j < run.first; ++j)
@@ -200,7 +204,7 @@ __device__ __forceinline__ void append_any(const kda_rope_params& p, const Block
         *code = (uint8_t)f32x2_to_e4m3x2(pk2(e4m3_to_float(*code) * b.again, 0.f));
       }
   for (int i = 0; i < run.n; ++i)
-    for (int c = lane; c < D; c += 32)
+    for (int c = lane; run.rows >> i & 1u && c < D; c += 32)
       k.block[(run.first + i) * k.token_stride + c] = (uint8_t)f32x2_to_e4m3x2(pk2(value(i, c) * b.inverse, 0.f));
   if (lane == 0) *k.scale = b.scale;
 }
@@ -273,33 +277,45 @@ __global__ void __launch_bounds__(APPEND_WARPS * 32, 2)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int split = (int)blockIdx.x % splits;
   const int half = p.rotary_dim >> 1, Hkv = p.cache.num_heads, P = p.cache.page_size;
-  // lane l has row t0 + l - 1: the row before this CTA's, its own, and those that their runs may reach to
+  // Lane l has row t0 + l: this CTA's, and those behind that their runs may reach to; and, of the rows before, in which those
+  // runs may have begun, row t0 - 15 + l.
   const int t0 = (int)blockIdx.x / splits * span;
-  const long long near = (long long)t0 + lane - 1, slots = (long long)p.cache.num_pages * P;
-  int pos = -1, slot = -1;
-  if (near >= 0 && near < p.num_tokens) {
+  const long long near = (long long)t0 + lane, slots = (long long)p.cache.num_pages * P;
+  const int back = lane - (SCALE_TOKENS - 1);
+  int pos = -1, slot = -1, pos_back = -1, slot_back = -1;
+  if (near < p.num_tokens) {
     pos = p.positions[near];
     slot = p.slots[near];
   }
-  const bool own = lane >= 1 && lane <= span && near < p.num_tokens;
+  if (back < 0 && t0 + back >= 0) {
+    pos_back = p.positions[t0 + back];
+    slot_back = p.slots[t0 + back];
+  }
   const bool bad = pos >= 0 && slot != -1 && (slot < 0 || slot >= slots);
-  if (bad && own && warp == 0 && split == 0 && p.error_word) atomicOr(p.error_word, KDA_ERR_PAGES);
+  if (bad && lane < span && warp == 0 && split == 0 && p.error_word) atomicOr(p.error_word, KDA_ERR_PAGES);
   if (pos < 0 || bad) slot = -1;
+  if (pos_back < 0) slot_back = -1;
   const int page = slot >= 0 ? slot / P : 0, off = slot >= 0 ? (slot - page * P) % SCALE_TOKENS : 0;
-  const int before = __shfl_up_sync(0xffffffffu, slot, 1);  // by all lanes
-  const bool follows = lane > 0 && slot > 0 && off > 0 && before == slot - 1;
-  const uint32_t follow = __ballot_sync(0xffffffffu, follows);
-  uint32_t starts = __ballot_sync(0xffffffffu, own && slot >= 0 && !follows);
+  const int base = slot - off;  // slot of the block's first token
+  const uint32_t shift = (uint32_t)slot - (uint32_t)lane, shift_back = (uint32_t)slot_back - (uint32_t)back;
+  uint32_t left = __ballot_sync(0xffffffffu, lane < span && slot >= 0);
   if (warp == 0) positions[lane] = pos;
-  while (starts) {  // the same for the whole CTA
-    const int at = __ffs(starts) - 1;
-    starts &= starts - 1;
+  while (left) {  // the same for the whole CTA
+    const int at = __ffs(left) - 1;
+    const int base_at = __shfl_sync(0xffffffffu, base, at);
+    const uint32_t shift_at = __shfl_sync(0xffffffffu, shift, at);
+    // the stored rows of the block: those as far apart as their slots
+    const uint32_t same = __ballot_sync(0xffffffffu, slot >= 0 && base == base_at && shift == shift_at);
+    const uint32_t begun = __ballot_sync(0xffffffffu, slot_back >= base_at && shift_back == shift_at);  // with a smaller slot
+    left &= ~same;
+    if (begun) continue;  // by an earlier CTA
     BlockRun run;
-    run.t0 = t0 + at - 1;
-    run.n = at == 31 ? 1 : __ffs(~(follow >> (at + 1)));  // `at` is at most 16, and a run at most 16 rows
+    run.t0 = t0 + at;
+    run.rows = same >> at;
+    run.n = 32 - __clz(run.rows);  // at most 16, up to lane 30: `at` is below 16
     run.page = __shfl_sync(0xffffffffu, page, at);
     run.first = __shfl_sync(0xffffffffu, off, at);
-    run.block = (__shfl_sync(0xffffffffu, slot, at) - run.page * P) / SCALE_TOKENS;
+    run.block = (base_at - run.page * P) / SCALE_TOKENS;
     auto task = [&](int x) {
       const bool keys = x < Hkv;
       const int h = keys ? x : x - Hkv;
@@ -329,15 +345,16 @@ __global__ void __launch_bounds__(APPEND_WARPS * 32, 2)
       table[y] = fast_turn((uint64_t)(uint32_t)positions[at + i] * p.freqs[c], p.mscale);
     }
     __syncthreads();
-    while (x < 2 * Hkv) {
-      if constexpr (E > 0)
+    if (E == 0 || (run.rows & (run.rows + 1u))) {  // some are left out
+      for (; x < 2 * Hkv; x += APPEND_WARPS * splits) append_any(p, run, task(x), table);
+    } else if constexpr (E > 0) {
+      while (x < 2 * Hkv) {
         append_rows<E>(p, run, k, rows, table);
-      else
-        append_any(p, run, k, table);
-      x += APPEND_WARPS * splits;
-      if (x < 2 * Hkv) {
-        k = task(x);
-        if constexpr (E > 0) load_rows<E>(run, k, rows);
+        x += APPEND_WARPS * splits;
+        if (x < 2 * Hkv) {
+          k = task(x);
+          load_rows<E>(run, k, rows);
+        }
       }
     }
   }

@@ -29,3 +29,18 @@ def test_three_e5m2_numbers_hold_an_fp16_weight():
     codes = torch.arange(256, dtype=torch.uint8)
     as_half = (codes.to(torch.int32) << 8).to(torch.int16).view(torch.float16)
     assert torch.equal(codes.view(torch.float8_e5m2).float().nan_to_num(7.0), as_half.float().nan_to_num(7.0))
+
+
+def test_rows_left_out_of_a_block_do_not_cut_it():
+    """The oracle's append takes the stored rows of a block together: one scale from all of them, earlier tokens rounded
+    anew once, tokens that stand between them as they were."""
+    from oracle import kda_paged_fp8_oracle as fp8
+    rng = np.random.default_rng(6)
+    codes = rng.integers(0, 0x70, (1, 16, 1, 4)).astype(np.uint8)
+    x = rng.normal(size=(8, 1, 4)) * np.array([1, 1, 1, 1, 1, 1, 1, 1000.0])[:, None, None]
+    slots = [5, 6, -1, 8, -1, -1, 11, 12]
+    got, scales, _, kind = fp8.write_side(x, slots, codes, np.full((1, 1, 1), 2.0 ** -30))
+    need = 2.0 ** fp8.scale_exponent(np.abs(x[[0, 1, 3, 6, 7]]).max())
+    assert scales[0, 0, 0] == need
+    assert kind[0, :, 0].tolist() == [1] * 5 + [2, 2, 0, 2, 0, 0, 2, 2] + [0] * 3
+    assert np.array_equal(got[0, [7, 9, 10, 13, 14, 15]], codes[0, [7, 9, 10, 13, 14, 15]])
