@@ -81,6 +81,8 @@ kda_status kda_rope_append_fp8(const kda_rope_params* p, const kda_paged_scales*
  *     for the row that follows its largest; its sum does not. So it is off by up
  *     to 2^-11 of itself, and at the least by 2^-31 of the row's largest (2^-35
  *     for few rows): n small ones beside a large one by up to n times that.
+ * Scores of 2^23 or more in magnitude, which fp32 holds no better than to a
+ * whole number, may give infinite or NaN numbers in the kernel for chunks.
  * A query with an infinite or NaN number gives NaN in out and lse. NaN codes
  * that a row sees act as NaN does in kda_paged_attention.
  *

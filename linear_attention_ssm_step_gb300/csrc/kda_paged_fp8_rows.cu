@@ -55,8 +55,8 @@ constexpr int BLOCK = KDA_FP8_SCALE_TOKENS, BLOCKS = UNIT / BLOCK;
 constexpr float LIFT = 10.f, SLACK = 4.f;  // log2 of the largest weight when the reference is set; its growth until the next
 static_assert(LIFT + SLACK <= 14.f, "16 times what the first part of a weight leaves is a number of E5M2");
 constexpr float LOG2E = 1.4426950408889634f;
-constexpr float NOTHING = -1e30f;  // the reference of a row that has seen no key: below any score, and no infinity, so that
-                                   // differences to it are numbers
+constexpr float NOTHING = -3.402823466e38f;  // the reference of a row that has seen no key: no finite score is below it, and no
+                                             // infinity, so that differences to it are numbers
 
 template <int D, int R>
 struct Shape {
