@@ -898,7 +898,9 @@ __global__ void __launch_bounds__(Shape<D, FP8>::THREADS, 1)
       float query_scale = 0.f;
       if constexpr (FP8) {
         bar_sync(2, SOFTMAX_THREADS);
-        query_scale = c * sh.m1[t][fresh_tid() & (TILE - 1)];
+        // Above 2^-100, so that the factor of no block (2^-40 at the least) is 0, which makes NaN of a masked score's -inf;
+        // scores of codes stay below 2^-35 then, and are nothing in an exponent.
+        query_scale = fmaxf(c * sh.m1[t][fresh_tid() & (TILE - 1)], 0x1p-100f);
       }
 
       // Keys [lo, hi) that this thread's row sees; a row of no token is carried along unmasked and goes nowhere.

@@ -46,3 +46,14 @@ def test_scores_of_any_size(dev, D, shape, power, sign):
     for r in range(3):
         want = np.repeat(v[int(a.table[r, 0]), 0], 2, axis=0)
         assert np.array_equal(f64(out)[a.cu[r]:a.cu[r + 1]], np.broadcast_to(want, (a.new[r], 4, D)))
+
+
+@pytest.mark.parametrize("shape", [CHUNKS, FEW])
+@pytest.mark.parametrize("D", [128, 64, 80])
+def test_scores_below_all_numbers(dev, D, shape):
+    """Queries, key scales and a scale so small that their product is below fp32's smallest number: every seen key has the
+    same weight, and the masked ones none."""
+    a = Attention(*shape, 4, 2, D, 16, window=60, seed=91, scale=1e-30).poison()
+    a.q *= 2.0 ** -60
+    a.ks[torch.isfinite(a.ks)] = 2.0 ** -40
+    a.check(*a.run(dev, kda))
