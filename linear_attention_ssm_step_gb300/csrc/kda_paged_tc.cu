@@ -1403,8 +1403,9 @@ cudaError_t launch_paged_attention_tc(const kda_attention_params& p, const kda_p
   const bool wide = p.cache.head_dim == 128;
   if (scales != nullptr) {
     const int rows = paged_attention_few_rows(p);
-    if (rows > 0) return launch_paged_attention_fp8_rows(p, *scales, rows, workspace, ctas, s);
-    cudaError_t e = code_pages_tensor_map(p.cache.k, p.cache, a.box, &km);
+    cudaError_t e = rows > 0 ? launch_paged_attention_fp8_rows(p, *scales, rows, workspace, ctas, s) : cudaErrorNotSupported;
+    if (e != cudaErrorNotSupported) return e;  // else too many items of few rows for its line; of this kernel's there are fewer
+    e = code_pages_tensor_map(p.cache.k, p.cache, a.box, &km);
     if (e == cudaSuccess) e = code_pages_tensor_map(p.cache.v, p.cache, a.box, &vm);
     if (e != cudaSuccess) return e;
     return wide ? launch_tc<128, true>(km, vm, a, ctas, s) : launch_tc<64, true>(km, vm, a, ctas, s);

@@ -1,11 +1,12 @@
-"""Attention over a paged cache in 8 bits at the ends of what scores can be."""
+"""Attention over a paged cache in 8 bits at the ends of what scores can be, and of what tables can be."""
 
 import numpy as np
 import pytest
 import torch
 
 from linear_attention_ssm_step_gb300 import kda
-from paged_fp8_cases import Attention, f64
+from paged_cases import ints
+from paged_fp8_cases import Attention, cache, f64
 
 pytestmark = pytest.mark.gpu
 
@@ -57,3 +58,23 @@ def test_scores_below_all_numbers(dev, D, shape):
     a.q *= 2.0 ** -60
     a.ks[torch.isfinite(a.ks)] = 2.0 ** -40
     a.check(*a.run(dev, kda))
+
+
+def test_a_table_too_wide_for_the_kernel_of_few_rows(dev):
+    """One token of 512 heads over 128, and a table of 1.2 billion tokens: two items of few rows (a token each at most, of
+    9.6 million units) for 128 heads would pass 32 bits, one item of chunks does not. The call gives what the kernel for chunks does (which the second call takes, its rows padded to 40: one
+    unit of keys, so that no bit depends on how the work is shared out)."""
+    H, D, page, width, kv = 128, 64, 4096, 300000, 100
+    gen = torch.Generator().manual_seed(92)
+    sides = [x.to(dev) for x in (*cache(2, page, H, D, "thd", gen), *cache(2, page, H, D, "thd", gen))]
+    kc, ks, vc, vs = sides
+    q = torch.randn((40, 4 * H, D), generator=gen).to(torch.bfloat16).to(dev)
+    table = torch.full((1, width), -1, dtype=torch.int32, device=dev)
+    table[0, 0] = 1
+    got = []
+    for rows, columns in ((1, width), (40, 1)):
+        lse = torch.zeros((rows, 4 * H), dtype=torch.float32, device=dev)
+        out = kda.kda_paged_attention_fp8(q[:rows], kc, vc, ks, vs, table[:, :columns], ints([0, 1], dev), ints([kv], dev),
+                                          lse=lse)
+        got.append((out[0], lse[0]))
+    assert torch.equal(got[0][1], got[1][1]) and torch.equal(got[0][0], got[1][0])
