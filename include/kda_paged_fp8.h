@@ -11,7 +11,8 @@
  * of them shorter where that leaves a rest. The cache holds code * scale.
  * Scales are powers of two from 2^-40 to 2^40; the calls that read take any
  * positive number in that range (and give undefined numbers, but nothing
- * else, outside it).
+ * else, outside it), the append takes powers of two alone where it continues a
+ * block.
  *
  * The calls take the parameters of their 16-bit forms, with these differences:
  *   - kda_paged_cache.k and .v point to uint8 codes; their strides are in
@@ -65,8 +66,9 @@ typedef struct {
  * are not stored (a negative position, slot -1 or outside the cache) stand for
  * the tokens in between, whose codes are left as they are and count with the
  * new scale. Where rows of a block come in any other order, or a slot twice,
- * that block's codes and scales are undefined. At most 2^30 rows a call. k is turned with sines and cosines good to 2^-20, far below the
- * rounding of a code; q as in kda_rope_append.
+ * that block's codes and scales are undefined. At most 2^30 rows a call.
+ * k is turned with sines and cosines good to 2^-20, far below the rounding of a
+ * code; q as in kda_rope_append.
  */
 kda_status kda_rope_append_fp8(const kda_rope_params* p, const kda_paged_scales* s, void* stream);
 
@@ -91,9 +93,13 @@ kda_status kda_rope_append_fp8(const kda_rope_params* p, const kda_paged_scales*
  * on the tensor cores, any other cache on the CUDA cores. The workspace is
  * kda_paged_attention's, and the two calls may take turns with one.
  *
+ * lse is off by up to 2^-21 of the largest |log2| of a value scale beside what
+ * its terms' rounding in fp32 makes.
+ *
  * Calls with up to 32 rows (new tokens times query heads of a key-value head) a
- * request on average run in a kernel for few rows, others in one for chunks. A
- * step that mixes decode tokens and chunks is faster as two calls, one for each.
+ * request on average (num_tokens over num_requests, idle ones too) run in a
+ * kernel for few rows, others in one for chunks. A step that mixes decode tokens
+ * and chunks is faster as two calls, one for each.
  */
 kda_status kda_paged_attention_fp8(const kda_attention_params* p, const kda_paged_scales* s, void* workspace,
                                    size_t workspace_bytes, void* stream);

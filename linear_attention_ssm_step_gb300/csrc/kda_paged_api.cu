@@ -105,7 +105,7 @@ kda_status check_rows(const char* name, const void* p, int64_t n, int64_t b_stri
 kda_status check_pages(const char* name, const kda_pages& g, const kda_paged_cache& c, int elem) {
   if (c.num_pages == 0) return KDA_OK;
   if (g.ptr == nullptr) return fail(KDA_EINVAL, "%s.ptr is NULL with num_pages = %d", name, c.num_pages);
-  if (!aligned(g.ptr, elem)) return fail(KDA_EINVAL, "%s.ptr is not 2-byte aligned", name);
+  if (!aligned(g.ptr, elem)) return fail(KDA_EINVAL, "%s.ptr is not %d-byte aligned", name, elem);
   if (g.page_stride < 0 || g.token_stride < 0 || g.head_stride < 0)
     return fail(KDA_EINVAL, "%s has a negative stride", name);
   if (g.page_stride >> 31 || g.token_stride >> 31 || g.head_stride >> 31)

@@ -29,12 +29,12 @@ constexpr int SCALE_LOW = -40, SCALE_HIGH = 40;  // exponents of the scales
 // left out read the rows twice (asking for every row of a run whether it is stored
 // cost the chunk below 1.3 us more).
 //
-// Measured: 8192 rows of 32 + 8 + 8 heads of 128, 43 us, of which the queries 20
+// Measured: 8192 rows of 32 + 8 + 8 heads of 128, 44 us, of which the queries 20
 // and keys and values 23 to 30, bound by latency: 1400 instructions a task, issued
 // in a third of the cycles. A CTA per row with its share of the run's tasks (each
 // forming the run's sines and cosines again): 58 us; one with four warps a task
-// and the turn in registers, 52 to 69. 256 decode rows 7.3 us: a launch, the slots,
-// the rows and scales, the codes.
+// and the turn in registers, 52 to 69. 256 decode rows 6.4 to 8.9 us: a launch, the
+// slots, the rows and scales, the codes.
 
 // A run: rows t0 .. t0 + n - 1, at tokens first .. of a block; those that are stored as bits, of which the first and the last
 // are set.
@@ -362,11 +362,16 @@ __global__ void __launch_bounds__(APPEND_WARPS * 32, 2)
 
 cudaError_t launch_rope_append_fp8(const kda_rope_params& p, const kda_paged_scales& sc, bool q_wide, int lane_elems,
                                    cudaStream_t s) {
-  // Up to 512 rows are mostly decode steps, whose rows may each be a run: a CTA per row. More are chunks, or so many rows that
-  // it does not matter: a CTA looks for runs in up to 16 rows, 512 CTAs. Up to 2048 rows the queries are in the same launch
-  // (1037 rows: 10.3 us, 11.9 in two launches). With more they go ahead in a launch of kda_rope_append_kernel without keys and
-  // values, which needs half the registers and runs at twice the occupancy, and this kernel is brought in while it ends (8192
-  // rows: 43 us, 47 in one launch).
+  // Up to 512 rows are mostly decode steps, whose rows may each be a run: a CTA per row. More are chunks, mostly: a CTA looks
+  // for runs in up to 16 rows, 512 CTAs. What the rows are stands in device memory, so one rule has to do for both. This one,
+  // and the best of spans of 1 to 16 rows with and without `splits`, us, 32 + 8 + 8 heads of 128, on decode rows in blocks of
+  // their own and on one chunk: 300 rows 7.0 (5.8 without splits) and 9.9 (7.7); 600: 11.2 (9.5) and 12.0 (10.5); 1000: 17.9
+  // (14.9) and 13.7 (12.2); 2000: 38.0 (34.3) and 25.3 (22.1); 4000: 62.6 (58.3) and 36.5 (31.7); 8000: 112 (106) and 57.9
+  // (57.7).
+  // Up to 2048 rows the queries are in the same launch (1000 rows of the chunk 13.7, 18.3 in two launches). With more they go
+  // ahead in a launch of kda_rope_append_kernel without keys and values, which needs half the registers and runs at twice the
+  // occupancy, and this kernel is brought in while it ends (4000 rows of the chunk 36.5, 45.2 in one launch; 2000 rows take 25.3
+  // in one and 24.2 in two).
   const bool fused = p.num_tokens <= 2048;
   const int span = p.num_tokens <= 512 ? 1 : p.num_tokens < 16 * 512 ? (p.num_tokens + 511) / 512 : SCALE_TOKENS;
   const int blocks = p.num_tokens / span + (p.num_tokens % span != 0), tasks = 2 * p.cache.num_heads;

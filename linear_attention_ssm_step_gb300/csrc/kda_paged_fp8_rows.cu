@@ -5,7 +5,7 @@
 // of the products, the R rows of an item (query heads of a key-value head, times
 // new tokens) their columns, so that nothing is padded to 128 rows and the codes
 // of the cache enter both products as they lie in the pages:
-//   S^T = K Q^T       Q as two E4M3 numbers each (put_query), 2 R columns
+//   S^T = K Q^T       Q as two E4M3 numbers each (query_codes), 2 R columns
 //   P^T = exp2(y - m), y = scale log2e ks S + log2 vs: weights times value scales
 //   O^T += V^T P^T    P as three E5M2 numbers each, 3 R columns
 // A weight p <= 2^14, as fp16, is p1 + 2^-4 p2 + 2^-8 p3, exactly, subnormals
@@ -27,14 +27,14 @@
 // and parts are written as whole rows.
 //
 // What bounds it: memory, and what is not hidden behind it. 64 decode requests of
-// 2048..8192 tokens, 8 key-value heads: 113 to 115 us, 5.5 TB/s; a unit takes 1360
-// cycles at the copy's rate. In a build with clocks read on the way (126 us) a call
-// began with 7800 cycles until the first scores and ended with an item's parts,
-// 2300 to 2700 a trip to memory under load, hence eight parts a trip (four: 47 us against 43
-// for 4 requests of 16384..65536 tokens). With rows as the rows of the products (the
+// 2048..8192 tokens, 8 key-value heads: 107 to 113 us by the machine, 5.6 to 5.9
+// TB/s; a unit takes 1360 cycles at the copy's rate. In a build with clocks read on
+// the way (126 us) a call began with 7800 cycles until the first scores and ended
+// with an item's parts, 2300 to 2700 a trip to memory under load, hence eight parts
+// a trip (four: 47 us against 43 for 4 requests of 16384..65536 tokens). With rows as the rows of the products (the
 // kernel for chunks) the same 64 requests took 220 us, bound by the padding to 128
-// rows and by the conversion of the values. 32 verify requests of 24 rows: 48 us,
-// 17 of memory.
+// rows and by the conversion of the values. 32 verify requests of 24 rows: 48 to
+// 49 us, 17 of memory (48.0 with E4M3 parts of the weights).
 // Scales: with one pair of units on its way a step waited for them under load
 // (600 cycles a unit in the slowest CTAs); with two it does not.
 #include <math.h>

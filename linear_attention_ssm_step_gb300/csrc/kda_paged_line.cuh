@@ -44,8 +44,8 @@ __device__ __forceinline__ Span item_span(int pos, int n, int i, int w, int wind
   return s;
 }
 
-// Length on the line of one key-value head of a request: n tokens, w an item, which takes LEAD beside its units. Called by whole warps, one request a lane; a request
-// of many items (a long chunk) is summed by the warp together.
+// Length on the line of one key-value head of a request: n tokens, w an item, which takes LEAD beside its units. Called by
+// whole warps, one request a lane; a request of many items (a long chunk) is summed by the warp together.
 template <int LEAD>
 __device__ __forceinline__ int head_units(int pos, int n, int w, int window) {
   const int items = (n + w - 1) / w;
@@ -144,8 +144,10 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// 1 / x and ln x to 2^-22 or better, for sums of weights (from 2^-8 on): bf16 outputs and a log of fp32 terms need no more,
-// and the exact forms are long code for once a run.
+// 1 / x and ln x to 2^-22 of themselves or better, for sums of weights: bf16 outputs and a log of fp32 terms need no more, and
+// the exact forms are long code for once a run. Sums are from 2^-8 on, those of a cache in 8 bits, where weights hold value
+// scales and sums do not, from 2^-34 to 2^70 and more: there a reference and the logarithm of its sum may be far larger than
+// their sum, lse, which is then off by 2^-21 of the larger (1e-5 where the value scales are 2^-40).
 __device__ __forceinline__ float rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -59,8 +59,8 @@
 // that the sum l takes them times 1 / vs. fp16 weights of up to 2^14 (a reference
 // set at 2^6, and 8 of growth) hold 11 bits down to 2^-14, so that keys of 2^-20
 // of the largest weight still count.
-// Two chunks of 2048 tokens over 4096..16384 cached, 32 query heads: 755 to 758 us,
-// 1.33 PFLOP/s. What that costs beside the 16-bit cache's chain was measured on an
+// Two chunks of 2048 tokens over 4096..16384 cached, 32 query heads: 735 to 741 us,
+// 1.37 PFLOP/s. What that costs beside the 16-bit cache's chain was measured on an
 // earlier build of 767 to 772 us: 733 with the conversion of the values left out,
 // 758 with one factor for all keys in place of the block scales, 698 with neither.
 // Another build spent 13700 cycles a run until its queries were codes (the 16-bit
@@ -1035,36 +1035,36 @@ __global__ void __launch_bounds__(Shape<D, FP8>::THREADS, 1)
             unpair(sum, l0, l1);
             l += l0 + l1;
           } else {
-          const uint64_t c2 = pair(c, c);
-          uint64_t sum[4] = {0, 0, 0, 0}, base2 = reference(m, c);
-          float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            const uint64_t c2 = pair(c, c);
+            uint64_t sum[4] = {0, 0, 0, 0}, base2 = reference(m, c);
+            float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int i = 0; i < UNIT; i += 8)
+            for (int i = 0; i < UNIT; i += 8)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              tops[j] = max3(tops[j], __uint_as_float(s[i + 2 * j]), __uint_as_float(s[i + 2 * j + 1]));
-          const float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]);
-          const bool grown = valid && top > m && (top - m) * c > SLACK;  // m = -inf: any key
-          if (__builtin_expect(__any_sync(0xffffffffu, grown), 0)) {
-            const float fade = grown ? ex2((m - top) * c) : 1.f;
-            if (grown) m = top;
-            l *= fade;
-            if (units > 0) fade_o(fade);  // the product of the unit before is done: these scores waited for it
-            base2 = reference(m, c);
-          }
-          weights<32>(s, c2, base2, sum, wa);
-          st16(s_addr, wa);
-          weights<32>(s + 32, c2, base2, sum, wa);
-          st16(s_addr + 16, wa);
-          weights<32>(s + 64, c2, base2, sum, wa);
-          st16(s_addr + 32, wa);
-          give(0);
-          weights<32>(s + FIRST, c2, base2, sum, wa);
-          st16(s_addr + FIRST / 2, wa);
-          give(1);
-          float l0, l1;
-          unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), l0, l1);
-          l += l0 + l1;
+              for (int j = 0; j < 4; ++j)
+                tops[j] = max3(tops[j], __uint_as_float(s[i + 2 * j]), __uint_as_float(s[i + 2 * j + 1]));
+            const float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]);
+            const bool grown = valid && top > m && (top - m) * c > SLACK;  // m = -inf: any key
+            if (__builtin_expect(__any_sync(0xffffffffu, grown), 0)) {
+              const float fade = grown ? ex2((m - top) * c) : 1.f;
+              if (grown) m = top;
+              l *= fade;
+              if (units > 0) fade_o(fade);  // the product of the unit before is done: these scores waited for it
+              base2 = reference(m, c);
+            }
+            weights<32>(s, c2, base2, sum, wa);
+            st16(s_addr, wa);
+            weights<32>(s + 32, c2, base2, sum, wa);
+            st16(s_addr + 16, wa);
+            weights<32>(s + 64, c2, base2, sum, wa);
+            st16(s_addr + 32, wa);
+            give(0);
+            weights<32>(s + FIRST, c2, base2, sum, wa);
+            st16(s_addr + FIRST / 2, wa);
+            give(1);
+            float l0, l1;
+            unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), l0, l1);
+            l += l0 + l1;
           }
         } else if (lane == 0) {
           mbar_arrive(&sh.p_full[t][0]);
